@@ -16,7 +16,8 @@ import torch
 
 __all__ = ["NF4Error", "NF4Weight", "nf4_dequant", "nf4_gemv", "nf4_gemv_ex", "DecodeStep", "nf4_quantize",
            "nf4_quantize_workspace_size", "nf4_quantize_noalloc", "nf4_version", "nf4_status_string",
-           "nf4_device_error_flags", "LIB_PATH"]
+           "nf4_device_error_flags", "LIB_PATH", "nf4_rope_table", "nf4_qk_norm_rope", "nf4_kv_append",
+           "nf4_prefix_attention", "nf4_prefix_attention_workspace_size"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnf4.so")
 
@@ -91,7 +92,8 @@ def nf4_status_string(status: int) -> str:
 
 
 def nf4_device_error_flags() -> int:
-    """Read and clear the device-side error flags (bit 0: a bounded wait ran out)."""
+    """Read and clear the device-side error flags (bit 0: a bounded wait ran out; bit 1: an index
+    that the attention side read on the device was out of range)."""
     f = ctypes.c_uint(0)
     _check(_lib.nf4_device_error_flags(ctypes.byref(f)), "nf4_device_error_flags")
     return int(f.value)
@@ -339,3 +341,7 @@ def gemv(wt: NF4Weight, x: torch.Tensor, y=None, stream=None, bias=None, out_dty
     return nf4_gemv_ex(wt.packed, wt.absmax_q, wt.absmax2, wt.code2, wt.offset, N, K, x, bias=bias,
                        y=y, out_dtype=out_dtype or torch.float32, blocksize=wt.blocksize,
                        s2_blocksize=wt.s2_blocksize, stream=stream)
+
+
+from .attention import (nf4_kv_append, nf4_prefix_attention,  # noqa: E402
+                        nf4_prefix_attention_workspace_size, nf4_qk_norm_rope, nf4_rope_table)

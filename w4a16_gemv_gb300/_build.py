@@ -13,7 +13,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnf4.so")
 SOURCES = ("nf4_api.cu", "nf4_dequant.cu", "nf4_gemv.cu", "nf4_gemv_b1.cu", "nf4_gemv_stream.cu",
-           "nf4_quantize.cu", "nf4_step.cu", "nf4_gemm_tc.cu")
+           "nf4_quantize.cu", "nf4_step.cu", "nf4_gemm_tc.cu", "nf4_attn_api.cu", "nf4_rope.cu",
+           "nf4_prefix_attn.cu")
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 
@@ -35,8 +36,8 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "nf4.h"),
-                                                                  os.path.abspath(__file__)]
+    deps = ([os.path.join(CSRC, f) for f in os.listdir(CSRC)] +
+            [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [os.path.abspath(__file__)])
     return any(os.path.getmtime(d) > t for d in deps)
 
 

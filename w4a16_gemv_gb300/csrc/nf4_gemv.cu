@@ -23,6 +23,7 @@
 //     registers; each x chunk is reused for R rows.
 //   * For thin layers several warps split K (ks > 1) and combine through
 //     shared memory, so that small N still spreads over all SMs.
+#include "nf4_attn.cuh"
 #include "nf4_internal.cuh"
 
 namespace nf4 {
@@ -375,8 +376,14 @@ cudaError_t dispatch_batch(const QuantTensor& t, int64_t N, int64_t K, const uin
 }  // namespace
 
 cudaError_t read_and_clear_device_flags(unsigned int* flags) {
-  // the tensor-core GEMV is the only kernel with waits that can run out
-  return read_and_clear_tc_flags(flags);
+  // one word per translation unit that reports something: the tensor-core
+  // GEMV (waits) and the attention side (indices read on the device)
+  unsigned int part[3] = {0u, 0u, 0u};
+  cudaError_t e = read_and_clear_tc_flags(&part[0]);
+  if (e == cudaSuccess) e = read_and_clear_rope_flags(&part[1]);
+  if (e == cudaSuccess) e = read_and_clear_prefix_flags(&part[2]);
+  if (e == cudaSuccess) *flags = part[0] | part[1] | part[2];
+  return e;
 }
 
 cudaError_t launch_gemv(const QuantTensor& t, int64_t N, int64_t K, const uint16_t* x, int batch,

@@ -1,0 +1,525 @@
+// nf4_prefix_attn.cu -- attention of a batch over a paged cache whose first
+// keys are shared by every sequence.
+//
+// out = sum_j exp(s_j - lse) v_j over the shared keys and then the sequence's
+// own ones. A softmax over a union of key ranges joins from the ranges'
+// (maximum m_x, sum l_x, unscaled output o_x): with m = max m_x,
+// out = sum_x e^(m_x - m) o_x / sum_x e^(m_x - m) l_x. So the shared keys are
+// treated once for all rows of a key/value head together (every query token
+// of the batch times its group of query heads: a matrix product instead of
+// one matrix-vector product per sequence), each sequence's own keys apart,
+// both cut into ranges of keys so that a few rows over a long axis still fill
+// the SMs, and a last kernel joins the ranges in order.
+#include "nf4_prefix_attn.cuh"
+
+namespace nf4 {
+namespace {
+
+__device__ unsigned int g_prefix_flags = 0;
+
+constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kKeys = 64;    // keys per stage
+constexpr int kStages = 3;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <typename H>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (H::kDtype == NF4_BF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Where a finished row goes: the partial results, or, when the row has one
+// range of keys only, the output itself.
+struct RowOut {
+  float* part;
+  float2* ml;
+  char* out;
+  float* lse;
+};
+__device__ __forceinline__ RowOut row_out(const PrefixArgs& a, const PrefixItem& it, int r) {
+  const int t = it.t0 + r / a.group;
+  const int h = it.head * a.group + r % a.group;
+  const int64_t row = int64_t(t) * a.q_heads + h;
+  RowOut o;
+  o.part = a.part + (int64_t(it.split) * a.tokens * a.q_heads + row) * a.dim;
+  o.ml = a.ml + row * a.splits + it.split;
+  o.out = a.out + int64_t(t) * a.out_ts + int64_t(h) * a.out_hs;
+  o.lse = a.lse ? a.lse + row : nullptr;
+  return o;
+}
+
+// One item with tiles of R rows. R = 64: a warp has 16 rows and all keys of a
+// stage; R = 16: the warps share the rows and a stage's keys are split among
+// them, joined through shared memory at the end.
+template <typename H, int DP, int R>
+__device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it, unsigned char* smem) {
+  constexpr int KW = R == 64 ? kKeys : kKeys / kWarps;  // keys of a stage per warp
+  constexpr int NB = KW / 8;                            // score blocks of 8 keys
+  constexpr int CPR = DP / 8;                           // 16-byte chunks per row
+  constexpr int RPI = 32 / CPR;                         // rows per copy instruction of a warp
+  constexpr uint32_t kTile = kKeys * DP * 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sbase = smem_u32(smem);
+  const int chunks = a.dim / 8;
+  const int ntiles = (it.k1 - it.k0 + kKeys - 1) / kKeys;
+
+  // copies of tile i: warp w brings rows 16 w .. 16 w + 15; lane l holds the
+  // offsets of row 16 w + (l & 15), looked up one tile ahead
+  int page = 0;
+  auto fetch_page = [&](int i) {
+    const int j = it.k0 + i * kKeys + warp * 16 + (lane & 15);
+    if (j < it.k1) page = key_page(a, it, j);
+  };
+  auto copy_tile = [&](int i) {
+    const int j = it.k0 + i * kKeys + warp * 16 + (lane & 15);
+    KeyOffset off{0, 0};
+    const bool real = j < it.k1 && key_offset(a, it, j, page, &g_prefix_flags, &off);
+    const uint32_t ks = sbase + uint32_t(i % kStages) * (2 * kTile);
+    const int c = lane % CPR;
+#pragma unroll
+    for (int x = 0; x < 16 / RPI; ++x) {
+      const int rl = x * RPI + lane / CPR;  // row within the warp's 16
+      const int64_t ko = __shfl_sync(0xffffffffu, off.k, rl);
+      const int64_t vo = __shfl_sync(0xffffffffu, off.v, rl);
+      const bool there = __shfl_sync(0xffffffffu, int(real), rl) && c < chunks;
+      const int row = warp * 16 + rl;
+      const uint32_t dst = ks + uint32_t(row) * (DP * 2) + uint32_t((c ^ (row & 7)) << 4);
+      // what is not there is filled with zeros, from no address of the cache
+      cp_async16(dst, there ? a.k + ko + c * 16 : a.q, there);
+      cp_async16(dst + kTile, there ? a.v + vo + c * 16 : a.q, there);
+    }
+  };
+
+  // the item's rows of Q as A fragments
+  const int rbase = R == 64 ? warp * 16 : 0;
+  const int ra = rbase + (lane >> 2), rb = ra + 8;  // this thread's two rows of the tile
+  uint32_t qf[DP / 16][4];
+  {
+    const char* qp[2];
+    bool there[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int rl = x ? rb : ra;
+      there[x] = rl < it.rows;
+      const int r = it.r0 + (there[x] ? rl : 0);
+      qp[x] = a.q + int64_t(it.t0 + r / a.group) * a.q_ts + int64_t(it.head * a.group + r % a.group) * a.q_hs;
+    }
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int d = s * 16 + (x >> 1) * 8 + (lane & 3) * 2;
+        qf[s][x] = there[x & 1] && d < a.dim ? __ldg(reinterpret_cast<const uint32_t*>(qp[x & 1] + d * 2)) : 0u;
+      }
+  }
+  // keys (within the segment) that the two rows see
+  const int lima = ra < it.rows ? min(visible_keys(it, (it.r0 + ra) / a.group), it.k1) : 0;
+  const int limb = rb < it.rows ? min(visible_keys(it, (it.r0 + rb) / a.group), it.k1) : 0;
+  // up to here no row of the tile is masked
+  const int free_to = min(visible_keys(it, it.r0 / a.group), it.k1);
+
+  float o[DP / 8][4];
+#pragma unroll
+  for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[i][x] = 0.0f;
+  float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;
+
+  fetch_page(0);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (i < ntiles) {
+      copy_tile(i);
+      fetch_page(i + 1);
+    }
+    cp_async_commit();
+  }
+  for (int i = 0; i < ntiles; ++i) {
+    cp_async_wait<kStages - 2>();
+    __syncthreads();  // tile i landed for every warp; everyone is done with tile i - 1's stage
+    if (i + kStages - 1 < ntiles) {
+      copy_tile(i + kStages - 1);
+      fetch_page(i + kStages);
+    }
+    cp_async_commit();
+    const uint32_t ks = sbase + uint32_t(i % kStages) * (2 * kTile);
+    const uint32_t vs = ks + kTile;
+    const int kw = R == 64 ? 0 : warp * KW;  // first key of the stage for this warp
+
+    float s[NB][4];
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[n][x] = 0.0f;
+#pragma unroll
+    for (int st = 0; st < DP / 16; ++st)
+#pragma unroll
+      for (int n = 0; n < NB / 2; ++n) {
+        const int key = kw + n * 16 + (lane & 7) + ((lane >> 4) << 3);
+        const int c = st * 2 + ((lane >> 3) & 1);
+        uint32_t b[4];
+        ldsm4(ks + uint32_t(key) * (DP * 2) + uint32_t((c ^ (key & 7)) << 4), b);
+        mma16816<H>(s[2 * n], qf[st], b[0], b[1]);
+        mma16816<H>(s[2 * n + 1], qf[st], b[2], b[3]);
+      }
+
+    const int j0 = it.k0 + i * kKeys + kw + (lane & 3) * 2;
+    if (it.k0 + (i + 1) * kKeys > free_to) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (j0 + n * 8 + (x & 1) >= (x < 2 ? lima : limb)) s[n][x] = -INFINITY;
+    }
+    float xa = -INFINITY, xb = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      xa = fmaxf(xa, fmaxf(s[n][0], s[n][1]));
+      xb = fmaxf(xb, fmaxf(s[n][2], s[n][3]));
+    }
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+      xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, d));
+      xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, d));
+    }
+    const float na = fmaxf(ma, xa * a.scale_log2), nb = fmaxf(mb, xb * a.scale_log2);
+    const float ba = na == -INFINITY ? 0.0f : na, bb = nb == -INFINITY ? 0.0f : nb;
+    const float fa = ex2(ma - ba), fb = ex2(mb - bb);
+    ma = na;
+    mb = nb;
+    la *= fa;
+    lb *= fb;
+    uint32_t pf[NB][2];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const float p0 = ex2(fmaf(s[n][0], a.scale_log2, -ba)), p1 = ex2(fmaf(s[n][1], a.scale_log2, -ba));
+      const float p2 = ex2(fmaf(s[n][2], a.scale_log2, -bb)), p3 = ex2(fmaf(s[n][3], a.scale_log2, -bb));
+      la += p0 + p1;
+      lb += p2 + p3;
+      pf[n][0] = H::down2(p0, p1);
+      pf[n][1] = H::down2(p2, p3);
+    }
+#pragma unroll
+    for (int d = 0; d < DP / 8; ++d) {
+      o[d][0] *= fa;
+      o[d][1] *= fa;
+      o[d][2] *= fb;
+      o[d][3] *= fb;
+    }
+#pragma unroll
+    for (int n = 0; n < NB / 2; ++n) {
+      const uint32_t pa[4] = {pf[2 * n][0], pf[2 * n][1], pf[2 * n + 1][0], pf[2 * n + 1][1]};
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d) {
+        const int key = kw + n * 16 + (lane & 7) + (((lane >> 3) & 1) << 3);
+        const int c = d * 2 + (lane >> 4);
+        uint32_t b[4];
+        ldsm4t(vs + uint32_t(key) * (DP * 2) + uint32_t((c ^ (key & 7)) << 4), b);
+        mma16816<H>(o[2 * d], pa, b[0], b[1]);
+        mma16816<H>(o[2 * d + 1], pa, b[2], b[3]);
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+    la += __shfl_xor_sync(0xffffffffu, la, d);
+    lb += __shfl_xor_sync(0xffffffffu, lb, d);
+  }
+  cp_async_wait<0>();
+
+  if constexpr (R != 64) {
+    // join the four warps' key shares: maxima and sums first, then the
+    // outputs scaled to the common maximum, added in warp order
+    __syncthreads();  // the stages are free
+    float2* sml = reinterpret_cast<float2*>(smem);             // [warp][16]
+    float* so = reinterpret_cast<float*>(smem + 512);          // [warp][16][DP + 4]
+    constexpr int kPitch = DP + 4;
+    if ((lane & 3) == 0) {
+      sml[warp * 16 + ra] = make_float2(ma, la);
+      sml[warp * 16 + rb] = make_float2(mb, lb);
+    }
+    __syncthreads();
+    float ta = -INFINITY, tb = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      ta = fmaxf(ta, sml[w * 16 + ra].x);
+      tb = fmaxf(tb, sml[w * 16 + rb].x);
+    }
+    const float fa = ma == -INFINITY ? 0.0f : ex2(ma - ta), fb = mb == -INFINITY ? 0.0f : ex2(mb - tb);
+#pragma unroll
+    for (int d = 0; d < DP / 8; ++d) {
+      const int col = d * 8 + (lane & 3) * 2;
+      *reinterpret_cast<float2*>(so + (warp * 16 + ra) * kPitch + col) = make_float2(o[d][0] * fa, o[d][1] * fa);
+      *reinterpret_cast<float2*>(so + (warp * 16 + rb) * kPitch + col) = make_float2(o[d][2] * fb, o[d][3] * fb);
+    }
+    __syncthreads();
+    // four lanes of a chunk of 4 elements each: thread -> (row, 4 columns)
+    for (int e = threadIdx.x; e < 16 * (DP / 4); e += kThreads) {
+      const int r = e / (DP / 4), col = (e % (DP / 4)) * 4;
+      if (r >= it.rows || col >= a.dim) continue;
+      float m = -INFINITY, l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sml[w * 16 + r].x);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 x = sml[w * 16 + r];
+        l += x.x == -INFINITY ? x.y : x.y * ex2(x.x - m);  // x.y is 0, or NaN
+        const float4 y = *reinterpret_cast<const float4*>(so + (w * 16 + r) * kPitch + col);
+        v.x += y.x;
+        v.y += y.y;
+        v.z += y.z;
+        v.w += y.w;
+      }
+      const RowOut ro = row_out(a, it, it.r0 + r);
+      if (!a.direct) {
+        *reinterpret_cast<float4*>(ro.part + col) = v;
+        if (col == 0) *ro.ml = make_float2(m, l);
+      } else {
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        *reinterpret_cast<uint2*>(ro.out + col * 2) =
+            make_uint2(H::down2(v.x * inv, v.y * inv), H::down2(v.z * inv, v.w * inv));
+        if (col == 0 && ro.lse) *ro.lse = l > 0.0f || l != l ? fmaf(m, kLn2, logf(l)) : -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = x ? rb : ra;
+      if (r >= it.rows) continue;
+      const float m = x ? mb : ma, l = x ? lb : la;
+      const RowOut ro = row_out(a, it, it.r0 + r);
+      if (!a.direct) {
+#pragma unroll
+        for (int d = 0; d < DP / 8; ++d) {
+          const int col = d * 8 + (lane & 3) * 2;
+          if (col < a.dim) *reinterpret_cast<float2*>(ro.part + col) = make_float2(o[d][2 * x], o[d][2 * x + 1]);
+        }
+        if ((lane & 3) == 0) *ro.ml = make_float2(m, l);
+      } else {
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+#pragma unroll
+        for (int d = 0; d < DP / 8; ++d) {
+          const int col = d * 8 + (lane & 3) * 2;
+          if (col < a.dim)
+            *reinterpret_cast<uint32_t*>(ro.out + col * 2) = H::down2(o[d][2 * x] * inv, o[d][2 * x + 1] * inv);
+        }
+        if ((lane & 3) == 0 && ro.lse) *ro.lse = l > 0.0f || l != l ? fmaf(m, kLn2, logf(l)) : -INFINITY;
+      }
+    }
+  }
+}
+
+template <typename H, int DP>
+__global__ void __launch_bounds__(kThreads) prefix_mma_kernel(const __grid_constant__ PrefixArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  pdl_allow_dependents();
+  pdl_wait_prior_grid();
+  const PrefixItem it = prefix_item(a, blockIdx.x, &g_prefix_flags);
+  if (it.rows <= 0) return;
+  if (it.own ? a.suffix_rows == 64 : a.prefix_rows == 64)
+    attend<H, DP, 64>(a, it, smem);
+  else
+    attend<H, DP, 16>(a, it, smem);
+}
+
+// Joins a row's partial results: one warp per row, four elements per lane.
+template <typename H>
+__global__ void __launch_bounds__(128) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
+  pdl_allow_dependents();
+  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = int64_t(a.tokens) * a.q_heads;
+  pdl_wait_prior_grid();
+  if (row >= rows) return;
+  const int t = int(row / a.q_heads);
+  int n = a.splits;
+  if (a.cu_q && a.suffix_splits > 0 && (t < a.cu_q[0] || t >= a.cu_q[a.batch])) n = a.prefix_splits;
+  const float2* ml = a.ml + row * a.splits;
+  float m = -INFINITY;
+  for (int s = lane; s < n; s += 32) m = fmaxf(m, ml[s].x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const bool mine = lane * 4 < a.dim;
+  const float* src = a.part + row * a.dim + lane * 4;
+  float l = 0.0f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < n; ++s) {
+    const float2 x = ml[s];
+    if (x.x == -INFINITY && x.y == 0.0f) continue;  // a range that the row does not see
+    const float f = x.x == -INFINITY ? 1.0f : ex2(x.x - m);
+    l = fmaf(x.y, f, l);
+    if (mine) {
+      const float4 y = *reinterpret_cast<const float4*>(src + int64_t(s) * rows * a.dim);
+      v.x = fmaf(y.x, f, v.x);
+      v.y = fmaf(y.y, f, v.y);
+      v.z = fmaf(y.z, f, v.z);
+      v.w = fmaf(y.w, f, v.w);
+    }
+  }
+  const bool any = l > 0.0f || l != l;
+  const float inv = any ? 1.0f / l : 0.0f;
+  if (mine) {
+    char* out = a.out + int64_t(t) * a.out_ts + int64_t(row - int64_t(t) * a.q_heads) * a.out_hs;
+    *reinterpret_cast<uint2*>(out + lane * 8) =
+        make_uint2(H::down2(v.x * inv, v.y * inv), H::down2(v.z * inv, v.w * inv));
+  }
+  if (lane == 0 && a.lse) a.lse[row] = any ? fmaf(m, kLn2, logf(l)) : -INFINITY;
+}
+
+// A call without a single key.
+template <typename H>
+__global__ void __launch_bounds__(128) prefix_empty_kernel(const __grid_constant__ PrefixArgs a) {
+  pdl_allow_dependents();
+  pdl_wait_prior_grid();
+  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= int64_t(a.tokens) * a.q_heads) return;
+  const int64_t t = row / a.q_heads;
+  char* out = a.out + t * a.out_ts + (row - t * a.q_heads) * a.out_hs;
+  if (lane * 4 < a.dim) *reinterpret_cast<uint2*>(out + lane * 8) = make_uint2(0u, 0u);
+  if (lane == 0 && a.lse) a.lse[row] = -INFINITY;
+}
+
+template <typename H, int DP>
+cudaError_t launch_mma(const PrefixArgs& p, unsigned items, cudaStream_t stream) {
+  auto kern = prefix_mma_kernel<H, DP>;
+  constexpr int smem = kStages * 2 * kKeys * DP * 2;
+  static PerDeviceCache attr_set;
+  const cudaError_t e = set_max_dynamic_smem_once(kern, smem, attr_set);
+  if (e != cudaSuccess) return e;
+  return launch_k(kern, dim3(items), dim3(kThreads), smem, stream, p);
+}
+
+template <typename H>
+cudaError_t launch_typed(const PrefixArgs& p, cudaStream_t stream) {
+  const int64_t rows = int64_t(p.tokens) * p.q_heads;
+  const unsigned row_blocks = unsigned((rows + 3) / 4);
+  if (p.splits == 0) return launch_k(prefix_empty_kernel<H>, dim3(row_blocks), dim3(128), 0, stream, p);
+  const int64_t items = (int64_t(p.prefix_tiles) * p.prefix_splits + int64_t(p.suffix_tiles) * p.suffix_splits) *
+                        p.k_heads;
+  if (items > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = p.dim <= 64 ? launch_mma<H, 64>(p, unsigned(items), stream)
+                                    : launch_mma<H, 128>(p, unsigned(items), stream);
+  if (e != cudaSuccess || p.direct) return e;
+  return launch_k(prefix_join_kernel<H>, dim3(row_blocks), dim3(128), 0, stream, p);
+}
+
+}  // namespace
+
+// Rows per tile, and the ranges of keys. Everything follows from the sizes
+// that the host knows (never from lengths on the device).
+void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, size_t* bytes) {
+  p->batch = int(a.batch);
+  p->tokens = int(a.tokens);
+  p->q_heads = int(a.q_heads);
+  p->k_heads = int(a.k_heads);
+  p->group = int(a.q_heads / a.k_heads);
+  p->dim = int(a.head_dim);
+  p->prefix_len = int(a.prefix_len);
+  p->suffix_max = a.batch > 0 ? int(a.suffix_pages_width * a.page_size) : 0;
+  const int64_t rows = a.tokens * p->group;  // of a key/value head
+  p->prefix_rows = rows > 32 ? 64 : 16;
+  p->suffix_rows = rows > 32 * a.batch ? 64 : 16;
+  p->prefix_tiles = int((rows + p->prefix_rows - 1) / p->prefix_rows);
+  // sum over sequences of ceil(rows / suffix_rows) is below both bounds
+  const int64_t whole = rows / p->suffix_rows + a.batch;
+  p->suffix_tiles = int(whole < rows ? whole : rows);
+  const int64_t pk = (int64_t(p->prefix_len) + kKeys - 1) / kKeys, sk = (int64_t(p->suffix_max) + kKeys - 1) / kKeys;
+  const int64_t total = (p->prefix_tiles * pk + p->suffix_tiles * sk) * p->k_heads;
+  // ranges of at least two stages, about eight items per SM, at most 64 ranges of each kind
+  int64_t per = total / (152 * 8);
+  per = per < 2 ? 2 : per;
+  const int64_t longest = pk > sk ? pk : sk;
+  if (longest > per * 64) per = (longest + 63) / 64;
+  p->chunk = int(per * kKeys > 0x40000000ll ? 0x40000000ll : per * kKeys);
+  p->prefix_splits = int((pk + per - 1) / per);
+  p->suffix_splits = int((sk + per - 1) / per);
+  if (rows == 0) p->prefix_splits = p->suffix_splits = 0;
+  p->splits = p->prefix_splits + p->suffix_splits;
+  const int64_t all = a.tokens * a.q_heads;
+  p->direct = p->prefix_splits == 1 && p->suffix_splits == 0;
+  *bytes = p->splits > 0 && !p->direct ? size_t(all) * size_t(p->splits) * (size_t(a.head_dim) * 4 + 8) : 0;
+}
+
+size_t prefix_attention_workspace_bytes(const nf4_prefix_attention_args& a) {
+  PrefixArgs p = {};
+  size_t bytes = 0;
+  plan_prefix_attention(a, &p, &bytes);
+  return bytes;
+}
+
+cudaError_t launch_prefix_attention(const nf4_prefix_attention_args& a, void* workspace, cudaStream_t stream) {
+  PrefixArgs p = {};
+  size_t bytes = 0;
+  plan_prefix_attention(a, &p, &bytes);
+  p.q = static_cast<const char*>(a.q);
+  p.out = static_cast<char*>(a.out);
+  p.k = static_cast<const char*>(a.k_cache);
+  p.v = static_cast<const char*>(a.v_cache);
+  p.q_ts = a.q_token_stride * 2;
+  p.q_hs = a.q_head_stride * 2;
+  p.out_ts = a.out_token_stride * 2;
+  p.out_hs = a.out_head_stride * 2;
+  p.k_ps = a.k_page_stride * 2;
+  p.k_ss = a.k_slot_stride * 2;
+  p.k_hs = a.k_head_stride * 2;
+  p.v_ps = a.v_page_stride * 2;
+  p.v_ss = a.v_slot_stride * 2;
+  p.v_hs = a.v_head_stride * 2;
+  p.lse = a.lse;
+  p.prefix_pages = a.prefix_pages;
+  p.suffix_pages = a.suffix_pages;
+  p.suffix_lens = a.suffix_lens;
+  p.cu_q = a.cu_q;
+  p.suffix_pages_stride = a.suffix_pages_stride;
+  p.page_size = int(a.page_size);
+  p.page_shift = -1;
+  for (int s = 0; s <= 16; ++s)
+    if (p.page_size == 1 << s) p.page_shift = s;
+  p.num_pages = int(a.num_pages);
+  p.scale_log2 = float(a.scale * 1.4426950408889634);
+  if (bytes > 0) {
+    p.part = static_cast<float*>(workspace);
+    p.ml = reinterpret_cast<float2*>(p.part + int64_t(p.splits) * a.tokens * a.q_heads * a.head_dim);
+  }
+  return a.dtype == NF4_BF16 ? launch_typed<Bf16>(p, stream) : launch_typed<Fp16>(p, stream);
+}
+
+cudaError_t read_and_clear_prefix_flags(unsigned int* flags) {
+  const unsigned int zero = 0;
+  const cudaError_t e = cudaMemcpyFromSymbol(flags, g_prefix_flags, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_prefix_flags, &zero, sizeof(unsigned int));
+}
+
+}  // namespace nf4

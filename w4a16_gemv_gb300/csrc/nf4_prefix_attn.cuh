@@ -1,0 +1,168 @@
+// nf4_prefix_attn.cuh -- what the kernels of nf4_prefix_attention share: the
+// arguments and the plan, the work items, and the paged rows of a cache.
+#pragma once
+
+#include "nf4_attn.cuh"
+
+namespace nf4 {
+
+// One call. A "row" of a key/value head is a (token, query head of its group)
+// pair: row r of a segment of tokens is token r / group, query head
+// k_head * group + r % group. A work item is a tile of rows against a range of
+// keys; it leaves an unscaled partial output (binary32), the running maximum
+// (of scores times log2 e) and the running sum, and a last kernel joins them.
+struct PrefixArgs {
+  const char* q;
+  char* out;
+  const char* k;
+  const char* v;
+  int64_t q_ts, q_hs, out_ts, out_hs;              // bytes
+  int64_t k_ps, k_ss, k_hs, v_ps, v_ss, v_hs;      // bytes
+  float* lse;
+  const int32_t* prefix_pages;
+  const int32_t* suffix_pages;
+  const int32_t* suffix_lens;
+  const int32_t* cu_q;
+  int64_t suffix_pages_stride;
+  int suffix_max;                                  // keys that the page table of a sequence can hold
+  int prefix_len;
+  int batch, tokens, q_heads, k_heads, group, dim;
+  int page_size, page_shift, num_pages;            // page_shift: log2 of page_size, or -1
+  float scale_log2;                                // scale * log2(e)
+  // plan
+  int prefix_rows, suffix_rows;                    // rows per tile
+  int prefix_tiles, suffix_tiles;                  // tiles of a key/value head (suffix: an upper bound)
+  int prefix_splits, suffix_splits, chunk;         // ranges of `chunk` keys each
+  int splits;                                      // prefix_splits + suffix_splits
+  int direct;                                      // 1: one range of shared keys is all; its items write the output
+  float* part;                                     // [splits][tokens * q_heads][dim]
+  float2* ml;                                      // [tokens * q_heads][splits]: (maximum, sum)
+};
+
+// The sizes and the plan of a call, and the bytes of its workspace.
+void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, size_t* bytes);
+
+// One work item, the same in every thread.
+struct PrefixItem {
+  const int32_t* pages;
+  int head;        // key/value head
+  int split;       // its place among a row's partial results
+  int t0;          // first token of the segment
+  int n;           // tokens of the segment
+  int r0;          // first row of the tile, within the segment
+  int rows;        // rows of the tile (0: nothing to do)
+  int k0, k1;      // keys of the item, within the segment's keys (k0 >= k1: none)
+  int len;         // keys of the segment
+  bool own;        // the sequence's own keys: token i sees the first len - n + i + 1
+};
+
+// Keys of the segment that token i (of n) sees.
+__device__ __forceinline__ int visible_keys(const PrefixItem& it, int i) {
+  return it.own ? min(max(it.len - it.n + i + 1, 0), it.len) : it.len;
+}
+
+// Item `index` of a launch that covers prefix items first (a key/value head's
+// tiles of one key range side by side, so that they meet in L2), then suffix
+// items. Tiles of the suffix are numbered along the batch; every warp finds
+// its own by a scan of cu_q, 32 sequences at a time. Called by whole warps.
+__device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, int64_t index, unsigned int* flags) {
+  PrefixItem it;
+  const int64_t prefix_items = int64_t(a.prefix_tiles) * a.k_heads * a.prefix_splits;
+  if (index < prefix_items) {
+    const int tile = int(index % a.prefix_tiles);
+    const int rest = int(index / a.prefix_tiles);
+    it.head = rest % a.k_heads;
+    it.split = rest / a.k_heads;
+    it.t0 = 0;
+    it.n = a.tokens;
+    it.r0 = tile * a.prefix_rows;
+    it.rows = min(a.prefix_rows, a.tokens * a.group - it.r0);
+    it.pages = a.prefix_pages;
+    it.len = a.prefix_len;
+    it.own = false;
+    it.k0 = int(min(int64_t(it.split) * a.chunk, int64_t(it.len)));
+    it.k1 = int(min(int64_t(it.k0) + a.chunk, int64_t(it.len)));
+    return it;
+  }
+  index -= prefix_items;
+  const int tile = int(index % a.suffix_tiles);
+  const int rest = int(index / a.suffix_tiles);
+  it.head = rest % a.k_heads;
+  const int split = rest / a.k_heads;
+  it.split = a.prefix_splits + split;
+  it.own = true;
+  it.rows = 0;
+  it.r0 = it.t0 = it.n = it.len = it.k0 = it.k1 = 0;
+  it.pages = a.suffix_pages;
+  const int lane = threadIdx.x & 31;
+  int before = 0;  // tiles of the sequences before this group of 32
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const int b = b0 + lane;
+    int lo = 0, hi = 0;
+    if (b < a.batch) {
+      lo = a.cu_q ? a.cu_q[b] : b;
+      hi = a.cu_q ? a.cu_q[b + 1] : b + 1;
+      const int l2 = min(max(lo, 0), a.tokens), h2 = min(max(hi, l2), a.tokens);
+      if (l2 != lo || h2 != hi) atomicOr(flags, kFlagBadIndex);
+      lo = l2;
+      hi = h2;
+    }
+    const int mine = ((hi - lo) * a.group + a.suffix_rows - 1) / a.suffix_rows;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + upto > tile);
+    if (past) {
+      const int src = __ffs(int(past)) - 1;
+      const int first = before + __shfl_sync(0xffffffffu, upto - mine, src);
+      const int seq = b0 + src;
+      it.t0 = __shfl_sync(0xffffffffu, lo, src);
+      it.n = __shfl_sync(0xffffffffu, hi, src) - it.t0;
+      it.r0 = (tile - first) * a.suffix_rows;
+      it.rows = min(a.suffix_rows, it.n * a.group - it.r0);
+      const int len = a.suffix_lens[seq];
+      it.len = min(max(len, 0), a.suffix_max);
+      if (it.len != len && lane == 0) atomicOr(flags, kFlagBadIndex);
+      it.pages = a.suffix_pages + int64_t(seq) * a.suffix_pages_stride;
+      const int sees = visible_keys(it, (it.r0 + it.rows - 1) / a.group);  // the tile's last row sees most
+      it.k0 = int(min(int64_t(split) * a.chunk, int64_t(sees)));
+      it.k1 = int(min(int64_t(it.k0) + a.chunk, int64_t(sees)));
+      return it;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return it;
+}
+
+// Byte offsets of key j's rows in the two caches. A page out of range is
+// reported; its keys are then taken as zeros (false).
+struct KeyOffset {
+  int64_t k, v;
+};
+__device__ __forceinline__ int key_page(const PrefixArgs& a, const PrefixItem& it, int j) {
+  return it.pages[a.page_shift >= 0 ? j >> a.page_shift : j / a.page_size];
+}
+__device__ __forceinline__ bool key_offset(const PrefixArgs& a, const PrefixItem& it, int j, int page,
+                                           unsigned int* flags, KeyOffset* off) {
+  if (unsigned(page) >= unsigned(a.num_pages)) {
+    atomicOr(flags, kFlagBadIndex);
+    return false;
+  }
+  const int slot = a.page_shift >= 0 ? j & (a.page_size - 1) : j % a.page_size;
+  off->k = int64_t(page) * a.k_ps + int64_t(slot) * a.k_ss + int64_t(it.head) * a.k_hs;
+  off->v = int64_t(page) * a.v_ps + int64_t(slot) * a.v_ss + int64_t(it.head) * a.v_hs;
+  return true;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+}  // namespace nf4
