@@ -39,16 +39,42 @@ _TYPES = {torch.bfloat16: NF4_BF16, torch.float16: NF4_FP16, torch.float32: NF4_
 _SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "ramp": 3}
 
 
-def _view(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> int:
-    """Pointer of a CUDA tensor of the given dtype and shape whose last dimension is contiguous."""
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(t: torch.Tensor, stream) -> int:
+    """The stream argument as a handle; None is the current stream of the tensor's device."""
+    if stream is None and _current_raw_stream is not None and t.is_cuda:
+        return _current_raw_stream(t.get_device())
+    return _stream(stream)
+
+
+# These calls stand between two launches of a decode step, where a microsecond on the host counts: each makes its
+# checks as one plain expression per tensor and builds the message only when one fails.
+
+def _bad(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple):
+    """Raises what is wrong with a tensor that should be on the GPU, of this dtype and shape."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.stride(-1) != 1 and shape[-1] > 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
+    raise ValueError(f"{name} must be contiguous" + (" in its last dimension" if len(shape) > 1 else ""))
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> tuple:
+    """(pointer, strides of the leading dimensions) of a tensor whose last dimension is contiguous."""
+    st = t.stride()
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or (st[-1] != 1 and shape[-1] > 1):
+        _bad(t, name, dtype, shape)
+    return t.data_ptr(), *st[:-1]
+
+
+def _flat(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> int:
+    """Pointer of a contiguous tensor."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _bad(t, name, dtype, shape)
     return t.data_ptr()
 
 
@@ -61,45 +87,55 @@ def nf4_rope_table(positions: int, rot_dim: int, base: float = 10000.0, scaling:
         raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
     if out is None:
         out = torch.empty((max(positions, 0), max(rot_dim, 0) // 2, 2), dtype=torch.float32, device=device or "cuda")
-    ptr = _view(out, "out", torch.float32, (positions, rot_dim // 2, 2))
-    if not out.is_contiguous():
-        raise ValueError("out must be contiguous")
+    ptr = _flat(out, "out", torch.float32, (positions, rot_dim // 2, 2))
     _check(_lib.nf4_rope_table(_TABLE.pack(ptr, positions, rot_dim, _SCALINGS[scaling], base, factor, low, high,
                                            original_positions, magnitude), _stream(stream)), "nf4_rope_table")
     return out
 
 
-def _qk_fields(q, q_out, k, k_out, positions, cos_sin, q_weight, k_weight, eps, interleaved) -> tuple:
-    """The fields of nf4_qk_norm_rope_args; q, or k_out, may be None."""
-    tokens, k_heads, dim = k.shape
+_NO_ROWS = (0, 0, 0, 0, 0, 0, 0)
+
+
+def _new_rows(x: torch.Tensor, shape: tuple) -> tuple:
+    """A new contiguous tensor like x, and its pointer and strides."""
+    y = x.new_empty(shape)
+    return y, (y.data_ptr(), shape[1] * shape[2], shape[2])
+
+
+def _qk_fields(q, q_out, k, k_out, append, positions, cos_sin, q_weight, k_weight, eps, interleaved) -> tuple:
+    """(q_out, k_out, fields of nf4_qk_norm_rope_args); outputs that are None are made, but no k_out to append."""
+    kshape = k.shape
+    tokens, k_heads, dim = kshape
     dt = k.dtype
-    if dt not in _TYPES:
+    code = _TYPES.get(dt)
+    if code is None:
         raise TypeError("q and k must be bf16, fp16 or fp32")
-    if cos_sin.dim() != 3 or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be contiguous, of shape [positions, rot_dim / 2, 2]")
-    max_pos, half, _ = cos_sin.shape
-    if not positions.is_contiguous():
-        raise ValueError("positions must be contiguous")
-    pos = _view(positions, "positions", torch.int64, (tokens,))
-    table = _view(cos_sin, "cos_sin", torch.float32, (max_pos, half, 2))
-    kp = _view(k, "k", dt, k.shape)
+    tshape = cos_sin.shape
+    if len(tshape) != 3 or tshape[2] != 2:
+        raise ValueError("cos_sin must have shape [positions, rot_dim / 2, 2]")
+    qf = _NO_ROWS
     if q is not None:
         heads = q.shape[1]
         shape = (tokens, heads, dim)
-        qs, qos = q.stride(), q_out.stride()
-        qf = (_view(q, "q", dt, shape), qs[0], qs[1], _view(q_out, "q_out", dt, shape), qos[0], qos[1], heads)
+        rows = _rows(q, "q", dt, shape)
+        if q_out is None:
+            q_out, orows = _new_rows(q, shape)
+        else:
+            orows = _rows(q_out, "q_out", dt, shape)
+        qf = (*rows, *orows, heads)
+    krows = _rows(k, "k", dt, kshape)
+    if append:
+        orows = (0, 0, 0)
+    elif k_out is None:
+        k_out, orows = _new_rows(k, kshape)
     else:
-        qf = (0, 0, 0, 0, 0, 0, 0)
-    ks = k.stride()
-    if k_out is not None:
-        kos = k_out.stride()
-        kf = (kp, ks[0], ks[1], _view(k_out, "k_out", dt, k.shape), kos[0], kos[1], k_heads)
-    else:
-        kf = (kp, ks[0], ks[1], 0, 0, 0, k_heads)
-    return (*qf, *kf, pos, table, max_pos, 2 * half, 1 if interleaved else 0,
-            _view(q_weight, "q_weight", dt, (dim,)) if q_weight is not None else 0,
-            _view(k_weight, "k_weight", dt, (dim,)) if k_weight is not None else 0,
-            eps, tokens, dim, _TYPES[dt])
+        orows = _rows(k_out, "k_out", dt, kshape)
+    return q_out, k_out, (*qf, *krows, *orows, k_heads, _flat(positions, "positions", torch.int64, (tokens,)),
+                          _flat(cos_sin, "cos_sin", torch.float32, tshape), tshape[0], 2 * tshape[1],
+                          1 if interleaved else 0,
+                          _flat(q_weight, "q_weight", dt, (dim,)) if q_weight is not None else 0,
+                          _flat(k_weight, "k_weight", dt, (dim,)) if k_weight is not None else 0,
+                          eps, tokens, dim, code)
 
 
 def nf4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
@@ -109,12 +145,10 @@ def nf4_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, 
     """Norm (where a weight is given) and rotation of q [tokens, q_heads, dim] and k [tokens, k_heads, dim];
     positions int64 [tokens], cos_sin as from nf4_rope_table. Returns (q_out, k_out), new tensors unless given
     (an output may be its input)."""
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    args = _QK.pack(*_qk_fields(q, q_out, k, k_out, positions, cos_sin, q_weight, k_weight, eps, interleaved))
-    _check(_lib.nf4_qk_norm_rope(args, _stream(stream)), "nf4_qk_norm_rope")
+    q_out, k_out, f = _qk_fields(q, q_out, k, k_out, False, positions, cos_sin, q_weight, k_weight, eps, interleaved)
+    status = _lib.nf4_qk_norm_rope(_QK.pack(*f), _stream_of(q, stream))
+    if status:
+        _check(status, "nf4_qk_norm_rope")
     return q_out, k_out
 
 
@@ -125,56 +159,51 @@ def nf4_kv_append(k_cache: torch.Tensor, v_cache: torch.Tensor, slots: torch.Ten
     """Writes the normed and rotated k and the v of each token to slot ``slots[token]`` (int64, page * page_size +
     offset; negative: nowhere) of the paged caches [pages, page_size, kv_heads, dim]. With q, its rows are normed
     and rotated in the same launch and returned."""
-    tokens, heads, dim = k.shape
+    kshape = k.shape
     dt = k.dtype
-    pages, page_size = k_cache.shape[0], k_cache.shape[1]
-    shape = (pages, page_size, heads, dim)
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if not slots.is_contiguous():
-        raise ValueError("slots must be contiguous")
-    vs, kc, vc = v.stride(), k_cache.stride(), v_cache.stride()
-    args = _APPEND.pack(*_qk_fields(q, q_out, k, None, positions, cos_sin, q_weight, k_weight, eps, interleaved),
-                        _view(v, "v", dt, k.shape), vs[0], vs[1], _view(slots, "slots", torch.int64, (tokens,)),
-                        _view(k_cache, "k_cache", dt, shape), kc[0], kc[1], kc[2],
-                        _view(v_cache, "v_cache", dt, shape), vc[0], vc[1], vc[2], pages, page_size)
-    _check(_lib.nf4_kv_append(args, _stream(stream)), "nf4_kv_append")
+    pages, page_size = k_cache.shape[:2]
+    shape = (pages, page_size, kshape[1], kshape[2])
+    q_out, _, f = _qk_fields(q, q_out, k, None, True, positions, cos_sin, q_weight, k_weight, eps, interleaved)
+    args = _APPEND.pack(*f, *_rows(v, "v", dt, kshape), _flat(slots, "slots", torch.int64, (kshape[0],)),
+                        *_rows(k_cache, "k_cache", dt, shape), *_rows(v_cache, "v_cache", dt, shape), pages, page_size)
+    status = _lib.nf4_kv_append(args, _stream_of(k, stream))
+    if status:
+        _check(status, "nf4_kv_append")
     return q_out
 
 
-def _attention_args(q, out, lse, k_cache, v_cache, prefix_pages, prefix_len, suffix_pages, suffix_lens, cu_q, scale):
-    tokens, heads, dim = q.shape
+def _attention_args(q, out_rows, lse, k_cache, v_cache, prefix_pages, prefix_len, suffix_pages, suffix_lens, cu_q,
+                    scale):
+    qshape = q.shape
+    tokens, heads, dim = qshape
     dt = q.dtype
-    if dt not in _TYPES:
+    code = _TYPES.get(dt)
+    if code is None:
         raise TypeError("q must be bf16 or fp16")
     shape = k_cache.shape
-    pages, page_size, k_heads, _ = shape
-    if shape[3] != dim:
-        raise ValueError(f"k_cache has head_dim {shape[3]}, q has {dim}")
-    batch, width = suffix_pages.shape
-    if prefix_pages.dim() != 1 or not prefix_pages.is_contiguous():
-        raise ValueError("prefix_pages must be contiguous, of one dimension")
-    if prefix_pages.shape[0] * page_size < prefix_len:
-        raise ValueError(f"prefix_pages has {prefix_pages.shape[0]} pages of {page_size}, prefix_len is {prefix_len}")
-    if not suffix_lens.is_contiguous() or (cu_q is not None and not cu_q.is_contiguous()):
-        raise ValueError("suffix_lens and cu_q must be contiguous")
-    qs, os, kc, vc = q.stride(), out.stride(), k_cache.stride(), v_cache.stride()
-    return _ATTN.pack(_view(q, "q", dt, q.shape), qs[0], qs[1], _view(out, "out", dt, q.shape), os[0], os[1],
-                      0 if lse is None else _view(lse, "lse", torch.float32, (tokens, heads)),
-                      _view(k_cache, "k_cache", dt, shape), kc[0], kc[1], kc[2],
-                      _view(v_cache, "v_cache", dt, shape), vc[0], vc[1], vc[2], pages, page_size,
-                      _view(prefix_pages, "prefix_pages", torch.int32, prefix_pages.shape), prefix_len,
-                      _view(suffix_pages, "suffix_pages", torch.int32, (batch, width)), suffix_pages.stride(0), width,
-                      _view(suffix_lens, "suffix_lens", torch.int32, (batch,)),
-                      0 if cu_q is None else _view(cu_q, "cu_q", torch.int32, (batch + 1,)),
-                      batch, tokens, heads, k_heads, dim, _TYPES[dt], scale)
+    pages, page_size, k_heads, kdim = shape
+    if kdim != dim:
+        raise ValueError(f"k_cache has head_dim {kdim}, q has {dim}")
+    sshape = suffix_pages.shape
+    batch, width = sshape
+    pshape = prefix_pages.shape
+    if len(pshape) != 1 or pshape[0] * page_size < prefix_len:
+        raise ValueError(f"prefix_pages of shape {tuple(pshape)}, pages of {page_size}, prefix_len {prefix_len}")
+    return _ATTN.pack(*_rows(q, "q", dt, qshape), *out_rows,
+                      0 if lse is None else _flat(lse, "lse", torch.float32, (tokens, heads)),
+                      *_rows(k_cache, "k_cache", dt, shape), *_rows(v_cache, "v_cache", dt, shape), pages, page_size,
+                      _flat(prefix_pages, "prefix_pages", torch.int32, pshape), prefix_len,
+                      *_rows(suffix_pages, "suffix_pages", torch.int32, sshape), width,
+                      _flat(suffix_lens, "suffix_lens", torch.int32, (batch,)),
+                      0 if cu_q is None else _flat(cu_q, "cu_q", torch.int32, (batch + 1,)),
+                      batch, tokens, heads, k_heads, dim, code, scale)
 
 
 def nf4_prefix_attention_workspace_size(q, k_cache, v_cache, prefix_pages, prefix_len, suffix_pages, suffix_lens,
                                         cu_q=None, scale: float = 1.0) -> int:
     """Bytes of workspace that nf4_prefix_attention needs for tensors of these shapes."""
     return int(_lib.nf4_prefix_attention_workspace_size(
-        _attention_args(q, q, None, k_cache, v_cache, prefix_pages, prefix_len, suffix_pages, suffix_lens, cu_q, scale)))
+        _attention_args(q, (0, 0, 0), None, k_cache, v_cache, prefix_pages, prefix_len, suffix_pages, suffix_lens, cu_q, scale)))
 
 
 def nf4_prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, prefix_pages: torch.Tensor,
@@ -187,23 +216,31 @@ def nf4_prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     ``suffix_lens`` (int32 [batch]) keys on its row of ``suffix_pages`` (int32 [batch, width]), causal among the
     sequence's tokens cu_q[b] .. cu_q[b + 1] - 1 (int32 [batch + 1]; None: one token each). Returns out, or
     (out, lse) with ``return_lse``. The scale defaults to 1 / sqrt(dim)."""
+    shape = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out, out_rows = _new_rows(q, shape)
+    else:
+        out_rows = _rows(out, "out", q.dtype, shape)
     if return_lse and lse is None:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    if lse is not None and not lse.is_contiguous():
-        raise ValueError("lse must be contiguous")
+        lse = q.new_empty(shape[:2], dtype=torch.float32)
     if scale is None:
-        scale = q.shape[2] ** -0.5
-    s = _stream(stream)
-    args = _attention_args(q, out, lse, k_cache, v_cache, prefix_pages, prefix_len, suffix_pages, suffix_lens, cu_q,
-                           scale)
-    need = _lib.nf4_prefix_attention_workspace_size(args)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None:  # the allocator may not hand it out again before this stream is done with it
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(s))
-    _check(_lib.nf4_prefix_attention(args, workspace.data_ptr() if workspace is not None else None,
-                                     workspace.numel() * workspace.element_size() if workspace is not None else 0, s),
-           "nf4_prefix_attention")
+        scale = shape[2] ** -0.5
+    s = _stream_of(q, stream)
+    args = _attention_args(q, out_rows, lse, k_cache, v_cache, prefix_pages, prefix_len, suffix_pages, suffix_lens,
+                           cu_q, scale)
+    if workspace is not None:
+        ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+    else:
+        ws, size = None, _lib.nf4_prefix_attention_workspace_size(args)
+        if size > 0:
+            workspace = q.new_empty(size, dtype=torch.uint8)
+            ws = workspace.data_ptr()
+            if stream is not None:  # the allocator may not hand it out again before this stream is done with it
+                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                        else torch.cuda.ExternalStream(s))
+    status = _lib.nf4_prefix_attention(args, ws, size, s)
+    if status:
+        _check(status, "nf4_prefix_attention")
     return (out, lse) if return_lse else out

@@ -13,6 +13,7 @@ constexpr unsigned kFlagWaitRanOut = 1u;  // a bounded wait ran out
 constexpr unsigned kFlagBadIndex = 2u;    // a position, slot, page, length or cu_q entry out of range
 cudaError_t read_and_clear_rope_flags(unsigned int* flags);
 cudaError_t read_and_clear_prefix_flags(unsigned int* flags);
+cudaError_t read_and_clear_prefix_tc_flags(unsigned int* flags);
 
 nf4_status status_of(cudaError_t e);
 

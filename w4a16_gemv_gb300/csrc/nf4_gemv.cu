@@ -378,11 +378,12 @@ cudaError_t dispatch_batch(const QuantTensor& t, int64_t N, int64_t K, const uin
 cudaError_t read_and_clear_device_flags(unsigned int* flags) {
   // one word per translation unit that reports something: the tensor-core
   // GEMV (waits) and the attention side (indices read on the device)
-  unsigned int part[3] = {0u, 0u, 0u};
+  unsigned int part[4] = {0u, 0u, 0u, 0u};
   cudaError_t e = read_and_clear_tc_flags(&part[0]);
   if (e == cudaSuccess) e = read_and_clear_rope_flags(&part[1]);
   if (e == cudaSuccess) e = read_and_clear_prefix_flags(&part[2]);
-  if (e == cudaSuccess) *flags = part[0] | part[1] | part[2];
+  if (e == cudaSuccess) e = read_and_clear_prefix_tc_flags(&part[3]);
+  if (e == cudaSuccess) *flags = part[0] | part[1] | part[2] | part[3];
   return e;
 }
 

@@ -22,15 +22,6 @@ constexpr int kWarps = 4;
 constexpr int kKeys = 64;    // keys per stage
 constexpr int kStages = 3;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -55,26 +46,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  "{%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Where a finished row goes: the partial results, or, when the row has one
-// range of keys only, the output itself.
-struct RowOut {
-  float* part;
-  float2* ml;
-  char* out;
-  float* lse;
-};
-__device__ __forceinline__ RowOut row_out(const PrefixArgs& a, const PrefixItem& it, int r) {
-  const int t = it.t0 + r / a.group;
-  const int h = it.head * a.group + r % a.group;
-  const int64_t row = int64_t(t) * a.q_heads + h;
-  RowOut o;
-  o.part = a.part + (int64_t(it.split) * a.tokens * a.q_heads + row) * a.dim;
-  o.ml = a.ml + row * a.splits + it.split;
-  o.out = a.out + int64_t(t) * a.out_ts + int64_t(h) * a.out_hs;
-  o.lse = a.lse ? a.lse + row : nullptr;
-  return o;
 }
 
 // One item with tiles of R rows. R = 64: a warp has 16 rows and all keys of a
@@ -339,17 +310,24 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
   }
 }
 
+// `beside`: the launch before this one is the tensor-core items of the same
+// call, which this one does not depend on. Its CTAs all waited for the grids
+// before it ahead of letting this one start, so there is nothing to wait for
+// here; but what follows (the join) only waits for this launch, so its last
+// CTA ends after the other launch did.
 template <typename H, int DP>
 __global__ void __launch_bounds__(kThreads) prefix_mma_kernel(const __grid_constant__ PrefixArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   pdl_allow_dependents();
-  pdl_wait_prior_grid();
-  const PrefixItem it = prefix_item(a, blockIdx.x, &g_prefix_flags);
-  if (it.rows <= 0) return;
-  if (it.own ? a.suffix_rows == 64 : a.prefix_rows == 64)
-    attend<H, DP, 64>(a, it, smem);
-  else
-    attend<H, DP, 16>(a, it, smem);
+  if (!a.beside) pdl_wait_prior_grid();
+  const PrefixItem it = prefix_item(a, int64_t(a.first) + blockIdx.x, &g_prefix_flags);
+  if (it.rows > 0) {
+    if (it.own ? a.suffix_rows == 64 : a.prefix_rows == 64)
+      attend<H, DP, 64>(a, it, smem);
+    else
+      attend<H, DP, 16>(a, it, smem);
+  }
+  if (a.beside && blockIdx.x + 1 == gridDim.x) pdl_wait_prior_grid();
 }
 
 // Joins a row's partial results: one warp per row, four elements per lane.
@@ -425,13 +403,59 @@ cudaError_t launch_typed(const PrefixArgs& p, cudaStream_t stream) {
   const int64_t rows = int64_t(p.tokens) * p.q_heads;
   const unsigned row_blocks = unsigned((rows + 3) / 4);
   if (p.splits == 0) return launch_k(prefix_empty_kernel<H>, dim3(row_blocks), dim3(128), 0, stream, p);
-  const int64_t items = (int64_t(p.prefix_tiles) * p.prefix_splits + int64_t(p.suffix_tiles) * p.suffix_splits) *
-                        p.k_heads;
-  if (items > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = p.dim <= 64 ? launch_mma<H, 64>(p, unsigned(items), stream)
-                                    : launch_mma<H, 128>(p, unsigned(items), stream);
+  const int64_t prefix_items = int64_t(p.prefix_tiles) * p.prefix_splits * p.k_heads;
+  const int64_t suffix_items = int64_t(p.suffix_tiles) * p.suffix_splits * p.k_heads;
+  if (prefix_items + suffix_items > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  const int64_t on_tc = (p.tc_prefix ? prefix_items : 0) + (p.tc_suffix ? suffix_items : 0);
+  cudaError_t e = cudaSuccess;
+  if (on_tc > 0) e = launch_prefix_tc(p, H::kDtype, unsigned(on_tc), stream);
+  const int64_t rest = prefix_items + suffix_items - on_tc;
+  if (e == cudaSuccess && rest > 0) {
+    PrefixArgs q = p;
+    q.first = int(on_tc);
+    q.beside = on_tc > 0;
+    e = p.dim <= 64 ? launch_mma<H, 64>(q, unsigned(rest), stream) : launch_mma<H, 128>(q, unsigned(rest), stream);
+  }
   if (e != cudaSuccess || p.direct) return e;
   return launch_k(prefix_join_kernel<H>, dim3(row_blocks), dim3(128), 0, stream, p);
+}
+
+}  // namespace
+
+namespace {
+
+constexpr int kSms = 152;
+constexpr int kMaxRanges = 64;  // per row, of the shared and of the own keys each
+#ifndef TCROWS
+#define TCROWS 32
+#endif
+
+// Keys per range of the mma kernel, in stages of 64: at least two stages,
+// about eight items per SM, at most kMaxRanges ranges.
+int64_t mma_range(int64_t tiles, int64_t stages) {
+  int64_t per = tiles * stages / (kSms * 8);
+  per = per < 2 ? 2 : per;
+  return stages > per * kMaxRanges ? (stages + kMaxRanges - 1) / kMaxRanges : per;
+}
+
+// Keys per range of the tensor-core kernel (one CTA per SM), in stages of 64
+// but whole tiles of 128: the number of ranges that ends soonest, counting a
+// wave of CTAs as its key tiles plus about three for its start and end, and
+// the partial results of a range (written and read in binary32, about 8 TB/s)
+// in the same unit of about a microsecond.
+int64_t tc_range(int64_t tiles, int64_t key_tiles, int64_t rows) {
+  int64_t best = key_tiles;
+  double least = 1e300;
+  for (int64_t s = 1; s <= kMaxRanges && s <= key_tiles; ++s) {
+    const int64_t per = (key_tiles + s - 1) / s, used = (key_tiles + per - 1) / per;
+    const int64_t waves = (tiles * used + kSms - 1) / kSms;
+    const double cost = double(waves) * double(per + 3) + (used > 1 ? double(used) * double(rows) * 1e-4 : 0.0);
+    if (cost < least) {
+      least = cost;
+      best = per;
+    }
+  }
+  return 2 * best;
 }
 
 }  // namespace
@@ -448,22 +472,29 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
   p->prefix_len = int(a.prefix_len);
   p->suffix_max = a.batch > 0 ? int(a.suffix_pages_width * a.page_size) : 0;
   const int64_t rows = a.tokens * p->group;  // of a key/value head
-  p->prefix_rows = rows > 32 ? 64 : 16;
-  p->suffix_rows = rows > 32 * a.batch ? 64 : 16;
+  // Many rows go to the tensor cores. (Suffix items only when the prefix's do,
+  // so that the items of each kernel are one range.)
+  p->tc_prefix = rows > TCROWS && p->prefix_len > 0;
+  p->tc_suffix = rows > 64 * a.batch && (p->tc_prefix || p->prefix_len == 0);
+  p->prefix_rows = p->tc_prefix ? 256 : rows > 32 ? 64 : 16;
+  p->suffix_rows = p->tc_suffix ? 256 : rows > 32 * a.batch ? 64 : 16;
   p->prefix_tiles = int((rows + p->prefix_rows - 1) / p->prefix_rows);
   // sum over sequences of ceil(rows / suffix_rows) is below both bounds
   const int64_t whole = rows / p->suffix_rows + a.batch;
   p->suffix_tiles = int(whole < rows ? whole : rows);
   const int64_t pk = (int64_t(p->prefix_len) + kKeys - 1) / kKeys, sk = (int64_t(p->suffix_max) + kKeys - 1) / kKeys;
-  const int64_t total = (p->prefix_tiles * pk + p->suffix_tiles * sk) * p->k_heads;
-  // ranges of at least two stages, about eight items per SM, at most 64 ranges of each kind
-  int64_t per = total / (152 * 8);
-  per = per < 2 ? 2 : per;
-  const int64_t longest = pk > sk ? pk : sk;
-  if (longest > per * 64) per = (longest + 63) / 64;
-  p->chunk = int(per * kKeys > 0x40000000ll ? 0x40000000ll : per * kKeys);
-  p->prefix_splits = int((pk + per - 1) / per);
-  p->suffix_splits = int((sk + per - 1) / per);
+  if (pk > 0) {
+    const int64_t per = p->tc_prefix ? tc_range(int64_t(p->prefix_tiles) * p->k_heads, (pk + 1) / 2, rows * p->k_heads)
+                                     : mma_range(int64_t(p->prefix_tiles) * p->k_heads, pk);
+    p->prefix_chunk = int(per * kKeys);
+    p->prefix_splits = int((pk + per - 1) / per);
+  }
+  if (sk > 0) {
+    const int64_t per = p->tc_suffix ? tc_range(int64_t(p->suffix_tiles) * p->k_heads, (sk + 1) / 2, rows * p->k_heads)
+                                     : mma_range(int64_t(p->suffix_tiles) * p->k_heads, sk);
+    p->suffix_chunk = int(per * kKeys);
+    p->suffix_splits = int((sk + per - 1) / per);
+  }
   if (rows == 0) p->prefix_splits = p->suffix_splits = 0;
   p->splits = p->prefix_splits + p->suffix_splits;
   const int64_t all = a.tokens * a.q_heads;

@@ -32,15 +32,22 @@ struct PrefixArgs {
   // plan
   int prefix_rows, suffix_rows;                    // rows per tile
   int prefix_tiles, suffix_tiles;                  // tiles of a key/value head (suffix: an upper bound)
-  int prefix_splits, suffix_splits, chunk;         // ranges of `chunk` keys each
+  int prefix_splits, suffix_splits;                // ranges of keys, of this many each:
+  int prefix_chunk, suffix_chunk;
   int splits;                                      // prefix_splits + suffix_splits
   int direct;                                      // 1: one range of shared keys is all; its items write the output
+  int tc_prefix, tc_suffix;                        // which items run on the tensor-core kernel
+  int first;                                       // first item of the launch
+  int beside;                                      // 1: runs beside the launch before it (see prefix_mma_kernel)
   float* part;                                     // [splits][tokens * q_heads][dim]
   float2* ml;                                      // [tokens * q_heads][splits]: (maximum, sum)
 };
 
 // The sizes and the plan of a call, and the bytes of its workspace.
 void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, size_t* bytes);
+
+// Items [0, items) on the tensor cores (nf4_prefix_attn_tc.cu).
+cudaError_t launch_prefix_tc(const PrefixArgs& p, nf4_dtype dtype, unsigned items, cudaStream_t stream);
 
 // One work item, the same in every thread.
 struct PrefixItem {
@@ -80,8 +87,8 @@ __device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, int64_t i
     it.pages = a.prefix_pages;
     it.len = a.prefix_len;
     it.own = false;
-    it.k0 = int(min(int64_t(it.split) * a.chunk, int64_t(it.len)));
-    it.k1 = int(min(int64_t(it.k0) + a.chunk, int64_t(it.len)));
+    it.k0 = int(min(int64_t(it.split) * a.prefix_chunk, int64_t(it.len)));
+    it.k1 = int(min(int64_t(it.k0) + a.prefix_chunk, int64_t(it.len)));
     return it;
   }
   index -= prefix_items;
@@ -128,8 +135,8 @@ __device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, int64_t i
       if (it.len != len && lane == 0) atomicOr(flags, kFlagBadIndex);
       it.pages = a.suffix_pages + int64_t(seq) * a.suffix_pages_stride;
       const int sees = visible_keys(it, (it.r0 + it.rows - 1) / a.group);  // the tile's last row sees most
-      it.k0 = int(min(int64_t(split) * a.chunk, int64_t(sees)));
-      it.k1 = int(min(int64_t(it.k0) + a.chunk, int64_t(sees)));
+      it.k0 = int(min(int64_t(split) * a.suffix_chunk, int64_t(sees)));
+      it.k1 = int(min(int64_t(it.k0) + a.suffix_chunk, int64_t(sees)));
       return it;
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
@@ -164,5 +171,34 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 constexpr float kLn2 = 0.6931471805599453f;
+
+// Where a finished row goes: the partial results, or, when one range of keys
+// is all there is, the output itself.
+struct RowOut {
+  float* part;
+  float2* ml;
+  char* out;
+  float* lse;
+};
+__device__ __forceinline__ RowOut row_out(const PrefixArgs& a, const PrefixItem& it, int r) {
+  const int t = it.t0 + r / a.group;
+  const int h = it.head * a.group + r % a.group;
+  const int64_t row = int64_t(t) * a.q_heads + h;
+  RowOut o;
+  o.part = a.part + (int64_t(it.split) * a.tokens * a.q_heads + row) * a.dim;
+  o.ml = a.ml + row * a.splits + it.split;
+  o.out = a.out + int64_t(t) * a.out_ts + int64_t(h) * a.out_hs;
+  o.lse = a.lse ? a.lse + row : nullptr;
+  return o;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 }  // namespace nf4

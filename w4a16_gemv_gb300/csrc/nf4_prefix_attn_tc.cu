@@ -1,0 +1,497 @@
+// nf4_prefix_attn_tc.cu -- the many-row items of nf4_prefix_attention on the
+// 5th-generation tensor cores: up to 256 rows of a key/value head (every query
+// token of the batch times its group of query heads) against a range of keys.
+//
+// S = Q K^T and O += P V per 128 keys, as two tiles of 128 rows that take
+// turns: while the softmax of one tile runs on the CUDA cores, the tensor
+// cores do the other's products. Per 128 keys and tile of 128 rows the two
+// products take 2 x 128 x 128 x 128 multiply-adds (about 1000 cycles of an
+// SM's tensor cores at head_dim 128), the softmax 16384 exponentials, about
+// half of that: with two full tiles the tensor cores bound it, with few rows the
+// bytes of the keys and values do (32 KB each per 128 keys).
+//
+// One CTA of 16 warps per SM:
+//   * warps 0-3 and 4-7: softmax of tile 0 and 1, one row per thread. Scores
+//     come from tensor memory into registers, the weights exp2(s - m) go back as
+//     16-bit pairs over the same columns, where the second product reads them
+//     as its A operand. m is the maximum at the time of the last rescale: O and l are
+//     rescaled only when a row's maximum has grown past 2^8 (exact all the same,
+//     since O and l share m; binary32 and the 16-bit weights hold 2^8 times 1
+//     with the same relative error), so that O is rarely touched;
+//   * warps 8-11: keys and values from their pages into a ring of 128-row
+//     tiles by 16-byte asynchronous copies (any page size and stride; rows past
+//     the range are zero-filled, so what lies in unused slots never reaches a
+//     product), swizzled for the tensor cores: the same layout serves K as a
+//     K-major and V as an N-major operand;
+//   * warp 12: issues the products. S of the next keys follows O += P V of a
+//     tile in issue order, so P is read before S overwrites it, and the signal
+//     that S is complete also says that O is at rest.
+// Tensor memory: S (and P) of the tiles in columns 0 and 128, O in 256 and 384.
+// Waits are bounded; one that runs out sets bit 0 of the device error flags.
+#include "nf4_prefix_attn.cuh"
+
+namespace nf4 {
+namespace {
+
+__device__ unsigned int g_prefix_tc_flags = 0;
+
+constexpr int kTcThreads = 512;
+constexpr int kTileRows = 128;
+constexpr int kTileKeys = 128;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kGrowth = 8.0f;  // log2 of the growth of a row's maximum that is let pass
+// Registers: 512 threads launch with 128 each (65536); the two softmax
+// warpgroups take 192, the others keep 64: 256 x 192 + 256 x 64 = 65536.
+constexpr int kLaunchRegs = 128;
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+// Shared-memory matrix descriptors, 128-byte swizzle: rows of 128 bytes in
+// groups of eight (1024 bytes apart).
+// K-major (rows along M or N, 64 elements of K per row; a further 64 elements
+// of K lie in the next block, addressed by the caller).
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t saddr) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
+         (uint64_t(2) << 61);
+}
+// N-major (rows along K, 64 elements of N per row; the next 64 elements of N
+// lie `block` bytes on).
+__device__ __forceinline__ uint64_t desc_n_major(uint32_t saddr, uint32_t block) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(block >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// Instruction descriptor of kind::f16: binary32 accumulator, A and B of the
+// same 16-bit type, M = 128.
+template <typename H>
+__device__ __forceinline__ constexpr uint32_t idesc(int n, bool b_n_major) {
+  return (1u << 4) | (H::kDtype == NF4_BF16 ? (1u << 7) | (1u << 10) : 0u) | (b_n_major ? 1u << 16 : 0u) |
+         (uint32_t(n >> 3) << 17) | (uint32_t(kTileRows >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(accumulate)
+      : "memory");
+}
+
+// 32 columns of this warp's lanes (a thread's 32 values are one row's).
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// The loaded values may be used after this (uses are tied to it by the
+// compiler through the operands).
+__device__ __forceinline__ void tmem_ld_wait(float* v, int n) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < n; ++i) asm volatile("" : "+f"(v[i]));
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+template <int DP>
+struct Layout {
+  static constexpr int kBlocks = DP / 64;                       // 128-byte columns blocks of a row
+  static constexpr uint32_t kBlock = 128 * 128;                 // bytes of one block of 128 rows
+  static constexpr uint32_t kTile = kBlocks * kBlock;           // 128 rows
+  static constexpr int kStages = DP == 128 ? 5 : 8;             // ring of K and V tiles
+  static constexpr int kLag = 3;                                // tiles that a loader leaves in flight
+  static constexpr uint32_t kRing = 2 * kTile;                  // after the two tiles of Q
+  static constexpr uint32_t kBars = kRing + kStages * kTile;
+  static constexpr uint32_t kBytes = kBars + 256 + 1024;        // + slack to align the base
+};
+
+template <typename H, int DP>
+__global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_constant__ PrefixArgs a) {
+  using L = Layout<DP>;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  unsigned char* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + L::kBars);  // ring tile landed (4 loader warps)
+  uint64_t* const empty = full + L::kStages;                            // its products are done
+  uint64_t* const sfull = empty + L::kStages;                           // S of a tile complete, O at rest
+  uint64_t* const pfull = sfull + 2;                                    // P of a tile written (4 softmax warps)
+  uint32_t* const s_taddr = reinterpret_cast<uint32_t*>(pfull + 2);
+
+  // Everything, the tensor memory included, waits for the previous grid: an
+  // allocation held by a grid that waits could starve the one waited for.
+  pdl_wait_prior_grid();
+  const PrefixItem it = prefix_item(a, blockIdx.x, &g_prefix_tc_flags);
+  const int n = (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys;  // key tiles
+  const bool works = it.rows > 0 && n > 0;                    // the same in the whole CTA
+  if (warp == 12 && works) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_taddr)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(&full[i], 4);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 4);
+    }
+    fence_mbar_init();
+  }
+  const int tiles = it.rows > kTileRows ? 2 : 1;
+  // Q: warp w of the softmax warps brings rows 32 w .. 32 w + 31 of the pair of tiles
+  if (warp < 8 && works && (warp >> 2) < tiles) {
+    constexpr int CPR = DP / 8, RPI = 32 / CPR;
+    const int r = warp * 32 + lane;
+    int64_t off = 0;
+    if (r < it.rows) {
+      const int rr = it.r0 + r;
+      off = int64_t(it.t0 + rr / a.group) * a.q_ts + int64_t(it.head * a.group + rr % a.group) * a.q_hs;
+    }
+    const int c = lane % CPR;
+#pragma unroll 4
+    for (int x = 0; x < 32 / RPI; ++x) {
+      const int rl = x * RPI + lane / CPR;
+      const int64_t o = __shfl_sync(0xffffffffu, off, rl);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (warp * 32 + rl < it.rows && c * 8 < a.dim) v = __ldg(reinterpret_cast<const uint4*>(a.q + o + c * 16));
+      const int row = (warp & 3) * 32 + rl;
+      *reinterpret_cast<uint4*>(smem + (warp >> 2) * L::kTile + (c >> 3) * L::kBlock + row * 128 +
+                                (((c & 7) ^ (row & 7)) << 4)) = v;
+    }
+    fence_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_allow_dependents();  // after the allocation, for the same reason
+  if (!works) {
+    for (int r = tid; r < it.rows; r += kTcThreads) {
+      const RowOut ro = row_out(a, it, it.r0 + r);
+      *ro.ml = make_float2(-INFINITY, 0.0f);  // (a plan with one range of keys has no empty range)
+    }
+    return;
+  }
+  const uint32_t tbase = *s_taddr;
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (ok) ok = mbar_wait_bounded(bar, parity, kWaitLimitCycles);
+  };
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    const int tile = warp >> 2;
+    if (tile < tiles) {
+      const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+      const uint32_t s_col = tbase + lanes + uint32_t(tile) * 128u;
+      const uint32_t o_col = tbase + lanes + 256u + uint32_t(tile) * 128u;
+      const int r = tile * kTileRows + (warp & 3) * 32 + lane;
+      const int limit = r < it.rows ? min(visible_keys(it, (it.r0 + r) / a.group), it.k1) - it.k0 : 0;
+      // key tiles below this one need no mask in this warp
+      int free_tiles = limit / kTileKeys;
+      if (r >= it.rows) free_tiles = n;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) free_tiles = min(free_tiles, __shfl_xor_sync(0xffffffffu, free_tiles, d));
+      float m = -INFINITY;
+      float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        wait(&sfull[tile], uint32_t(i) & 1u);
+        __syncwarp();
+        tc_fence_after();
+        float s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32u * c, s + 32 * c);
+        tmem_ld_wait(s, 128);
+        if (i >= free_tiles) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (i * kTileKeys + j >= limit) s[j] = -INFINITY;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = s[c];
+#pragma unroll
+          for (int j = 1; j < 32; ++j) mx[c] = fmaxf(mx[c], s[4 * j + c]);
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        if (i == 0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, top > m + kGrowth)) {
+          const float nm = fmaxf(m, top);
+          const float f = nm == -INFINITY ? 1.0f : ex2(m - nm);
+          m = nm;
+          l2[0].x *= f;
+          l2[0].y *= f;
+          l2[1].x *= f;
+          l2[1].y *= f;
+#pragma unroll 1
+          for (int c = 0; c < DP / 32; ++c) {
+            float o[32];
+            tmem_ld32(o_col + 32u * c, o);
+            tmem_ld_wait(o, 32);
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(o[j] * f);
+            tmem_st32(o_col + 32u * c, w);
+          }
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+        const float2 nb2 = make_float2(-base, -base);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t p[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float2 e = fma2(make_float2(s[64 * h + 2 * j], s[64 * h + 2 * j + 1]), scale2, nb2);
+            const float2 w = make_float2(ex2(e.x), ex2(e.y));
+            l2[j & 1] = add2(l2[j & 1], w);
+            p[j] = H::down2(w.x, w.y);
+          }
+          tmem_st32(s_col + 32u * h, p);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[tile]);
+      }
+      wait(&sfull[tile], uint32_t(n) & 1u);  // the last product is in O
+      __syncwarp();
+      tc_fence_after();
+      const float l = l2[0].x + l2[0].y + (l2[1].x + l2[1].y);
+      const bool any = l > 0.0f || l != l;
+      const float inv = any ? 1.0f / l : 0.0f;
+      const bool mine = r < it.rows;
+      const RowOut ro = row_out(a, it, it.r0 + (mine ? r : 0));
+      const float bad = ok ? 0.0f : __uint_as_float(0x7fc00000u);
+#pragma unroll 1
+      for (int c = 0; c < DP / 32; ++c) {
+        float o[32];
+        tmem_ld32(o_col + 32u * c, o);
+        tmem_ld_wait(o, 32);
+        if (!mine) continue;
+        if (!a.direct) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            if (32 * c + j < a.dim)
+              *reinterpret_cast<float4*>(ro.part + 32 * c + j) =
+                  make_float4(o[j] + bad, o[j + 1] + bad, o[j + 2] + bad, o[j + 3] + bad);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; j += 8)
+            if (32 * c + j < a.dim)
+              *reinterpret_cast<uint4*>(ro.out + (32 * c + j) * 2) =
+                  make_uint4(H::down2(o[j] * inv + bad, o[j + 1] * inv + bad), H::down2(o[j + 2] * inv + bad, o[j + 3] * inv + bad),
+                             H::down2(o[j + 4] * inv + bad, o[j + 5] * inv + bad), H::down2(o[j + 6] * inv + bad, o[j + 7] * inv + bad));
+        }
+      }
+      if (mine) {
+        if (!a.direct)
+          *ro.ml = make_float2(m, l);
+        else if (ro.lse)
+          *ro.lse = any ? fmaf(m, kLn2, logf(l)) : -INFINITY;
+      }
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    constexpr int CPR = DP / 8, RPI = 32 / CPR;
+    const int w = warp - 8;
+    const int c = lane % CPR;
+    const bool col = c * 8 < a.dim;
+    const uint32_t col_off = uint32_t(c >> 3) * L::kBlock;
+    KeyOffset off{0, 0};
+    bool real = false;
+    int page = 0;
+    auto fetch_page = [&](int i) {
+      const int j = it.k0 + i * kTileKeys + w * 32 + lane;
+      if (j < it.k1) page = key_page(a, it, j);
+    };
+    fetch_page(0);
+#pragma unroll 1
+    for (int u = 0; u < 2 * n; ++u) {
+      const int slot = u % L::kStages;
+      if (u >= L::kStages) wait(&empty[slot], uint32_t(u / L::kStages - 1) & 1u);
+      if ((u & 1) == 0) {
+        const int j = it.k0 + (u >> 1) * kTileKeys + w * 32 + lane;
+        real = j < it.k1 && key_offset(a, it, j, page, &g_prefix_tc_flags, &off);
+        if (u + 2 < 2 * n) fetch_page((u >> 1) + 1);
+      }
+      const char* src = (u & 1) == 0 ? a.k : a.v;
+      const int64_t mine = (u & 1) == 0 ? off.k : off.v;
+      const uint32_t dst = sbase + L::kRing + uint32_t(slot) * L::kTile + col_off;
+#pragma unroll
+      for (int x = 0; x < 32 / RPI; ++x) {
+        const int rl = x * RPI + lane / CPR;
+        const int64_t o = __shfl_sync(0xffffffffu, mine, rl);
+        const bool there = __shfl_sync(0xffffffffu, int(real), rl) && col;
+        const int row = w * 32 + rl;
+        cp_async16(dst + uint32_t(row) * 128u + uint32_t(((c & 7) ^ (row & 7)) << 4), there ? src + o + c * 16 : a.q, there);
+      }
+      cp_async_commit();
+      if (u >= L::kLag) {
+        cp_async_wait<L::kLag>();
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[(u - L::kLag) % L::kStages]);
+      }
+    }
+    cp_async_wait<0>();
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0)
+      for (int u = 2 * n > L::kLag ? 2 * n - L::kLag : 0; u < 2 * n; ++u) mbar_arrive(&full[u % L::kStages]);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 12 && lane == 0) {
+      constexpr uint32_t kIdS = idesc<H>(kTileKeys, false);
+      constexpr uint32_t kIdO = idesc<H>(DP, true);
+      const uint32_t ring = sbase + L::kRing;
+      auto wait_full = [&](int u) {
+        wait(&full[u % L::kStages], uint32_t(u / L::kStages) & 1u);
+        tc_fence_after();
+      };
+      auto product_s = [&](int t, int u) {  // S_t = Q_t K^T, K in ring tile u
+        const uint64_t qd = desc_k_major(sbase + uint32_t(t) * L::kTile);
+        const uint64_t kd = desc_k_major(ring + uint32_t(u % L::kStages) * L::kTile);
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s) {
+          const uint64_t step = uint64_t((s >> 2) * (L::kBlock >> 4) + (s & 3) * 2);
+          mma_ss(tbase + uint32_t(t) * 128u, qd + step, kd + step, kIdS, s > 0 ? 1u : 0u);
+        }
+        tc_commit(&sfull[t]);
+      };
+      wait_full(0);
+      for (int t = 0; t < tiles; ++t) product_s(t, 0);
+      tc_commit(&empty[0]);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int uv = 2 * i + 1, uk = 2 * i + 2;
+        const bool more = i + 1 < n;
+        wait_full(uv);
+        const uint64_t vd = desc_n_major(ring + uint32_t(uv % L::kStages) * L::kTile, L::kBlock);
+        for (int t = 0; t < tiles; ++t) {
+          wait(&pfull[t], uint32_t(i) & 1u);
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < kTileKeys / 16; ++s)  // 16 keys: two groups of eight rows
+            mma_ts(tbase + 256u + uint32_t(t) * 128u, tbase + uint32_t(t) * 128u + 8u * s, vd + uint64_t(s * (2048 >> 4)),
+                   kIdO, (i > 0 || s > 0) ? 1u : 0u);
+          if (t + 1 == tiles) tc_commit(&empty[uv % L::kStages]);
+          if (more) {
+            if (t == 0) wait_full(uk);
+            product_s(t, uk);
+            if (t + 1 == tiles) tc_commit(&empty[uk % L::kStages]);
+          } else {
+            tc_commit(&sfull[t]);
+          }
+        }
+      }
+      // The ring's last tiles: every product is done before the memory is given back.
+      const int last = 2 * n - 1;
+      ok = mbar_wait_bounded(&empty[last % L::kStages], uint32_t(last / L::kStages) & 1u, kWaitLimitCycles) && ok;
+    }
+    __syncwarp();
+  }
+  if (!ok) atomicOr(&g_prefix_tc_flags, kFlagWaitRanOut);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(kTmemCols) : "memory");
+  }
+}
+
+template <typename H, int DP>
+cudaError_t launch_one(const PrefixArgs& p, unsigned items, cudaStream_t stream) {
+  auto kern = prefix_tc_kernel<H, DP>;
+  static PerDeviceCache attr_set, regs;
+  cudaError_t e = set_max_dynamic_smem_once(kern, int(Layout<DP>::kBytes), attr_set);
+  if (e != cudaSuccess) return e;
+  // The register split above only adds up for exactly this launch size.
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int r = regs.get(dev, [&] {
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kern);
+    return e == cudaSuccess ? attr.numRegs : -1;
+  });
+  if (e != cudaSuccess) return e;
+  if (r != kLaunchRegs) return cudaErrorInvalidKernelImage;
+  return launch_k(kern, dim3(items), dim3(kTcThreads), Layout<DP>::kBytes, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_tc(const PrefixArgs& p, nf4_dtype dtype, unsigned items, cudaStream_t stream) {
+  if (dtype == NF4_BF16) return p.dim <= 64 ? launch_one<Bf16, 64>(p, items, stream) : launch_one<Bf16, 128>(p, items, stream);
+  return p.dim <= 64 ? launch_one<Fp16, 64>(p, items, stream) : launch_one<Fp16, 128>(p, items, stream);
+}
+
+cudaError_t read_and_clear_prefix_tc_flags(unsigned int* flags) {
+  const unsigned int zero = 0;
+  const cudaError_t e = cudaMemcpyFromSymbol(flags, g_prefix_tc_flags, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_prefix_tc_flags, &zero, sizeof(unsigned int));
+}
+
+}  // namespace nf4

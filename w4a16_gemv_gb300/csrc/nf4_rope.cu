@@ -13,9 +13,11 @@
 // chunks otherwise), one lane per unit, so that a row's norm is a butterfly
 // over the 2^k lanes that share it and both elements of a pair are in one
 // lane's registers: no shared memory, and an output may be its input. A warp
-// takes one token: its table row and weights are loaded into registers once
-// and serve all the heads that the warp walks over, four row groups in flight
-// at a time.
+// takes one token: the weights times the token's cosines and sines are formed
+// once and serve all the heads that the warp walks over (two multiplications
+// and additions per element, packed two to an instruction), and a row group's
+// registers are loaded again as soon as they are stored, so that four groups
+// stay in flight.
 #include <math.h>
 
 #include <initializer_list>
@@ -85,22 +87,39 @@ struct RopeArgs {
   int per_warp, parts;        // groups a warp walks over; warps per token
 };
 
-template <typename T>
-struct Elem;  // a 16-byte chunk as binary32 values and back
+// Two 16-byte chunks as P pairs (a_i, b_i) of binary32 and back: in the half
+// layout a comes from the first chunk and b from the second, in the
+// interleaved layout they alternate.
 template <typename H>
 struct Elem16 {
   static constexpr int kSize = 2, kPer = 8;
-  static __device__ __forceinline__ void up(const uint4& v, float* f) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  template <bool kInterleaved>
+  static __device__ __forceinline__ void up(const uint4& x0, const uint4& x1, float (&a)[8], float (&b)[8]) {
+    const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const float2 p = H::up2(w[i]);
-      f[2 * i] = p.x;
-      f[2 * i + 1] = p.y;
+      if (kInterleaved) {
+        a[i] = p.x;
+        b[i] = p.y;
+      } else {
+        (i < 4 ? a : b)[2 * (i & 3)] = p.x;
+        (i < 4 ? a : b)[2 * (i & 3) + 1] = p.y;
+      }
     }
   }
-  static __device__ __forceinline__ uint4 down(const float* f) {
-    return make_uint4(H::down2(f[0], f[1]), H::down2(f[2], f[3]), H::down2(f[4], f[5]), H::down2(f[6], f[7]));
+  template <bool kInterleaved>
+  static __device__ __forceinline__ void down(const float (&a)[8], const float (&b)[8], uint4& x0, uint4& x1) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (kInterleaved)
+        w[i] = H::down2(a[i], b[i]);
+      else
+        w[i] = i < 4 ? H::down2(a[2 * i], a[2 * i + 1]) : H::down2(b[2 * (i - 4)], b[2 * (i - 4) + 1]);
+    }
+    x0 = make_uint4(w[0], w[1], w[2], w[3]);
+    x1 = make_uint4(w[4], w[5], w[6], w[7]);
   }
   static __device__ __forceinline__ float load(const char* p) {
     return H::up2(*reinterpret_cast<const uint16_t*>(p)).x;
@@ -109,6 +128,8 @@ struct Elem16 {
     *reinterpret_cast<uint16_t*>(p) = uint16_t(H::down2(v, v) & 0xffffu);
   }
 };
+template <typename T>
+struct Elem;
 template <>
 struct Elem<Bf16> : Elem16<Bf16> {};
 template <>
@@ -116,18 +137,51 @@ struct Elem<Fp16> : Elem16<Fp16> {};
 template <>
 struct Elem<float> {
   static constexpr int kSize = 4, kPer = 4;
-  static __device__ __forceinline__ void up(const uint4& v, float* f) {
-    f[0] = __uint_as_float(v.x);
-    f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z);
-    f[3] = __uint_as_float(v.w);
+  template <bool kInterleaved>
+  static __device__ __forceinline__ void up(const uint4& x0, const uint4& x1, float (&a)[4], float (&b)[4]) {
+    const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = __uint_as_float(w[kInterleaved ? 2 * i : i]);
+      b[i] = __uint_as_float(w[kInterleaved ? 2 * i + 1 : i + 4]);
+    }
   }
-  static __device__ __forceinline__ uint4 down(const float* f) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  template <bool kInterleaved>
+  static __device__ __forceinline__ void down(const float (&a)[4], const float (&b)[4], uint4& x0, uint4& x1) {
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[kInterleaved ? 2 * i : i] = a[i];
+      w[kInterleaved ? 2 * i + 1 : i + 4] = b[i];
+    }
+    x0 = make_uint4(__float_as_uint(w[0]), __float_as_uint(w[1]), __float_as_uint(w[2]), __float_as_uint(w[3]));
+    x1 = make_uint4(__float_as_uint(w[4]), __float_as_uint(w[5]), __float_as_uint(w[6]), __float_as_uint(w[7]));
   }
   static __device__ __forceinline__ float load(const char* p) { return *reinterpret_cast<const float*>(p); }
   static __device__ __forceinline__ void store(char* p, float v) { *reinterpret_cast<float*>(p) = v; }
 };
+
+// Two binary32 operations in one instruction, each rounded to nearest even.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
 // Where a token's key and value go: the first byte of (slot, head 0) of each
 // cache. False: nowhere (a negative slot, or one past the cache, which is
@@ -151,11 +205,15 @@ __device__ __forceinline__ bool slot_base(const RopeArgs& a, int64_t slot, int s
   return true;
 }
 
-constexpr int kRopeThreads = 256;
-constexpr int kInFlight = 4;  // row groups whose loads are issued together
+constexpr int kRopeThreads = 128;
+constexpr int kInFlight = 4;  // row groups in flight per warp
+#ifndef KMAXPER
+#define KMAXPER 16
+#endif
+constexpr int kMaxPerWarp = KMAXPER;
 
-template <typename T>
-__global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_constant__ RopeArgs a) {
+template <typename T, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_rows_kernel(const __grid_constant__ RopeArgs a) {
   using E = Elem<T>;
   constexpr int P = E::kPer;  // elements per chunk = pairs per unit
   pdl_allow_dependents();
@@ -171,40 +229,50 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
   const int rot_units = a.rot / (2 * P);
   const bool active = unit < a.dim / (2 * P);
   const bool turned = unit < rot_units;
-  int c0, c1;  // the unit's chunks
-  if (turned && !a.interleaved) {
-    c0 = unit;
-    c1 = unit + rot_units;
+  int c0, c1;  // byte offsets of the unit's chunks
+  if (turned && !kInterleaved) {
+    c0 = 16 * unit;
+    c1 = c0 + 16 * rot_units;
   } else {
-    c0 = 2 * unit;
-    c1 = c0 + 1;
+    c0 = 32 * unit;
+    c1 = c0 + 16;
   }
-  const int g0 = part * a.per_warp;
-  const int g1 = min(g0 + a.per_warp, a.gq + a.gk + a.gv);
+  // this warp's row groups: q's, then k's, then v's
+  const int g = part * a.per_warp;
+  const int g_end = min(g + a.per_warp, a.gq + a.gk + a.gv);
 
-  // the row of group g that this lane works on: 0 q, 1 k, 2 v, and its head (-1: none)
-  auto row_of = [&](int g, int* head) {
-    const int kind = g < a.gq ? 0 : g < a.gq + a.gk ? 1 : 2;
-    const int h = (g - (kind == 0 ? 0 : kind == 1 ? a.gq : a.gq + a.gk)) * rows + sub;
-    const int n = kind == 0 ? a.q.heads : kind == 1 ? a.k.heads : a.v.heads;
-    *head = (g < g1 && active && h < n) ? h : -1;
-    return kind;
+  // the groups of one kind (0 q, 1 k, 2 v) that this warp has: [from, to) of the kind's own
+  struct Part {
+    const char* src;
+    int64_t step;
+    int from, to, heads;
   };
-  auto load = [&](int g, uint4& x0, uint4& x1) {
-    int h;
-    const int kind = row_of(g, &h);
-    x0 = x1 = make_uint4(0u, 0u, 0u, 0u);
-    if (h < 0) return;
+  auto part_of = [&](int kind) {
     const RowSet& r = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-    const char* p = r.in + (int64_t(t) * r.in_ts + int64_t(h) * r.in_hs) * E::kSize;
-    x0 = *reinterpret_cast<const uint4*>(p + c0 * 16);
-    x1 = *reinterpret_cast<const uint4*>(p + c1 * 16);
+    const int first = kind == 0 ? 0 : kind == 1 ? a.gq : a.gq + a.gk;
+    const int n = kind == 0 ? a.gq : kind == 1 ? a.gk : a.gv;
+    return Part{r.in + int64_t(t) * r.in_ts * E::kSize, r.in_hs * E::kSize, max(g - first, 0), min(g_end - first, n),
+                r.heads};
   };
-
   uint4 x[kInFlight][2];
+  auto load = [&](const Part& s, int gi, uint4 (&v)[2]) {
+    const int h = gi * rows + sub;
+    v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (gi < s.to && active && h < s.heads) {
+      const char* p = s.src + int64_t(h) * s.step;
+      v[0] = *reinterpret_cast<const uint4*>(p + c0);
+      v[1] = *reinterpret_cast<const uint4*>(p + c1);
+    }
+  };
+  // the first rows are on their way before the position and its table row are asked for
+  const int kind0 = g < a.gq ? 0 : g < a.gq + a.gk ? 1 : 2;
+  {
+    const Part s = part_of(kind0);
 #pragma unroll
-  for (int u = 0; u < kInFlight; ++u) load(g0 + u, x[u][0], x[u][1]);
-  // the token's table row and place in the cache, and the weights
+    for (int u = 0; u < kInFlight; ++u) load(s, s.from + u, x[u]);
+  }
+
+  const int64_t slot = a.slots ? a.slots[t] : 0;
   float cosv[P], sinv[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
@@ -214,8 +282,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
   if (a.rot > 0) {
     const int64_t pos = a.positions[t];
     const bool good = pos >= 0 && pos < a.max_positions;
-    if (!good && lane == 0) atomicOr(&g_rope_flags, kFlagBadIndex);
     if (!good) {  // NaN in every element of the token's rows, turned or not
+      if (lane == 0) atomicOr(&g_rope_flags, kFlagBadIndex);
 #pragma unroll
       for (int i = 0; i < P; ++i) cosv[i] = sinv[i] = __uint_as_float(0x7fc00000u);
     } else if (turned) {
@@ -232,87 +300,98 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
   }
   char *kdst = nullptr, *vdst = nullptr;
   bool stored = true;
-  if (a.slots) stored = slot_base(a, a.slots[t], E::kSize, &kdst, &vdst);
-  uint4 wq[2], wk[2];
-  wq[0] = wq[1] = wk[0] = wk[1] = make_uint4(0u, 0u, 0u, 0u);
-  if (active) {
-    if (a.qw) {
-      wq[0] = __ldg(reinterpret_cast<const uint4*>(a.qw) + c0);
-      wq[1] = __ldg(reinterpret_cast<const uint4*>(a.qw) + c1);
-    }
-    if (a.kw) {
-      wk[0] = __ldg(reinterpret_cast<const uint4*>(a.kw) + c0);
-      wk[1] = __ldg(reinterpret_cast<const uint4*>(a.kw) + c1);
-    }
-  }
+  if (a.slots) stored = slot_base(a, slot, E::kSize, &kdst, &vdst);
 
-  for (int g = g0; g < g1; g += kInFlight) {
-    if (g > g0) {
+  // One kind of rows at a time: `kind` is the same for the whole warp.
+  for (int kind = kind0; kind < 3; ++kind) {
+    const Part s = part_of(kind);
+    if (s.from >= s.to || (kind > 0 && !stored)) continue;
+    if (kind != kind0) {
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u) load(g + u, x[u][0], x[u][1]);
+      for (int u = 0; u < kInFlight; ++u) load(s, s.from + u, x[u]);
     }
+    char* dst = kind == 0   ? a.q.out + int64_t(t) * a.q.out_ts * E::kSize
+                : !a.slots  ? a.k.out + int64_t(t) * a.k.out_ts * E::kSize
+                : kind == 1 ? kdst
+                            : vdst;
+    const int64_t out_step = (kind == 0 ? a.q.out_hs : kind == 1 ? a.k.out_hs : a.v.out_hs) * E::kSize;
+
+    // weight times cosine and sine: a' = a (wa c) - b (wb s), b' = b (wb c) + a (wa s)
+    const char* wt = reinterpret_cast<const char*>(kind == 0 ? a.qw : kind == 1 ? a.kw : nullptr);
+    uint64_t ac[P / 2], bs[P / 2], bc[P / 2], as[P / 2];
+    {
+      float wa[P], wb[P];
+      if (wt && active) {
+        E::template up<kInterleaved>(__ldg(reinterpret_cast<const uint4*>(wt + c0)),
+                                     __ldg(reinterpret_cast<const uint4*>(wt + c1)), wa, wb);
+      } else {
 #pragma unroll
-    for (int u = 0; u < kInFlight; ++u) {
-      int h;
-      const int kind = row_of(g + u, &h);
-      uint4 y0 = x[u][0], y1 = x[u][1];
-      if (kind < 2) {
-        float f0[P], f1[P];
-        E::up(y0, f0);
-        E::up(y1, f1);
-        if (kind == 0 ? a.qw != nullptr : a.kw != nullptr) {  // the same for the whole warp
-          float ss = 0.0f;
+        for (int i = 0; i < P; ++i) wa[i] = wb[i] = 1.0f;
+      }
 #pragma unroll
-          for (int i = 0; i < P; ++i) ss = fmaf(f0[i], f0[i], fmaf(f1[i], f1[i], ss));
-          for (int m = 1 << a.lane_bits >> 1; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-          const float inv = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
-          float w0[P], w1[P];
-          E::up(kind == 0 ? wq[0] : wk[0], w0);
-          E::up(kind == 0 ? wq[1] : wk[1], w1);
+      for (int i = 0; i < P / 2; ++i) {
+        const uint64_t c = pack2(cosv[2 * i], cosv[2 * i + 1]), s = pack2(sinv[2 * i], sinv[2 * i + 1]);
+        const uint64_t va = pack2(wa[2 * i], wa[2 * i + 1]), vb = pack2(wb[2 * i], wb[2 * i + 1]);
+        ac[i] = mul2(va, c);
+        bc[i] = mul2(vb, c);
+        as[i] = mul2(va, s);
+        bs[i] = mul2(vb, pack2(-sinv[2 * i], -sinv[2 * i + 1]));
+      }
+    }
+
+    for (int base = s.from; base < s.to; base += kInFlight) {
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            f0[i] = f0[i] * inv * w0[i];
-            f1[i] = f1[i] * inv * w1[i];
-          }
-        }
-        if (turned && a.interleaved) {
-          // pairs (f0[0], f0[1]), ... then (f1[0], f1[1]), ...
+      for (int u = 0; u < kInFlight; ++u) {
+        const int gi = base + u;
+        if (gi >= s.to) break;
+        uint4 y0 = x[u][0], y1 = x[u][1];
+        load(s, gi + kInFlight, x[u]);
+        if (kind < 2) {
+          float fa[P], fb[P];
+          E::template up<kInterleaved>(y0, y1, fa, fb);
+          uint64_t pa[P / 2], pb[P / 2];
 #pragma unroll
           for (int i = 0; i < P / 2; ++i) {
-            const float p = f0[2 * i], r = f0[2 * i + 1];
-            f0[2 * i] = p * cosv[i] - r * sinv[i];
-            f0[2 * i + 1] = r * cosv[i] + p * sinv[i];
-            const float p1 = f1[2 * i], r1 = f1[2 * i + 1];
-            f1[2 * i] = p1 * cosv[P / 2 + i] - r1 * sinv[P / 2 + i];
-            f1[2 * i + 1] = r1 * cosv[P / 2 + i] + p1 * sinv[P / 2 + i];
+            pa[i] = pack2(fa[2 * i], fa[2 * i + 1]);
+            pb[i] = pack2(fb[2 * i], fb[2 * i + 1]);
           }
-        } else {
-          // the pairs (f0[i], f1[i]); for a unit that is not turned (1, 0), or NaN
+          float inv = 1.0f;
+          if (wt) {
+            uint64_t sq = mul2(pa[0], pa[0]);
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const float p = f0[i], r = f1[i];
-            f0[i] = p * cosv[i];
-            f1[i] = r * cosv[i];
-            if (turned) {
-              f0[i] -= r * sinv[i];
-              f1[i] += p * sinv[i];
-            }
+            for (int i = 1; i < P / 2; ++i) sq = fma2(pa[i], pa[i], sq);
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) sq = fma2(pb[i], pb[i], sq);
+            const float2 two = unpack2(sq);
+            float ss = two.x + two.y;
+            for (int m = 1 << a.lane_bits >> 1; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+            inv = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
           }
+          const uint64_t inv2 = pack2(inv, inv);
+#pragma unroll
+          for (int i = 0; i < P / 2; ++i) {
+            uint64_t ya = mul2(pa[i], ac[i]), yb = mul2(pb[i], bc[i]);
+            if (turned) {
+              ya = fma2(pb[i], bs[i], ya);
+              yb = fma2(pa[i], as[i], yb);
+            }
+            if (wt) {
+              ya = mul2(ya, inv2);
+              yb = mul2(yb, inv2);
+            }
+            const float2 u2 = unpack2(ya), v2 = unpack2(yb);
+            fa[2 * i] = u2.x;
+            fa[2 * i + 1] = u2.y;
+            fb[2 * i] = v2.x;
+            fb[2 * i + 1] = v2.y;
+          }
+          E::template down<kInterleaved>(fa, fb, y0, y1);
         }
-        y0 = E::down(f0);
-        y1 = E::down(f1);
-      }
-      if (h >= 0) {
-        char* p;
-        if (kind == 0)
-          p = a.q.out + (int64_t(t) * a.q.out_ts + int64_t(h) * a.q.out_hs) * E::kSize;
-        else if (!a.slots)
-          p = a.k.out + (int64_t(t) * a.k.out_ts + int64_t(h) * a.k.out_hs) * E::kSize;
-        else
-          p = kind == 1 ? kdst + int64_t(h) * a.k.out_hs * E::kSize : vdst + int64_t(h) * a.v.out_hs * E::kSize;
-        if (kind == 0 || stored) {
-          *reinterpret_cast<uint4*>(p + c0 * 16) = y0;
-          *reinterpret_cast<uint4*>(p + c1 * 16) = y1;
+        const int h = gi * rows + sub;
+        if (active && h < s.heads) {
+          char* p = dst + int64_t(h) * out_step;
+          *reinterpret_cast<uint4*>(p + c0) = y0;
+          *reinterpret_cast<uint4*>(p + c1) = y1;
         }
       }
     }
@@ -414,13 +493,14 @@ cudaError_t launch_rows(RopeArgs& a, cudaStream_t stream) {
   // more when there is plenty, so that a warp's table row and weights serve
   // several groups.
   const int groups = a.gq + a.gk + a.gv;
-  int64_t per = int64_t(a.tokens) * groups / (152 * 64);
-  per = per < 1 ? 1 : per > 16 ? 16 : per;
+  int64_t per = int64_t(a.tokens) * groups / (152 * 16);
+  per = per < 1 ? 1 : per > kMaxPerWarp ? kMaxPerWarp : per;
   a.parts = int((groups + per - 1) / per);
   a.per_warp = (groups + a.parts - 1) / a.parts;
   const int64_t blocks = (int64_t(a.tokens) * a.parts + per_block - 1) / per_block;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  return launch_k(rope_rows_kernel<T>, dim3(unsigned(blocks)), dim3(kRopeThreads), 0, stream, a);
+  return launch_k(a.interleaved ? rope_rows_kernel<T, true> : rope_rows_kernel<T, false>, dim3(unsigned(blocks)),
+                  dim3(kRopeThreads), 0, stream, a);
 }
 
 }  // namespace
