@@ -17,10 +17,20 @@ namespace {
 
 __device__ unsigned int g_prefix_flags = 0;
 
-constexpr int kThreads = 128;
-constexpr int kWarps = 4;
-constexpr int kKeys = 64;    // keys per stage
-constexpr int kStages = 3;
+constexpr int kUnit = 64;    // granularity of the plan's ranges of keys
+constexpr int kStages = 2;
+
+// Tiles of 64 rows: four warps with 16 rows each and all keys of a stage of
+// 64. Tiles of 16 rows: two warps that share the rows and have half the keys of
+// a stage of 32 each; small CTAs (48 KB at 128 elements), so that four are on an SM
+// and the start of one (three dependent loads before its first keys) hides
+// behind the keys of the others.
+template <int R>
+struct Shape {
+  static constexpr int kWarps = R == 64 ? 4 : 2;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kKeys = R == 64 ? 64 : 32;  // keys per stage
+};
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -48,11 +58,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// One item with tiles of R rows. R = 64: a warp has 16 rows and all keys of a
-// stage; R = 16: the warps share the rows and a stage's keys are split among
-// them, joined through shared memory at the end.
+// One item with tiles of R rows. The warps' key shares of R = 16 are joined
+// through shared memory at the end.
 template <typename H, int DP, int R>
 __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it, unsigned char* smem) {
+  constexpr int kWarps = Shape<R>::kWarps, kThreads = Shape<R>::kThreads, kKeys = Shape<R>::kKeys;
   constexpr int KW = R == 64 ? kKeys : kKeys / kWarps;  // keys of a stage per warp
   constexpr int NB = KW / 8;                            // score blocks of 8 keys
   constexpr int CPR = DP / 8;                           // 16-byte chunks per row
@@ -310,60 +320,91 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
   }
 }
 
-// `beside`: the launch before this one is the tensor-core items of the same
-// call, which this one does not depend on. Its CTAs all waited for the grids
-// before it ahead of letting this one start, so there is nothing to wait for
-// here; but what follows (the join) only waits for this launch, so its last
-// CTA ends after the other launch did.
-template <typename H, int DP>
-__global__ void __launch_bounds__(kThreads) prefix_mma_kernel(const __grid_constant__ PrefixArgs a) {
+// `beside`: the launch before this one is other items of the same call, which
+// this one does not depend on. Its CTAs all waited for the grids before it
+// ahead of letting this one start, so there is nothing to wait for here; but
+// what follows (the join) only waits for this launch, so its last CTA ends
+// after the other launch did.
+template <typename H, int DP, int R>
+__global__ void __launch_bounds__(Shape<R>::kThreads) prefix_mma_kernel(const __grid_constant__ PrefixArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
-  pdl_allow_dependents();
   if (!a.beside) pdl_wait_prior_grid();
+  pdl_allow_dependents();
   const PrefixItem it = prefix_item(a, int64_t(a.first) + blockIdx.x, &g_prefix_flags);
-  if (it.rows > 0) {
-    if (it.own ? a.suffix_rows == 64 : a.prefix_rows == 64)
-      attend<H, DP, 64>(a, it, smem);
-    else
-      attend<H, DP, 16>(a, it, smem);
-  }
+  if (it.rows > 0) attend<H, DP, R>(a, it, smem);
   if (a.beside && blockIdx.x + 1 == gridDim.x) pdl_wait_prior_grid();
 }
 
-// Joins a row's partial results: one warp per row, four elements per lane.
-template <typename H>
-__global__ void __launch_bounds__(128) prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
+// Joins a row's partial results: 1 to 8 warps per row (the more ranges, the
+// more), four elements per lane, kBatch ranges in flight per warp. The partial
+// outputs are asked for together with the maxima and sums, not after them
+// (those of ranges that hold nothing are read and dropped): one latency, which
+// is most of this kernel's time. The order of the sums depends on the plan
+// alone.
+constexpr int kJoinWarps = 8;
+template <typename H, int kBatch>
+__global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __grid_constant__ PrefixArgs a, int per_row) {
+  __shared__ float4 sv[kJoinWarps][32];
+  __shared__ float sl[kJoinWarps];
   pdl_allow_dependents();
-  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = int64_t(blockIdx.x) * (kJoinWarps / per_row) + warp / per_row;
+  const int share = warp % per_row;
   const int64_t rows = int64_t(a.tokens) * a.q_heads;
-  pdl_wait_prior_grid();
-  if (row >= rows) return;
-  const int t = int(row / a.q_heads);
-  int n = a.splits;
-  if (a.cu_q && a.suffix_splits > 0 && (t < a.cu_q[0] || t >= a.cu_q[a.batch])) n = a.prefix_splits;
-  const float2* ml = a.ml + row * a.splits;
-  float m = -INFINITY;
-  for (int s = lane; s < n; s += 32) m = fmaxf(m, ml[s].x);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const bool there = row < rows;
+  const int t = there ? int(row / a.q_heads) : 0;
   const bool mine = lane * 4 < a.dim;
-  const float* src = a.part + row * a.dim + lane * 4;
-  float l = 0.0f;
+  pdl_wait_prior_grid();
+  float l = 0.0f, m = -INFINITY;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < n; ++s) {
-    const float2 x = ml[s];
-    if (x.x == -INFINITY && x.y == 0.0f) continue;  // a range that the row does not see
-    const float f = x.x == -INFINITY ? 1.0f : ex2(x.x - m);
-    l = fmaf(x.y, f, l);
-    if (mine) {
-      const float4 y = *reinterpret_cast<const float4*>(src + int64_t(s) * rows * a.dim);
-      v.x = fmaf(y.x, f, v.x);
-      v.y = fmaf(y.y, f, v.y);
-      v.z = fmaf(y.z, f, v.z);
-      v.w = fmaf(y.w, f, v.w);
+  if (there) {
+    int n = a.splits;
+    const float2* ml = a.ml + row * a.splits;
+    const float* src = a.part + row * a.dim + lane * 4;
+    const int64_t step = rows * a.dim;
+    float4 y[kBatch];
+    auto load = [&](int s0) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        y[u] = mine && s0 + u < n ? *reinterpret_cast<const float4*>(src + (s0 + u) * step)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(share * kBatch);
+    if (a.cu_q && a.suffix_splits > 0 && (t < a.cu_q[0] || t >= a.cu_q[a.batch])) n = a.prefix_splits;
+    for (int s = lane; s < n; s += 32) m = fmaxf(m, ml[s].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    for (int s0 = share * kBatch; s0 < n; s0 += per_row * kBatch) {
+      if (s0 > share * kBatch) load(s0);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const float2 x = s0 + u < n ? ml[s0 + u] : make_float2(-INFINITY, 0.0f);
+        // a range that holds nothing has no partial output to speak of
+        if (x.x == -INFINITY && x.y == 0.0f) continue;
+        const float w = x.x == -INFINITY ? 1.0f : ex2(x.x - m);
+        l = fmaf(x.y, w, l);
+        v.x = fmaf(y[u].x, w, v.x);
+        v.y = fmaf(y[u].y, w, v.y);
+        v.z = fmaf(y[u].z, w, v.z);
+        v.w = fmaf(y[u].w, w, v.w);
+      }
     }
   }
+  if (per_row > 1) {
+    sv[warp][lane] = v;
+    if (lane == 0) sl[warp] = l;
+    __syncthreads();
+    if (share != 0) return;
+    for (int s = 1; s < per_row; ++s) {
+      const float4 y = sv[warp + s][lane];
+      v.x += y.x;
+      v.y += y.y;
+      v.z += y.z;
+      v.w += y.w;
+      l += sl[warp + s];
+    }
+  }
+  if (!there) return;
   const bool any = l > 0.0f || l != l;
   const float inv = any ? 1.0f / l : 0.0f;
   if (mine) {
@@ -388,36 +429,52 @@ __global__ void __launch_bounds__(128) prefix_empty_kernel(const __grid_constant
   if (lane == 0 && a.lse) a.lse[row] = -INFINITY;
 }
 
-template <typename H, int DP>
+template <typename H, int DP, int R>
 cudaError_t launch_mma(const PrefixArgs& p, unsigned items, cudaStream_t stream) {
-  auto kern = prefix_mma_kernel<H, DP>;
-  constexpr int smem = kStages * 2 * kKeys * DP * 2;
+  auto kern = prefix_mma_kernel<H, DP, R>;
+  constexpr int smem = kStages * 2 * Shape<R>::kKeys * DP * 2;
   static PerDeviceCache attr_set;
   const cudaError_t e = set_max_dynamic_smem_once(kern, smem, attr_set);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, dim3(items), dim3(kThreads), smem, stream, p);
+  return launch_k(kern, dim3(items), dim3(Shape<R>::kThreads), smem, stream, p);
+}
+
+template <typename H>
+cudaError_t launch_rows(const PrefixArgs& p, int rows, unsigned items, cudaStream_t stream) {
+  if (rows == 64) return p.dim <= 64 ? launch_mma<H, 64, 64>(p, items, stream) : launch_mma<H, 128, 64>(p, items, stream);
+  return p.dim <= 64 ? launch_mma<H, 64, 16>(p, items, stream) : launch_mma<H, 128, 16>(p, items, stream);
 }
 
 template <typename H>
 cudaError_t launch_typed(const PrefixArgs& p, cudaStream_t stream) {
   const int64_t rows = int64_t(p.tokens) * p.q_heads;
-  const unsigned row_blocks = unsigned((rows + 3) / 4);
-  if (p.splits == 0) return launch_k(prefix_empty_kernel<H>, dim3(row_blocks), dim3(128), 0, stream, p);
+  if (p.splits == 0)
+    return launch_k(prefix_empty_kernel<H>, dim3(unsigned((rows + 3) / 4)), dim3(128), 0, stream, p);
   const int64_t prefix_items = int64_t(p.prefix_tiles) * p.prefix_splits * p.k_heads;
   const int64_t suffix_items = int64_t(p.suffix_tiles) * p.suffix_splits * p.k_heads;
   if (prefix_items + suffix_items > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  const int64_t on_tc = (p.tc_prefix ? prefix_items : 0) + (p.tc_suffix ? suffix_items : 0);
+  // Prefix items, then suffix items; one launch where both take the same kernel.
+  const int64_t counts[2] = {prefix_items, suffix_items};
+  const int tile_rows[2] = {p.prefix_rows, p.suffix_rows};
+  int64_t first = 0;
   cudaError_t e = cudaSuccess;
-  if (on_tc > 0) e = launch_prefix_tc(p, H::kDtype, unsigned(on_tc), stream);
-  const int64_t rest = prefix_items + suffix_items - on_tc;
-  if (e == cudaSuccess && rest > 0) {
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+    int64_t items = counts[i];
+    const int tile = tile_rows[i];
+    if (i == 0 && tile == tile_rows[1]) items += counts[1];
+    if (items == 0 || first == prefix_items + suffix_items) continue;
     PrefixArgs q = p;
-    q.first = int(on_tc);
-    q.beside = on_tc > 0;
-    e = p.dim <= 64 ? launch_mma<H, 64>(q, unsigned(rest), stream) : launch_mma<H, 128>(q, unsigned(rest), stream);
+    q.first = int(first);
+    q.beside = first > 0;
+    e = tile == 256 ? launch_prefix_tc(q, H::kDtype, unsigned(items), stream)
+                    : launch_rows<H>(q, tile, unsigned(items), stream);
+    first += items;
   }
   if (e != cudaSuccess || p.direct) return e;
-  return launch_k(prefix_join_kernel<H>, dim3(row_blocks), dim3(128), 0, stream, p);
+  const int per_row = p.splits <= 8 ? 1 : p.splits <= 16 ? 2 : p.splits <= 32 ? 4 : 8;
+  const int64_t blocks = (rows * per_row + kJoinWarps - 1) / kJoinWarps;
+  return launch_k(p.splits <= 4 ? prefix_join_kernel<H, 4> : prefix_join_kernel<H, 8>, dim3(unsigned(blocks)),
+                  dim3(32 * kJoinWarps), 0, stream, p, per_row);
 }
 
 }  // namespace
@@ -425,10 +482,7 @@ cudaError_t launch_typed(const PrefixArgs& p, cudaStream_t stream) {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kMaxRanges = 64;  // per row, of the shared and of the own keys each
-#ifndef TCROWS
-#define TCROWS 32
-#endif
+constexpr int kMaxRanges = 152;  // per row, of the shared and of the own keys each
 
 // Keys per range of the mma kernel, in stages of 64: at least two stages,
 // about eight items per SM, at most kMaxRanges ranges.
@@ -472,27 +526,23 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
   p->prefix_len = int(a.prefix_len);
   p->suffix_max = a.batch > 0 ? int(a.suffix_pages_width * a.page_size) : 0;
   const int64_t rows = a.tokens * p->group;  // of a key/value head
-  // Many rows go to the tensor cores. (Suffix items only when the prefix's do,
-  // so that the items of each kernel are one range.)
-  p->tc_prefix = rows > TCROWS && p->prefix_len > 0;
-  p->tc_suffix = rows > 64 * a.batch && (p->tc_prefix || p->prefix_len == 0);
-  p->prefix_rows = p->tc_prefix ? 256 : rows > 32 ? 64 : 16;
-  p->suffix_rows = p->tc_suffix ? 256 : rows > 32 * a.batch ? 64 : 16;
+  p->prefix_rows = rows > 32 ? 256 : rows > 32 ? 64 : 16;
+  p->suffix_rows = rows > 64 * a.batch ? 256 : rows > 32 * a.batch ? 64 : 16;
   p->prefix_tiles = int((rows + p->prefix_rows - 1) / p->prefix_rows);
   // sum over sequences of ceil(rows / suffix_rows) is below both bounds
   const int64_t whole = rows / p->suffix_rows + a.batch;
   p->suffix_tiles = int(whole < rows ? whole : rows);
-  const int64_t pk = (int64_t(p->prefix_len) + kKeys - 1) / kKeys, sk = (int64_t(p->suffix_max) + kKeys - 1) / kKeys;
+  const int64_t pk = (int64_t(p->prefix_len) + kUnit - 1) / kUnit, sk = (int64_t(p->suffix_max) + kUnit - 1) / kUnit;
   if (pk > 0) {
-    const int64_t per = p->tc_prefix ? tc_range(int64_t(p->prefix_tiles) * p->k_heads, (pk + 1) / 2, rows * p->k_heads)
+    const int64_t per = p->prefix_rows == 256 ? tc_range(int64_t(p->prefix_tiles) * p->k_heads, (pk + 1) / 2, rows * p->k_heads)
                                      : mma_range(int64_t(p->prefix_tiles) * p->k_heads, pk);
-    p->prefix_chunk = int(per * kKeys);
+    p->prefix_chunk = int(per * kUnit);
     p->prefix_splits = int((pk + per - 1) / per);
   }
   if (sk > 0) {
-    const int64_t per = p->tc_suffix ? tc_range(int64_t(p->suffix_tiles) * p->k_heads, (sk + 1) / 2, rows * p->k_heads)
+    const int64_t per = p->suffix_rows == 256 ? tc_range(int64_t(p->suffix_tiles) * p->k_heads, (sk + 1) / 2, rows * p->k_heads)
                                      : mma_range(int64_t(p->suffix_tiles) * p->k_heads, sk);
-    p->suffix_chunk = int(per * kKeys);
+    p->suffix_chunk = int(per * kUnit);
     p->suffix_splits = int((sk + per - 1) / per);
   }
   if (rows == 0) p->prefix_splits = p->suffix_splits = 0;

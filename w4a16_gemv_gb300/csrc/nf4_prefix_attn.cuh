@@ -30,15 +30,14 @@ struct PrefixArgs {
   int page_size, page_shift, num_pages;            // page_shift: log2 of page_size, or -1
   float scale_log2;                                // scale * log2(e)
   // plan
-  int prefix_rows, suffix_rows;                    // rows per tile
+  int prefix_rows, suffix_rows;                    // rows per tile: 16, 64 or 256
   int prefix_tiles, suffix_tiles;                  // tiles of a key/value head (suffix: an upper bound)
   int prefix_splits, suffix_splits;                // ranges of keys, of this many each:
   int prefix_chunk, suffix_chunk;
   int splits;                                      // prefix_splits + suffix_splits
   int direct;                                      // 1: one range of shared keys is all; its items write the output
-  int tc_prefix, tc_suffix;                        // which items run on the tensor-core kernel
   int first;                                       // first item of the launch
-  int beside;                                      // 1: runs beside the launch before it (see prefix_mma_kernel)
+  int beside;                                      // 1: runs beside the launch before it of the same call
   float* part;                                     // [splits][tokens * q_heads][dim]
   float2* ml;                                      // [tokens * q_heads][splits]: (maximum, sum)
 };
@@ -46,7 +45,8 @@ struct PrefixArgs {
 // The sizes and the plan of a call, and the bytes of its workspace.
 void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, size_t* bytes);
 
-// Items [0, items) on the tensor cores (nf4_prefix_attn_tc.cu).
+// Items [p.first, p.first + items), tiles of 256 rows, on the tensor cores
+// (nf4_prefix_attn_tc.cu).
 cudaError_t launch_prefix_tc(const PrefixArgs& p, nf4_dtype dtype, unsigned items, cudaStream_t stream);
 
 // One work item, the same in every thread.
@@ -105,8 +105,9 @@ __device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, int64_t i
   int before = 0;  // tiles of the sequences before this group of 32
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     const int b = b0 + lane;
-    int lo = 0, hi = 0;
+    int lo = 0, hi = 0, length = 0;
     if (b < a.batch) {
+      length = a.suffix_lens[b];  // with cu_q, not after it: one latency
       lo = a.cu_q ? a.cu_q[b] : b;
       hi = a.cu_q ? a.cu_q[b + 1] : b + 1;
       const int l2 = min(max(lo, 0), a.tokens), h2 = min(max(hi, l2), a.tokens);
@@ -130,7 +131,7 @@ __device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, int64_t i
       it.n = __shfl_sync(0xffffffffu, hi, src) - it.t0;
       it.r0 = (tile - first) * a.suffix_rows;
       it.rows = min(a.suffix_rows, it.n * a.group - it.r0);
-      const int len = a.suffix_lens[seq];
+      const int len = __shfl_sync(0xffffffffu, length, src);
       it.len = min(max(len, 0), a.suffix_max);
       if (it.len != len && lane == 0) atomicOr(flags, kFlagBadIndex);
       it.pages = a.suffix_pages + int64_t(seq) * a.suffix_pages_stride;

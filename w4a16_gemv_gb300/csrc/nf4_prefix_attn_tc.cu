@@ -170,12 +170,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
   uint64_t* const empty = full + L::kStages;                            // its products are done
   uint64_t* const sfull = empty + L::kStages;                           // S of a tile complete, O at rest
   uint64_t* const pfull = sfull + 2;                                    // P of a tile written (4 softmax warps)
-  uint32_t* const s_taddr = reinterpret_cast<uint32_t*>(pfull + 2);
+  uint64_t* const qfull = pfull + 2;                                    // Q of a tile in place (4 softmax warps)
+  uint32_t* const s_taddr = reinterpret_cast<uint32_t*>(qfull + 2);
 
   // Everything, the tensor memory included, waits for the previous grid: an
   // allocation held by a grid that waits could starve the one waited for.
-  pdl_wait_prior_grid();
-  const PrefixItem it = prefix_item(a, blockIdx.x, &g_prefix_tc_flags);
+  if (!a.beside) pdl_wait_prior_grid();
+  const PrefixItem it = prefix_item(a, int64_t(a.first) + blockIdx.x, &g_prefix_tc_flags);
   const int n = (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys;  // key tiles
   const bool works = it.rows > 0 && n > 0;                    // the same in the whole CTA
   if (warp == 12 && works) {
@@ -192,32 +193,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 4);
+      mbar_init(&qfull[i], 4);
     }
     fence_mbar_init();
   }
   const int tiles = it.rows > kTileRows ? 2 : 1;
-  // Q: warp w of the softmax warps brings rows 32 w .. 32 w + 31 of the pair of tiles
-  if (warp < 8 && works && (warp >> 2) < tiles) {
-    constexpr int CPR = DP / 8, RPI = 32 / CPR;
-    const int r = warp * 32 + lane;
-    int64_t off = 0;
-    if (r < it.rows) {
-      const int rr = it.r0 + r;
-      off = int64_t(it.t0 + rr / a.group) * a.q_ts + int64_t(it.head * a.group + rr % a.group) * a.q_hs;
-    }
-    const int c = lane % CPR;
-#pragma unroll 4
-    for (int x = 0; x < 32 / RPI; ++x) {
-      const int rl = x * RPI + lane / CPR;
-      const int64_t o = __shfl_sync(0xffffffffu, off, rl);
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (warp * 32 + rl < it.rows && c * 8 < a.dim) v = __ldg(reinterpret_cast<const uint4*>(a.q + o + c * 16));
-      const int row = (warp & 3) * 32 + rl;
-      *reinterpret_cast<uint4*>(smem + (warp >> 2) * L::kTile + (c >> 3) * L::kBlock + row * 128 +
-                                (((c & 7) ^ (row & 7)) << 4)) = v;
-    }
-    fence_async_smem();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -227,6 +207,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
       const RowOut ro = row_out(a, it, it.r0 + r);
       *ro.ml = make_float2(-INFINITY, 0.0f);  // (a plan with one range of keys has no empty range)
     }
+    if (a.beside && blockIdx.x + 1 == gridDim.x) pdl_wait_prior_grid();
     return;
   }
   const uint32_t tbase = *s_taddr;
@@ -239,6 +220,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
     asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int tile = warp >> 2;
     if (tile < tiles) {
+      // Q: each warp brings its 32 rows
+      {
+        constexpr int CPR = DP / 8, RPI = 32 / CPR;
+        const int r = warp * 32 + lane;
+        int64_t off = 0;
+        if (r < it.rows) {
+          const int rr = it.r0 + r;
+          off = int64_t(it.t0 + rr / a.group) * a.q_ts + int64_t(it.head * a.group + rr % a.group) * a.q_hs;
+        }
+        const int c = lane % CPR;
+        uint4 v[32 / RPI];
+#pragma unroll
+        for (int x = 0; x < 32 / RPI; ++x) {
+          const int rl = x * RPI + lane / CPR;
+          const int64_t o = __shfl_sync(0xffffffffu, off, rl);
+          v[x] = make_uint4(0u, 0u, 0u, 0u);
+          if (warp * 32 + rl < it.rows && c * 8 < a.dim) v[x] = __ldg(reinterpret_cast<const uint4*>(a.q + o + c * 16));
+        }
+#pragma unroll
+        for (int x = 0; x < 32 / RPI; ++x) {
+          const int row = (warp & 3) * 32 + x * RPI + lane / CPR;
+          *reinterpret_cast<uint4*>(smem + tile * L::kTile + (c >> 3) * L::kBlock + row * 128 +
+                                    (((c & 7) ^ (row & 7)) << 4)) = v[x];
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qfull[tile]);
+      }
       const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
       const uint32_t s_col = tbase + lanes + uint32_t(tile) * 128u;
       const uint32_t o_col = tbase + lanes + 256u + uint32_t(tile) * 128u;
@@ -323,26 +332,44 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
       const bool mine = r < it.rows;
       const RowOut ro = row_out(a, it, it.r0 + (mine ? r : 0));
       const float bad = ok ? 0.0f : __uint_as_float(0x7fc00000u);
+      // 128 bytes of every row at a time through this warp's part of the Q
+      // tile (its products are done), so that rows leave in whole sectors:
+      // 32 columns of partial results, or 64 of the 16-bit output.
+      unsigned char* const stage = smem + tile * L::kTile + (warp & 3) * 4096;
+      char* const row_dst = a.direct ? ro.out : reinterpret_cast<char*>(ro.part);
+      const int row_bytes = a.dim * (a.direct ? 2 : 4);
 #pragma unroll 1
-      for (int c = 0; c < DP / 32; ++c) {
+      for (int c = 0; c < (a.direct ? DP / 64 : DP / 32); ++c) {
         float o[32];
-        tmem_ld32(o_col + 32u * c, o);
-        tmem_ld_wait(o, 32);
-        if (!mine) continue;
+        uint32_t w[32];
         if (!a.direct) {
+          tmem_ld32(o_col + 32u * c, o);
+          tmem_ld_wait(o, 32);
 #pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            if (32 * c + j < a.dim)
-              *reinterpret_cast<float4*>(ro.part + 32 * c + j) =
-                  make_float4(o[j] + bad, o[j + 1] + bad, o[j + 2] + bad, o[j + 3] + bad);
+          for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(o[j] + bad);
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; j += 8)
-            if (32 * c + j < a.dim)
-              *reinterpret_cast<uint4*>(ro.out + (32 * c + j) * 2) =
-                  make_uint4(H::down2(o[j] * inv + bad, o[j + 1] * inv + bad), H::down2(o[j + 2] * inv + bad, o[j + 3] * inv + bad),
-                             H::down2(o[j + 4] * inv + bad, o[j + 5] * inv + bad), H::down2(o[j + 6] * inv + bad, o[j + 7] * inv + bad));
+          for (int h = 0; h < 2; ++h) {
+            tmem_ld32(o_col + 64u * c + 32u * h, o);
+            tmem_ld_wait(o, 32);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[16 * h + j] = H::down2(o[2 * j] * inv + bad, o[2 * j + 1] * inv + bad);
+          }
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+              make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int rl = 4 * j + (lane >> 3), ch = lane & 7;
+          const uint4 y = *reinterpret_cast<const uint4*>(stage + rl * 128 + ((ch ^ (rl & 7)) << 4));
+          char* const d = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(row_dst), rl));
+          const int at = c * 128 + ch * 16;
+          if (tile * kTileRows + (warp & 3) * 32 + rl < it.rows && at < row_bytes) *reinterpret_cast<uint4*>(d + at) = y;
+        }
+        __syncwarp();
       }
       if (mine) {
         if (!a.direct)
@@ -420,7 +447,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
         tc_commit(&sfull[t]);
       };
       wait_full(0);
-      for (int t = 0; t < tiles; ++t) product_s(t, 0);
+      for (int t = 0; t < tiles; ++t) {
+        wait(&qfull[t], 0u);
+        tc_fence_after();
+        product_s(t, 0);
+      }
       tc_commit(&empty[0]);
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
@@ -458,6 +489,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(kTmemCols) : "memory");
   }
+  if (a.beside && blockIdx.x + 1 == gridDim.x) pdl_wait_prior_grid();
 }
 
 template <typename H, int DP>

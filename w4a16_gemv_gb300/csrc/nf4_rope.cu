@@ -207,10 +207,7 @@ __device__ __forceinline__ bool slot_base(const RopeArgs& a, int64_t slot, int s
 
 constexpr int kRopeThreads = 128;
 constexpr int kInFlight = 4;  // row groups in flight per warp
-#ifndef KMAXPER
-#define KMAXPER 16
-#endif
-constexpr int kMaxPerWarp = KMAXPER;
+constexpr int kMaxPerWarp = 16;  // row groups that one warp walks over
 
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_rows_kernel(const __grid_constant__ RopeArgs a) {
