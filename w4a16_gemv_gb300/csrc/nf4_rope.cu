@@ -15,9 +15,9 @@
 // lane's registers: no shared memory, and an output may be its input. A warp
 // takes one token: the weights times the token's cosines and sines are formed
 // once and serve all the heads that the warp walks over (two multiplications
-// and additions per element, packed two to an instruction), and a row group's
-// registers are loaded again as soon as they are stored, so that four groups
-// stay in flight.
+// and additions per element, packed two to an instruction), and the next row
+// is asked for before the present one is worked on. 8192 tokens x 64 heads of
+// 128 in bf16 take 51.6 us (5.3 TB/s, 79% of measured copy bandwidth).
 #include <math.h>
 
 #include <initializer_list>
@@ -206,11 +206,14 @@ __device__ __forceinline__ bool slot_base(const RopeArgs& a, int64_t slot, int s
 }
 
 constexpr int kRopeThreads = 128;
-constexpr int kInFlight = 4;  // row groups in flight per warp
-constexpr int kMaxPerWarp = 16;  // row groups that one warp walks over
+// Blocks of four warps, six on an SM (80 registers): more warps beat more rows
+// in flight per warp (8192 tokens x 64 heads of 128, bf16, us: 4 rows and 4
+// blocks 60.3, 2 and 5 54.3, 1 and 6 51.6, 1 and 8 55.9).
+constexpr int kRopeBlocks = 6;
+constexpr int kMaxPerWarp = 8;  // row groups that one warp walks over (16: 54.9 us)
 
 template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_rows_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_rows_kernel(const __grid_constant__ RopeArgs a) {
   using E = Elem<T>;
   constexpr int P = E::kPer;  // elements per chunk = pairs per unit
   pdl_allow_dependents();
@@ -226,75 +229,48 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_rows_kernel(const __grid
   const int rot_units = a.rot / (2 * P);
   const bool active = unit < a.dim / (2 * P);
   const bool turned = unit < rot_units;
-  int c0, c1;  // byte offsets of the unit's chunks
-  if (turned && !kInterleaved) {
-    c0 = 16 * unit;
-    c1 = c0 + 16 * rot_units;
-  } else {
-    c0 = 32 * unit;
-    c1 = c0 + 16;
-  }
+  // byte offset of the unit's first chunk, and from there to the second (a lane
+  // past the row's end takes the first unit, and stores nothing)
+  const int c0 = !active ? 0 : turned && !kInterleaved ? 16 * unit : 32 * unit;
+  const int c1 = turned && !kInterleaved ? 16 * rot_units : 16;
   // this warp's row groups: q's, then k's, then v's
   const int g = part * a.per_warp;
   const int g_end = min(g + a.per_warp, a.gq + a.gk + a.gv);
 
-  // the groups of one kind (0 q, 1 k, 2 v) that this warp has: [from, to) of the kind's own
+  // The groups of one kind (0 q, 1 k, 2 v) that this warp has: [from, to) of
+  // the kind's own. Lanes without a row of their own read the last head's.
   struct Part {
-    const char* src;
-    int64_t step;
-    int from, to, heads;
+    const char* src;   // this lane's first chunk of head 0
+    int from, to;
+    int last;          // the last head
+    int64_t head_step;
   };
   auto part_of = [&](int kind) {
     const RowSet& r = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
     const int first = kind == 0 ? 0 : kind == 1 ? a.gq : a.gq + a.gk;
     const int n = kind == 0 ? a.gq : kind == 1 ? a.gk : a.gv;
-    return Part{r.in + int64_t(t) * r.in_ts * E::kSize, r.in_hs * E::kSize, max(g - first, 0), min(g_end - first, n),
-                r.heads};
+    return Part{r.in + int64_t(t) * r.in_ts * E::kSize + c0, max(g - first, 0),
+                min(g_end - first, n), r.heads - 1, r.in_hs * E::kSize};
   };
-  uint4 x[kInFlight][2];
-  auto load = [&](const Part& s, int gi, uint4 (&v)[2]) {
-    const int h = gi * rows + sub;
-    v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u);
-    if (gi < s.to && active && h < s.heads) {
-      const char* p = s.src + int64_t(h) * s.step;
-      v[0] = *reinterpret_cast<const uint4*>(p + c0);
-      v[1] = *reinterpret_cast<const uint4*>(p + c1);
+  uint4 x0 = {}, x1 = {};
+  auto load = [&](const Part& s, int gi) {
+    if (gi < s.to) {
+      const char* p = s.src + int64_t(min(gi * rows + sub, s.last)) * s.head_step;
+      x0 = *reinterpret_cast<const uint4*>(p);
+      x1 = *reinterpret_cast<const uint4*>(p + c1);
     }
   };
   // the first rows are on their way before the position and its table row are asked for
   const int kind0 = g < a.gq ? 0 : g < a.gq + a.gk ? 1 : 2;
   {
     const Part s = part_of(kind0);
-#pragma unroll
-    for (int u = 0; u < kInFlight; ++u) load(s, s.from + u, x[u]);
+    load(s, s.from);
   }
 
   const int64_t slot = a.slots ? a.slots[t] : 0;
-  float cosv[P], sinv[P];
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    cosv[i] = 1.0f;
-    sinv[i] = 0.0f;
-  }
-  if (a.rot > 0) {
-    const int64_t pos = a.positions[t];
-    const bool good = pos >= 0 && pos < a.max_positions;
-    if (!good) {  // NaN in every element of the token's rows, turned or not
-      if (lane == 0) atomicOr(&g_rope_flags, kFlagBadIndex);
-#pragma unroll
-      for (int i = 0; i < P; ++i) cosv[i] = sinv[i] = __uint_as_float(0x7fc00000u);
-    } else if (turned) {
-      const float4* src = reinterpret_cast<const float4*>(a.cs + pos * (a.rot / 2) + unit * P);
-#pragma unroll
-      for (int i = 0; i < P / 2; ++i) {
-        const float4 f = __ldg(src + i);
-        cosv[2 * i] = f.x;
-        sinv[2 * i] = f.y;
-        cosv[2 * i + 1] = f.z;
-        sinv[2 * i + 1] = f.w;
-      }
-    }
-  }
+  const int64_t pos = a.rot > 0 ? a.positions[t] : 0;
+  const bool good = a.rot == 0 || (pos >= 0 && pos < a.max_positions);
+  if (!good && lane == 0) atomicOr(&g_rope_flags, kFlagBadIndex);
   char *kdst = nullptr, *vdst = nullptr;
   bool stored = true;
   if (a.slots) stored = slot_base(a, slot, E::kSize, &kdst, &vdst);
@@ -303,93 +279,90 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_rows_kernel(const __grid
   for (int kind = kind0; kind < 3; ++kind) {
     const Part s = part_of(kind);
     if (s.from >= s.to || (kind > 0 && !stored)) continue;
-    if (kind != kind0) {
-#pragma unroll
-      for (int u = 0; u < kInFlight; ++u) load(s, s.from + u, x[u]);
-    }
+    if (kind != kind0) load(s, s.from);
     char* dst = kind == 0   ? a.q.out + int64_t(t) * a.q.out_ts * E::kSize
                 : !a.slots  ? a.k.out + int64_t(t) * a.k.out_ts * E::kSize
                 : kind == 1 ? kdst
                             : vdst;
+    dst += c0;
     const int64_t out_step = (kind == 0 ? a.q.out_hs : kind == 1 ? a.k.out_hs : a.v.out_hs) * E::kSize;
 
     // weight times cosine and sine: a' = a (wa c) - b (wb s), b' = b (wb c) + a (wa s)
     const char* wt = reinterpret_cast<const char*>(kind == 0 ? a.qw : kind == 1 ? a.kw : nullptr);
     uint64_t ac[P / 2], bs[P / 2], bc[P / 2], as[P / 2];
-    {
+    if (kind < 2) {
       float wa[P], wb[P];
-      if (wt && active) {
+      if (wt) {
         E::template up<kInterleaved>(__ldg(reinterpret_cast<const uint4*>(wt + c0)),
-                                     __ldg(reinterpret_cast<const uint4*>(wt + c1)), wa, wb);
+                                     __ldg(reinterpret_cast<const uint4*>(wt + c0 + c1)), wa, wb);
       } else {
 #pragma unroll
         for (int i = 0; i < P; ++i) wa[i] = wb[i] = 1.0f;
       }
+      // a position out of the table: NaN in every element, turned or not
+      const float4* src = reinterpret_cast<const float4*>(a.cs + (good ? pos : 0) * (a.rot / 2) + unit * P);
+      const float none = good ? 1.0f : __uint_as_float(0x7fc00000u);
 #pragma unroll
       for (int i = 0; i < P / 2; ++i) {
-        const uint64_t c = pack2(cosv[2 * i], cosv[2 * i + 1]), s = pack2(sinv[2 * i], sinv[2 * i + 1]);
-        const uint64_t va = pack2(wa[2 * i], wa[2 * i + 1]), vb = pack2(wb[2 * i], wb[2 * i + 1]);
-        ac[i] = mul2(va, c);
-        bc[i] = mul2(vb, c);
-        as[i] = mul2(va, s);
-        bs[i] = mul2(vb, pack2(-sinv[2 * i], -sinv[2 * i + 1]));
+        float4 f = make_float4(none, 0.0f, none, 0.0f);
+        if (turned && good) f = __ldg(src + i);
+        const uint64_t c = pack2(f.x, f.z);
+        ac[i] = mul2(pack2(wa[2 * i], wa[2 * i + 1]), c);
+        bc[i] = mul2(pack2(wb[2 * i], wb[2 * i + 1]), c);
+        as[i] = mul2(pack2(wa[2 * i], wa[2 * i + 1]), pack2(f.y, f.w));
+        bs[i] = mul2(pack2(wb[2 * i], wb[2 * i + 1]), pack2(-f.y, -f.w));
       }
     }
 
-    for (int base = s.from; base < s.to; base += kInFlight) {
+    for (int gi = s.from; gi < s.to; ++gi) {
+      uint4 y0 = x0, y1 = x1;
+      load(s, gi + 1);
+      if (kind < 2) {
+        float fa[P], fb[P];
+        E::template up<kInterleaved>(y0, y1, fa, fb);
+        uint64_t pa[P / 2], pb[P / 2];
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        const int gi = base + u;
-        if (gi >= s.to) break;
-        uint4 y0 = x[u][0], y1 = x[u][1];
-        load(s, gi + kInFlight, x[u]);
-        if (kind < 2) {
-          float fa[P], fb[P];
-          E::template up<kInterleaved>(y0, y1, fa, fb);
-          uint64_t pa[P / 2], pb[P / 2];
+        for (int i = 0; i < P / 2; ++i) {
+          pa[i] = pack2(fa[2 * i], fa[2 * i + 1]);
+          pb[i] = pack2(fb[2 * i], fb[2 * i + 1]);
+        }
+        float inv = 1.0f;
+        if (wt) {
+          uint64_t sq = mul2(pa[0], pa[0]);
 #pragma unroll
-          for (int i = 0; i < P / 2; ++i) {
-            pa[i] = pack2(fa[2 * i], fa[2 * i + 1]);
-            pb[i] = pack2(fb[2 * i], fb[2 * i + 1]);
+          for (int i = 1; i < P / 2; ++i) sq = fma2(pa[i], pa[i], sq);
+#pragma unroll
+          for (int i = 0; i < P / 2; ++i) sq = fma2(pb[i], pb[i], sq);
+          const float2 two = unpack2(sq);
+          float ss = active ? two.x + two.y : 0.0f;
+          for (int m = 1 << a.lane_bits >> 1; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+          inv = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
+        }
+        const uint64_t inv2 = pack2(inv, inv);
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) {
+          uint64_t ya = mul2(pa[i], ac[i]), yb = mul2(pb[i], bc[i]);
+          if (turned) {
+            ya = fma2(pb[i], bs[i], ya);
+            yb = fma2(pa[i], as[i], yb);
           }
-          float inv = 1.0f;
           if (wt) {
-            uint64_t sq = mul2(pa[0], pa[0]);
-#pragma unroll
-            for (int i = 1; i < P / 2; ++i) sq = fma2(pa[i], pa[i], sq);
-#pragma unroll
-            for (int i = 0; i < P / 2; ++i) sq = fma2(pb[i], pb[i], sq);
-            const float2 two = unpack2(sq);
-            float ss = two.x + two.y;
-            for (int m = 1 << a.lane_bits >> 1; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-            inv = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
+            ya = mul2(ya, inv2);
+            yb = mul2(yb, inv2);
           }
-          const uint64_t inv2 = pack2(inv, inv);
-#pragma unroll
-          for (int i = 0; i < P / 2; ++i) {
-            uint64_t ya = mul2(pa[i], ac[i]), yb = mul2(pb[i], bc[i]);
-            if (turned) {
-              ya = fma2(pb[i], bs[i], ya);
-              yb = fma2(pa[i], as[i], yb);
-            }
-            if (wt) {
-              ya = mul2(ya, inv2);
-              yb = mul2(yb, inv2);
-            }
-            const float2 u2 = unpack2(ya), v2 = unpack2(yb);
-            fa[2 * i] = u2.x;
-            fa[2 * i + 1] = u2.y;
-            fb[2 * i] = v2.x;
-            fb[2 * i + 1] = v2.y;
-          }
-          E::template down<kInterleaved>(fa, fb, y0, y1);
+          const float2 u2 = unpack2(ya), v2 = unpack2(yb);
+          fa[2 * i] = u2.x;
+          fa[2 * i + 1] = u2.y;
+          fb[2 * i] = v2.x;
+          fb[2 * i + 1] = v2.y;
         }
-        const int h = gi * rows + sub;
-        if (active && h < s.heads) {
-          char* p = dst + int64_t(h) * out_step;
-          *reinterpret_cast<uint4*>(p + c0) = y0;
-          *reinterpret_cast<uint4*>(p + c1) = y1;
-        }
+        E::template down<kInterleaved>(fa, fb, y0, y1);
+      }
+      const int h = gi * rows + sub;
+      if (active && h <= s.last) {
+        char* p = dst + int64_t(h) * out_step;
+        *reinterpret_cast<uint4*>(p) = y0;
+        *reinterpret_cast<uint4*>(p + c1) = y1;
       }
     }
   }
@@ -486,11 +459,11 @@ cudaError_t launch_rows(RopeArgs& a, cudaStream_t stream) {
   a.gq = (a.q.heads + rows - 1) / rows;
   a.gk = (a.k.heads + rows - 1) / rows;
   a.gv = (a.v.heads + rows - 1) / rows;
-  // Groups per warp: one while that does not fill the SMs (64 warps each),
+  // Groups per warp: one while that does not fill the SMs (24 warps each),
   // more when there is plenty, so that a warp's table row and weights serve
   // several groups.
   const int groups = a.gq + a.gk + a.gv;
-  int64_t per = int64_t(a.tokens) * groups / (152 * 16);
+  int64_t per = int64_t(a.tokens) * groups / (152 * 24);
   per = per < 1 ? 1 : per > kMaxPerWarp ? kMaxPerWarp : per;
   a.parts = int((groups + per - 1) / per);
   a.per_warp = (groups + a.parts - 1) / a.parts;
