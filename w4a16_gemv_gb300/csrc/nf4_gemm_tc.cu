@@ -555,6 +555,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
+}  // namespace
+
 // cuTensorMapEncodeTiled from the driver, looked up once.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   // initialised once, thread-safely (function-local static)
@@ -569,6 +571,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   }();
   return fn;
 }
+
+namespace {
 
 template <int BN>
 cudaError_t launch_tc(const TcArgs& a, const CUtensorMap& tmx, const CUtensorMap& tmw, int grid,

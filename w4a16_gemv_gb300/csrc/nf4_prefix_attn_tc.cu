@@ -18,19 +18,30 @@
 //     rescaled only when a row's maximum has grown past 2^8 (exact all the same,
 //     since O and l share m; binary32 and the 16-bit weights hold 2^8 times 1
 //     with the same relative error), so that O is rarely touched;
-//   * warps 8-11: keys and values from their pages into a ring of 128-row
-//     tiles by 16-byte asynchronous copies (any page size and stride; rows past
-//     the range are zero-filled, so what lies in unused slots never reaches a
-//     product), swizzled for the tensor cores: the same layout serves K as a
+//   * warp 8: keys and values from their pages into a ring of 128-row tiles, by
+//     tensor copies (TMA) of as many rows as are sure to lie in one page, one
+//     lane per box; boxes past the range, or on a page that does not exist,
+//     have their page coordinate past the end and arrive as zeros. Warp 9
+//     zeroes what a last box brought from beyond the range, so that what lies in
+//     unused slots never reaches a product. The copies' swizzle serves K as a
 //     K-major and V as an N-major operand;
+//   * page sizes without a factor of eight, and caches that no tensor map
+//     describes: warps 8-11 bring the same tiles by 16-byte asynchronous copies
+//     (about 1000 cycles of a warp per tile, where the tensor copies take 100);
 //   * warp 12: issues the products. S of the next keys follows O += P V of a
 //     tile in issue order, so P is read before S overwrites it, and the signal
 //     that S is complete also says that O is at rest.
 // Tensor memory: S (and P) of the tiles in columns 0 and 128, O in 256 and 384.
 // Waits are bounded; one that runs out sets bit 0 of the device error flags.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "nf4_prefix_attn.cuh"
 
 namespace nf4 {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
 namespace {
 
 __device__ unsigned int g_prefix_tc_flags = 0;
@@ -147,6 +158,28 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+// The two caches as 4-D tensors: 64 elements x box_rows slots of one head and
+// page. *_slot and *_head: which of the last three coordinates is the slot and
+// the head; the other is the page (the tensor's dimensions are in the order of
+// their strides).
+struct CacheMaps {
+  CUtensorMap k, v;
+  int box_rows;
+  int k_slot, k_head, v_slot, v_head;
+};
+
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, int x, int slot_at, int head_at,
+                                             int slot, int head, int page, uint64_t* bar) {
+  const int c1 = slot_at == 0 ? slot : head_at == 0 ? head : page;
+  const int c2 = slot_at == 1 ? slot : head_at == 1 ? head : page;
+  const int c3 = slot_at == 2 ? slot : head_at == 2 ? head : page;
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+
 template <int DP>
 struct Layout {
   static constexpr int kBlocks = DP / 64;                       // 128-byte columns blocks of a row
@@ -159,19 +192,21 @@ struct Layout {
   static constexpr uint32_t kBytes = kBars + 256 + 1024;        // + slack to align the base
 };
 
-template <typename H, int DP>
-__global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_constant__ PrefixArgs a) {
+template <typename H, int DP, bool kTma>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    prefix_tc_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CacheMaps maps) {
   using L = Layout<DP>;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + L::kBars);  // ring tile landed (4 loader warps)
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + L::kBars);  // ring tile landed
   uint64_t* const empty = full + L::kStages;                            // its products are done
   uint64_t* const sfull = empty + L::kStages;                           // S of a tile complete, O at rest
   uint64_t* const pfull = sfull + 2;                                    // P of a tile written (4 softmax warps)
   uint64_t* const qfull = pfull + 2;                                    // Q of a tile in place (4 softmax warps)
-  uint32_t* const s_taddr = reinterpret_cast<uint32_t*>(qfull + 2);
+  uint64_t* const tail = qfull + 2;                                     // the last tile of V landed, to be cleaned
+  uint32_t* const s_taddr = reinterpret_cast<uint32_t*>(tail + 1);
 
   // Everything, the tensor memory included, waits for the previous grid: an
   // allocation held by a grid that waits could starve the one waited for.
@@ -187,9 +222,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
   }
   if (tid == 0) {
     for (int i = 0; i < L::kStages; ++i) {
-      mbar_init(&full[i], 4);
+      mbar_init(&full[i], kTma ? 1 : 4);
       mbar_init(&empty[i], 1);
     }
+    mbar_init(tail, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 4);
@@ -378,7 +414,69 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
           *ro.lse = any ? fmaf(m, kLn2, logf(l)) : -INFINITY;
       }
     }
-  } else if (warp < 12) {
+  } else if (kTma && warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    const int rows = maps.box_rows;
+    const int valid = it.k1 - it.k0 - (n - 1) * kTileKeys;  // keys of the last tile
+    const bool clean = valid % rows != 0;                   // its last box reaches past them
+    if (warp == 8) {
+      const int per_tile = (kTileKeys / rows) * L::kBlocks;  // boxes of a tile: up to 32
+      const int box = lane / L::kBlocks, block = lane % L::kBlocks;
+      const bool mine = lane < per_tile;
+      // (page, first slot) of this lane's box of key tile i; past the range, or
+      // on a page that does not exist, the first page past the end
+      int page = a.num_pages, slot0 = 0;
+      auto fetch = [&](int i, int* pg, int* sl) {
+        const int j = it.k0 + i * kTileKeys + box * rows;
+        *pg = a.num_pages;
+        *sl = 0;
+        if (mine && j < it.k1) {
+          *pg = key_page(a, it, j);
+          *sl = a.page_shift >= 0 ? j & (a.page_size - 1) : j % a.page_size;
+        }
+      };
+      fetch(0, &page, &slot0);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        if (unsigned(page) > unsigned(a.num_pages) || (page == a.num_pages && mine && it.k0 + i * kTileKeys + box * rows < it.k1)) {
+          atomicOr(&g_prefix_tc_flags, kFlagBadIndex);
+          page = a.num_pages;
+        }
+        int next_page, next_slot;
+        fetch(i + 1, &next_page, &next_slot);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int u = 2 * i + kv, slot = u % L::kStages;
+          if (u >= L::kStages) wait(&empty[slot], uint32_t(u / L::kStages - 1) & 1u);
+          uint64_t* const bar = kv == 1 && clean && i + 1 == n ? tail : &full[slot];
+          if (lane == 0) mbar_arrive_expect_tx(bar, L::kTile);
+          __syncwarp();
+          const uint32_t dst = sbase + L::kRing + uint32_t(slot) * L::kTile + uint32_t(block) * L::kBlock + uint32_t(box * rows) * 128u;
+          if (mine) {
+            if (kv == 0)
+              tma_load_box(dst, &maps.k, block * 64, maps.k_slot, maps.k_head, slot0, it.head, page, bar);
+            else
+              tma_load_box(dst, &maps.v, block * 64, maps.v_slot, maps.v_head, slot0, it.head, page, bar);
+          }
+        }
+        page = next_page;
+        slot0 = next_slot;
+      }
+    } else if (warp == 9 && clean) {
+      wait(tail, 0u);
+      __syncwarp();
+      const int u = 2 * n - 1, to = (valid + rows - 1) / rows * rows;
+      unsigned char* const tile = smem + L::kRing + (u % L::kStages) * L::kTile;
+      for (int e = valid * 8 + lane; e < to * 8; e += 32)
+#pragma unroll
+        for (int b = 0; b < L::kBlocks; ++b)
+          *reinterpret_cast<uint4*>(tile + b * L::kBlock + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[u % L::kStages]);
+    }
+    __syncwarp();
+  } else if (!kTma && warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     constexpr int CPR = DP / 8, RPI = 32 / CPR;
     const int w = warp - 8;
@@ -483,6 +581,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
     __syncwarp();
   }
   if (!ok) atomicOr(&g_prefix_tc_flags, kFlagWaitRanOut);
+  // After a wait that ran out, tensor copies may still be in flight: wait for
+  // them, with the same bound, before the shared memory is given back.
+  if (__syncthreads_or(!ok) && kTma && tid == 0)
+    for (int u = 2 * n > L::kStages ? 2 * n - L::kStages : 0; u < 2 * n; ++u)
+      mbar_wait_bounded(&full[u % L::kStages], uint32_t(u / L::kStages) & 1u, kWaitLimitCycles);
   tc_fence_before();
   __syncthreads();
   if (warp == 12) {
@@ -492,9 +595,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefix_tc_kernel(const __grid_c
   if (a.beside && blockIdx.x + 1 == gridDim.x) pdl_wait_prior_grid();
 }
 
-template <typename H, int DP>
-cudaError_t launch_one(const PrefixArgs& p, unsigned items, cudaStream_t stream) {
-  auto kern = prefix_tc_kernel<H, DP>;
+template <typename H, int DP, bool kTma>
+cudaError_t launch_one(const PrefixArgs& p, const CacheMaps& maps, unsigned items, cudaStream_t stream) {
+  auto kern = prefix_tc_kernel<H, DP, kTma>;
   static PerDeviceCache attr_set, regs;
   cudaError_t e = set_max_dynamic_smem_once(kern, int(Layout<DP>::kBytes), attr_set);
   if (e != cudaSuccess) return e;
@@ -509,14 +612,71 @@ cudaError_t launch_one(const PrefixArgs& p, unsigned items, cudaStream_t stream)
   });
   if (e != cudaSuccess) return e;
   if (r != kLaunchRegs) return cudaErrorInvalidKernelImage;
-  return launch_k(kern, dim3(items), dim3(kTcThreads), Layout<DP>::kBytes, stream, p);
+  return launch_k(kern, dim3(items), dim3(kTcThreads), Layout<DP>::kBytes, stream, p, maps);
+}
+
+// One cache as a tensor map; false: no map describes it.
+bool encode_cache(const PrefixArgs& p, nf4_dtype dtype, const char* base, int64_t page_stride, int64_t slot_stride,
+                  int64_t head_stride, int box_rows, CUtensorMap* map, int* slot_at, int* head_at) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (!encode) return false;
+  struct Dim {
+    int64_t size, stride;
+    int box;
+    int* at;
+  } d[3] = {{p.page_size, slot_stride, box_rows, slot_at}, {p.k_heads, head_stride, 1, head_at},
+            {p.num_pages, page_stride, 1, nullptr}};
+  for (Dim& x : d) {
+    if (x.size == 1) x.stride = 256;  // never used, but a valid stride
+    if (x.stride <= 0) return false;
+  }
+  for (int i = 0; i < 2; ++i)  // in the order of their strides
+    for (int j = 0; j < 2 - i; ++j)
+      if (d[j].stride > d[j + 1].stride) {
+        const Dim t = d[j];
+        d[j] = d[j + 1];
+        d[j + 1] = t;
+      }
+  cuuint64_t dims[4] = {cuuint64_t(p.dim), 0, 0, 0}, strides[3];
+  cuuint32_t box[4] = {64u, 0u, 0u, 0u};
+  const cuuint32_t elem[4] = {1u, 1u, 1u, 1u};
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = cuuint64_t(d[i].size);
+    strides[i] = cuuint64_t(d[i].stride);
+    box[i + 1] = cuuint32_t(d[i].box);
+    if (d[i].at) *d[i].at = i;
+  }
+  return encode(map, dtype == NF4_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                const_cast<char*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kTma>
+cudaError_t launch_typed(const PrefixArgs& p, const CacheMaps& maps, nf4_dtype dtype, unsigned items,
+                         cudaStream_t stream) {
+  if (dtype == NF4_BF16)
+    return p.dim <= 64 ? launch_one<Bf16, 64, kTma>(p, maps, items, stream)
+                       : launch_one<Bf16, 128, kTma>(p, maps, items, stream);
+  return p.dim <= 64 ? launch_one<Fp16, 64, kTma>(p, maps, items, stream)
+                     : launch_one<Fp16, 128, kTma>(p, maps, items, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_prefix_tc(const PrefixArgs& p, nf4_dtype dtype, unsigned items, cudaStream_t stream) {
-  if (dtype == NF4_BF16) return p.dim <= 64 ? launch_one<Bf16, 64>(p, items, stream) : launch_one<Bf16, 128>(p, items, stream);
-  return p.dim <= 64 ? launch_one<Fp16, 64>(p, items, stream) : launch_one<Fp16, 128>(p, items, stream);
+  CacheMaps maps = {};
+  // Rows of a box: the largest power of two that divides the page (a box that
+  // starts at a multiple of it stays in one page), 8 to 128.
+  maps.box_rows = p.page_size & -p.page_size;
+  if (maps.box_rows > kTileKeys) maps.box_rows = kTileKeys;
+  if (maps.box_rows >= 8 && p.num_pages > 0 &&
+      encode_cache(p, dtype, p.k, p.k_ps, p.k_ss, p.k_hs, maps.box_rows, &maps.k, &maps.k_slot,
+                   &maps.k_head) &&
+      encode_cache(p, dtype, p.v, p.v_ps, p.v_ss, p.v_hs, maps.box_rows, &maps.v, &maps.v_slot,
+                   &maps.v_head))
+    return launch_typed<true>(p, maps, dtype, items, stream);
+  return launch_typed<false>(p, maps, dtype, items, stream);
 }
 
 cudaError_t read_and_clear_prefix_tc_flags(unsigned int* flags) {
