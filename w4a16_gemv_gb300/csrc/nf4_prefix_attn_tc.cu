@@ -50,6 +50,7 @@ constexpr int kTcThreads = 512;
 constexpr int kTileRows = 128;
 constexpr int kTileKeys = 128;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kGo = 4;  // key tiles whose loads may be under way (a ring of 8 tiles holds less than 4 pairs)
 constexpr float kGrowth = 8.0f;  // log2 of the growth of a row's maximum that is let pass
 // Registers: 512 threads launch with 128 each (65536); the two softmax
 // warpgroups take 192, the others keep 64: 256 x 192 + 256 x 64 = 65536.
@@ -65,6 +66,22 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
+}
+
+// Waits for phase `parity` of `bar`: at most 1000 sleeps of up to a
+// millisecond each. (Without a clock to read between them this wakes sooner
+// than the shared bounded wait, and 512 threads poll here.)
+__device__ __forceinline__ bool mbar_wait_counted(uint64_t* bar, uint32_t parity) {
+  const uint32_t addr = smem_u32(bar);
+  uint32_t done = 0;
+#pragma unroll 1
+  for (int k = 0; k < 1000 && !done; ++k)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(addr), "r"(parity), "r"(1000000)
+        : "memory");
+  return done != 0;
 }
 
 // Shared-memory matrix descriptors, 128-byte swizzle: rows of 128 bytes in
@@ -196,15 +213,21 @@ template <typename H, int DP, bool kTma>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefix_tc_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CacheMaps maps) {
   using L = Layout<DP>;
+  constexpr int kLoaders = kTma ? 1 : 4;  // arrivals for a ring tile
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + L::kBars);  // ring tile landed
-  uint64_t* const empty = full + L::kStages;                            // its products are done
+  // go: all that the products of key tile i need besides P of the second tile
+  // of rows: P of the first, V_i and K_{i+1}. One barrier, because a look at
+  // a barrier costs the issuing thread some 250 cycles while the tensor cores
+  // keep the shared memory busy, and their queue does not bridge that.
+  uint64_t* const go = reinterpret_cast<uint64_t*>(smem + L::kBars);    // [kGo], key tile i: i % kGo
+  uint64_t* const kfirst = go + kGo;                                    // K_0 landed
+  uint64_t* const empty = kfirst + 1;                                   // a ring tile's products are done
   uint64_t* const sfull = empty + L::kStages;                           // S of a tile complete, O at rest
-  uint64_t* const pfull = sfull + 2;                                    // P of a tile written (4 softmax warps)
-  uint64_t* const qfull = pfull + 2;                                    // Q of a tile in place (4 softmax warps)
+  uint64_t* const psecond = sfull + 2;                                  // P of the second tile written
+  uint64_t* const qfull = psecond + 1;                                  // Q of a tile in place (4 softmax warps)
   uint64_t* const tail = qfull + 2;                                     // the last tile of V landed, to be cleaned
   uint32_t* const s_taddr = reinterpret_cast<uint32_t*>(tail + 1);
 
@@ -221,14 +244,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 0) {
-    for (int i = 0; i < L::kStages; ++i) {
-      mbar_init(&full[i], kTma ? 1 : 4);
-      mbar_init(&empty[i], 1);
-    }
+    for (int i = 0; i < kGo; ++i) mbar_init(&go[i], 4 + 2 * kLoaders);
+    for (int i = 0; i < L::kStages; ++i) mbar_init(&empty[i], 1);
+    mbar_init(kfirst, kLoaders);
+    mbar_init(psecond, 4);
     mbar_init(tail, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 4);
       mbar_init(&qfull[i], 4);
     }
     fence_mbar_init();
@@ -249,7 +271,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t tbase = *s_taddr;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (ok) ok = mbar_wait_bounded(bar, parity, kWaitLimitCycles);
+    if (ok) ok = mbar_wait_counted(bar, parity);
   };
 
   if (warp < 8) {
@@ -357,7 +379,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[tile]);
+        if (lane == 0) mbar_arrive(tile == 0 ? &go[i % kGo] : psecond);
       }
       wait(&sfull[tile], uint32_t(n) & 1u);  // the last product is in O
       __syncwarp();
@@ -448,7 +470,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int kv = 0; kv < 2; ++kv) {
           const int u = 2 * i + kv, slot = u % L::kStages;
           if (u >= L::kStages) wait(&empty[slot], uint32_t(u / L::kStages - 1) & 1u);
-          uint64_t* const bar = kv == 1 && clean && i + 1 == n ? tail : &full[slot];
+          uint64_t* const bar = kv == 0 ? (i == 0 ? kfirst : &go[(i - 1) % kGo])
+                                : clean && i + 1 == n ? tail : &go[i % kGo];
           if (lane == 0) mbar_arrive_expect_tx(bar, L::kTile);
           __syncwarp();
           const uint32_t dst = sbase + L::kRing + uint32_t(slot) * L::kTile + uint32_t(block) * L::kBlock + uint32_t(box * rows) * 128u;
@@ -462,6 +485,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         page = next_page;
         slot0 = next_slot;
       }
+      if (lane == 0) mbar_arrive(&go[(n - 1) % kGo]);  // there is no K after the last V
     } else if (warp == 9 && clean) {
       wait(tail, 0u);
       __syncwarp();
@@ -473,7 +497,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           *reinterpret_cast<uint4*>(tile + b * L::kBlock + e * 16) = make_uint4(0u, 0u, 0u, 0u);
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[u % L::kStages]);
+      if (lane == 0) mbar_arrive(&go[(n - 1) % kGo]);
     }
     __syncwarp();
   } else if (!kTma && warp < 12) {
@@ -490,6 +514,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int j = it.k0 + i * kTileKeys + w * 32 + lane;
       if (j < it.k1) page = key_page(a, it, j);
     };
+    auto landed = [&](int u) { return u == 0 ? kfirst : &go[((u - 1) >> 1) % kGo]; };
     fetch_page(0);
 #pragma unroll 1
     for (int u = 0; u < 2 * n; ++u) {
@@ -516,24 +541,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         cp_async_wait<L::kLag>();
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[(u - L::kLag) % L::kStages]);
+        if (lane == 0) mbar_arrive(landed(u - L::kLag));
       }
     }
     cp_async_wait<0>();
     fence_async_smem();
     __syncwarp();
-    if (lane == 0)
-      for (int u = 2 * n > L::kLag ? 2 * n - L::kLag : 0; u < 2 * n; ++u) mbar_arrive(&full[u % L::kStages]);
+    if (lane == 0) {
+      for (int u = 2 * n > L::kLag ? 2 * n - L::kLag : 0; u < 2 * n; ++u) mbar_arrive(landed(u));
+      mbar_arrive(&go[(n - 1) % kGo]);  // there is no K after the last V
+    }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 12 && lane == 0) {
       constexpr uint32_t kIdS = idesc<H>(kTileKeys, false);
       constexpr uint32_t kIdO = idesc<H>(DP, true);
       const uint32_t ring = sbase + L::kRing;
-      auto wait_full = [&](int u) {
-        wait(&full[u % L::kStages], uint32_t(u / L::kStages) & 1u);
-        tc_fence_after();
-      };
       auto product_s = [&](int t, int u) {  // S_t = Q_t K^T, K in ring tile u
         const uint64_t qd = desc_k_major(sbase + uint32_t(t) * L::kTile);
         const uint64_t kd = desc_k_major(ring + uint32_t(u % L::kStages) * L::kTile);
@@ -544,31 +567,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         tc_commit(&sfull[t]);
       };
-      wait_full(0);
+      wait(kfirst, 0u);
       for (int t = 0; t < tiles; ++t) {
         wait(&qfull[t], 0u);
-        tc_fence_after();
         product_s(t, 0);
       }
       tc_commit(&empty[0]);
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const int uv = 2 * i + 1, uk = 2 * i + 2;
-        const bool more = i + 1 < n;
-        wait_full(uv);
         const uint64_t vd = desc_n_major(ring + uint32_t(uv % L::kStages) * L::kTile, L::kBlock);
         for (int t = 0; t < tiles; ++t) {
-          wait(&pfull[t], uint32_t(i) & 1u);
+          if (t == 0)
+            wait(&go[i % kGo], uint32_t(i / kGo) & 1u);
+          else
+            wait(psecond, uint32_t(i) & 1u);
           tc_fence_after();
 #pragma unroll
           for (int s = 0; s < kTileKeys / 16; ++s)  // 16 keys: two groups of eight rows
             mma_ts(tbase + 256u + uint32_t(t) * 128u, tbase + uint32_t(t) * 128u + 8u * s, vd + uint64_t(s * (2048 >> 4)),
                    kIdO, (i > 0 || s > 0) ? 1u : 0u);
-          if (t + 1 == tiles) tc_commit(&empty[uv % L::kStages]);
-          if (more) {
-            if (t == 0) wait_full(uk);
+          const bool end = t + 1 == tiles;
+          if (end) tc_commit(&empty[uv % L::kStages]);
+          if (i + 1 < n) {
             product_s(t, uk);
-            if (t + 1 == tiles) tc_commit(&empty[uk % L::kStages]);
+            if (end) tc_commit(&empty[uk % L::kStages]);
           } else {
             tc_commit(&sfull[t]);
           }
@@ -576,7 +599,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       // The ring's last tiles: every product is done before the memory is given back.
       const int last = 2 * n - 1;
-      ok = mbar_wait_bounded(&empty[last % L::kStages], uint32_t(last / L::kStages) & 1u, kWaitLimitCycles) && ok;
+      ok = mbar_wait_counted(&empty[last % L::kStages], uint32_t(last / L::kStages) & 1u) && ok;
     }
     __syncwarp();
   }
@@ -584,8 +607,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // After a wait that ran out, tensor copies may still be in flight: wait for
   // them, with the same bound, before the shared memory is given back.
   if (__syncthreads_or(!ok) && kTma && tid == 0)
-    for (int u = 2 * n > L::kStages ? 2 * n - L::kStages : 0; u < 2 * n; ++u)
-      mbar_wait_bounded(&full[u % L::kStages], uint32_t(u / L::kStages) & 1u, kWaitLimitCycles);
+    for (int i = n > kGo ? n - kGo : 0; i < n; ++i) mbar_wait_counted(&go[i % kGo], uint32_t(i / kGo) & 1u);
   tc_fence_before();
   __syncthreads();
   if (warp == 12) {
