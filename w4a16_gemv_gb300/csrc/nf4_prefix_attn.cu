@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads) prefix_mma_kernel(const __
   extern __shared__ __align__(128) unsigned char smem[];
   if (!a.beside) pdl_wait_prior_grid();
   pdl_allow_dependents();
-  const PrefixItem it = prefix_item(a, int64_t(a.first) + blockIdx.x, &g_prefix_flags);
+  const PrefixItem it = prefix_item(a, unsigned(a.first) + blockIdx.x, &g_prefix_flags);
   if (it.rows > 0) attend<H, DP, R>(a, it, smem);
   if (a.beside && blockIdx.x + 1 == gridDim.x) pdl_wait_prior_grid();
 }

@@ -72,14 +72,14 @@ __device__ __forceinline__ int visible_keys(const PrefixItem& it, int i) {
 // tiles of one key range side by side, so that they meet in L2), then suffix
 // items. Tiles of the suffix are numbered along the batch; every warp finds
 // its own by a scan of cu_q, 32 sequences at a time. Called by whole warps.
-__device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, int64_t index, unsigned int* flags) {
+__device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, unsigned index, unsigned int* flags) {
   PrefixItem it;
-  const int64_t prefix_items = int64_t(a.prefix_tiles) * a.k_heads * a.prefix_splits;
+  const unsigned prefix_items = unsigned(a.prefix_tiles) * unsigned(a.k_heads) * unsigned(a.prefix_splits);
   if (index < prefix_items) {
-    const int tile = int(index % a.prefix_tiles);
-    const int rest = int(index / a.prefix_tiles);
-    it.head = rest % a.k_heads;
-    it.split = rest / a.k_heads;
+    const unsigned rest = index / unsigned(a.prefix_tiles);
+    const int tile = int(index - rest * unsigned(a.prefix_tiles));
+    it.split = int(rest / unsigned(a.k_heads));
+    it.head = int(rest) - it.split * a.k_heads;
     it.t0 = 0;
     it.n = a.tokens;
     it.r0 = tile * a.prefix_rows;
@@ -92,10 +92,10 @@ __device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, int64_t i
     return it;
   }
   index -= prefix_items;
-  const int tile = int(index % a.suffix_tiles);
-  const int rest = int(index / a.suffix_tiles);
-  it.head = rest % a.k_heads;
-  const int split = rest / a.k_heads;
+  const unsigned rest = index / unsigned(a.suffix_tiles);
+  const int tile = int(index - rest * unsigned(a.suffix_tiles));
+  const int split = int(rest / unsigned(a.k_heads));
+  it.head = int(rest) - split * a.k_heads;
   it.split = a.prefix_splits + split;
   it.own = true;
   it.rows = 0;

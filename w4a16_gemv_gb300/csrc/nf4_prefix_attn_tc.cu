@@ -53,7 +53,9 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kGo = 4;  // key tiles whose loads may be under way (a ring of 8 tiles holds less than 4 pairs)
 constexpr float kGrowth = 8.0f;  // log2 of the growth of a row's maximum that is let pass
 // Registers: 512 threads launch with 128 each (65536); the two softmax
-// warpgroups take 192, the others keep 64: 256 x 192 + 256 x 64 = 65536.
+// warpgroups take 184, the others keep 72: 256 x 184 + 256 x 72 = 65536. (With
+// 192 and 64 the loading and issuing warps spill, and a spill's reload behind
+// streaming keys costs a microsecond per key tile.)
 constexpr int kLaunchRegs = 128;
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -231,18 +233,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* const tail = qfull + 2;                                     // the last tile of V landed, to be cleaned
   uint32_t* const s_taddr = reinterpret_cast<uint32_t*>(tail + 1);
 
-  // Everything, the tensor memory included, waits for the previous grid: an
-  // allocation held by a grid that waits could starve the one waited for.
-  if (!a.beside) pdl_wait_prior_grid();
-  const PrefixItem it = prefix_item(a, int64_t(a.first) + blockIdx.x, &g_prefix_tc_flags);
-  const int n = (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys;  // key tiles
-  const bool works = it.rows > 0 && n > 0;                    // the same in the whole CTA
-  if (warp == 12 && works) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_taddr)),
-                 "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
   if (tid == 0) {
     for (int i = 0; i < kGo; ++i) mbar_init(&go[i], 4 + 2 * kLoaders);
     for (int i = 0; i < L::kStages; ++i) mbar_init(&empty[i], 1);
@@ -255,12 +245,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     fence_mbar_init();
   }
+  if (kTma && tid == 32 * 8) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
+  }
+  __syncthreads();  // the barriers exist; from here the warps start their parts as they can
+  // Everything else, the tensor memory included, waits for the previous grid:
+  // an allocation held by a grid that waits could starve the one waited for.
+  if (!a.beside) pdl_wait_prior_grid();
+  const PrefixItem it = prefix_item(a, unsigned(a.first) + blockIdx.x, &g_prefix_tc_flags);
+  const int n = (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys;  // key tiles
+  const bool works = it.rows > 0 && n > 0;                    // the same in the whole CTA
   const int tiles = it.rows > kTileRows ? 2 : 1;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  pdl_allow_dependents();  // after the allocation, for the same reason
   if (!works) {
+    pdl_allow_dependents();
     for (int r = tid; r < it.rows; r += kTcThreads) {
       const RowOut ro = row_out(a, it, it.r0 + r);
       *ro.ml = make_float2(-INFINITY, 0.0f);  // (a plan with one range of keys has no empty range)
@@ -268,44 +266,48 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (a.beside && blockIdx.x + 1 == gridDim.x) pdl_wait_prior_grid();
     return;
   }
-  const uint32_t tbase = *s_taddr;
+  // The softmax warps and the issuing warp meet here, when the tensor memory
+  // is allocated; the next grid may start after that, for the same reason as
+  // above (one thread of the CTA says so).
+  auto tmem_address = [&]() {
+    tc_fence_before();
+    asm volatile("bar.sync 1, 288;" ::: "memory");
+    tc_fence_after();
+    return *s_taddr;
+  };
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = mbar_wait_counted(bar, parity);
   };
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int tile = warp >> 2;
+    // Q: each warp asks for its 32 rows first
     if (tile < tiles) {
-      // Q: each warp brings its 32 rows
-      {
-        constexpr int CPR = DP / 8, RPI = 32 / CPR;
-        const int r = warp * 32 + lane;
-        int64_t off = 0;
-        if (r < it.rows) {
-          const int rr = it.r0 + r;
-          off = int64_t(it.t0 + rr / a.group) * a.q_ts + int64_t(it.head * a.group + rr % a.group) * a.q_hs;
-        }
-        const int c = lane % CPR;
-        uint4 v[32 / RPI];
-#pragma unroll
-        for (int x = 0; x < 32 / RPI; ++x) {
-          const int rl = x * RPI + lane / CPR;
-          const int64_t o = __shfl_sync(0xffffffffu, off, rl);
-          v[x] = make_uint4(0u, 0u, 0u, 0u);
-          if (warp * 32 + rl < it.rows && c * 8 < a.dim) v[x] = __ldg(reinterpret_cast<const uint4*>(a.q + o + c * 16));
-        }
-#pragma unroll
-        for (int x = 0; x < 32 / RPI; ++x) {
-          const int row = (warp & 3) * 32 + x * RPI + lane / CPR;
-          *reinterpret_cast<uint4*>(smem + tile * L::kTile + (c >> 3) * L::kBlock + row * 128 +
-                                    (((c & 7) ^ (row & 7)) << 4)) = v[x];
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&qfull[tile]);
+      constexpr int kQChunks = DP / 8, kQStep = 32 / kQChunks;
+      const int r = warp * 32 + lane, c = lane % kQChunks;
+      int64_t off = 0;
+      if (r < it.rows) {
+        const int t = (it.r0 + r) / a.group;
+        off = int64_t(it.t0 + t) * a.q_ts + int64_t(it.head * a.group + (it.r0 + r - t * a.group)) * a.q_hs;
       }
+      const uint32_t dst = sbase + uint32_t(tile) * L::kTile + uint32_t(c >> 3) * L::kBlock;
+#pragma unroll
+      for (int x = 0; x < 32 / kQStep; ++x) {
+        const int rl = x * kQStep + lane / kQChunks, row = (warp & 3) * 32 + rl;
+        const int64_t o = __shfl_sync(0xffffffffu, off, rl);
+        const bool there = warp * 32 + rl < it.rows && c * 8 < a.dim;
+        cp_async16(dst + uint32_t(row) * 128u + uint32_t(((c & 7) ^ (row & 7)) << 4), there ? a.q + o + c * 16 : a.q, there);
+      }
+      cp_async_commit();
+    }
+    const uint32_t tbase = tmem_address();
+    if (tile < tiles) {
+      cp_async_wait<0>();
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qfull[tile]);
       const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
       const uint32_t s_col = tbase + lanes + uint32_t(tile) * 128u;
       const uint32_t o_col = tbase + lanes + 256u + uint32_t(tile) * 128u;
@@ -394,17 +396,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // tile (its products are done), so that rows leave in whole sectors:
       // 32 columns of partial results, or 64 of the 16-bit output.
       unsigned char* const stage = smem + tile * L::kTile + (warp & 3) * 4096;
-      char* const row_dst = a.direct ? ro.out : reinterpret_cast<char*>(ro.part);
       const int row_bytes = a.dim * (a.direct ? 2 : 4);
+      const int ch = lane & 7;  // this lane's 16 bytes of rows lane / 8, lane / 8 + 4, ..
+      char* dst[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int rl = 4 * j + (lane >> 3);
+        dst[j] = reinterpret_cast<char*>(__shfl_sync(
+            0xffffffffu, reinterpret_cast<uint64_t>(a.direct ? ro.out : reinterpret_cast<char*>(ro.part)), rl));
+        if (tile * kTileRows + (warp & 3) * 32 + rl >= it.rows) dst[j] = nullptr;
+      }
+      const int passes = a.direct ? DP / 64 : DP / 32;
+      float o[32];
+      if (!a.direct) tmem_ld32(o_col, o);
 #pragma unroll 1
-      for (int c = 0; c < (a.direct ? DP / 64 : DP / 32); ++c) {
-        float o[32];
+      for (int c = 0; c < passes; ++c) {
         uint32_t w[32];
         if (!a.direct) {
-          tmem_ld32(o_col + 32u * c, o);
           tmem_ld_wait(o, 32);
 #pragma unroll
           for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(o[j] + bad);
+          if (c + 1 < passes) tmem_ld32(o_col + 32u * (c + 1), o);
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -414,20 +426,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int j = 0; j < 16; ++j) w[16 * h + j] = H::down2(o[2 * j] * inv + bad, o[2 * j + 1] * inv + bad);
           }
         }
+        __syncwarp();  // the stage's last pass has been read
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
               make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         __syncwarp();
+        uint4 y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int rl = 4 * j + (lane >> 3), ch = lane & 7;
-          const uint4 y = *reinterpret_cast<const uint4*>(stage + rl * 128 + ((ch ^ (rl & 7)) << 4));
-          char* const d = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(row_dst), rl));
-          const int at = c * 128 + ch * 16;
-          if (tile * kTileRows + (warp & 3) * 32 + rl < it.rows && at < row_bytes) *reinterpret_cast<uint4*>(d + at) = y;
+          const int rl = 4 * j + (lane >> 3);
+          y[j] = *reinterpret_cast<const uint4*>(stage + rl * 128 + ((ch ^ (rl & 7)) << 4));
         }
-        __syncwarp();
+        const int at = c * 128 + ch * 16;
+        if (at < row_bytes) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (dst[j]) *reinterpret_cast<uint4*>(dst[j] + at) = y[j];
+        }
       }
       if (mine) {
         if (!a.direct)
@@ -437,7 +453,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
   } else if (kTma && warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int rows = maps.box_rows;
     const int valid = it.k1 - it.k0 - (n - 1) * kTileKeys;  // keys of the last tile
     const bool clean = valid % rows != 0;                   // its last box reaches past them
@@ -501,7 +517,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     __syncwarp();
   } else if (!kTma && warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     constexpr int CPR = DP / 8, RPI = 32 / CPR;
     const int w = warp - 8;
     const int c = lane % CPR;
@@ -552,8 +568,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_arrive(&go[(n - 1) % kGo]);  // there is no K after the last V
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 12) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_taddr)),
+                   "r"(kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+      pdl_allow_dependents();
+      tmem_address();
+    }
     if (warp == 12 && lane == 0) {
+      const uint32_t tbase = *s_taddr;
       constexpr uint32_t kIdS = idesc<H>(kTileKeys, false);
       constexpr uint32_t kIdO = idesc<H>(DP, true);
       const uint32_t ring = sbase + L::kRing;
@@ -612,7 +637,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   if (warp == 12) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*s_taddr), "r"(kTmemCols) : "memory");
   }
   if (a.beside && blockIdx.x + 1 == gridDim.x) pdl_wait_prior_grid();
 }
