@@ -71,6 +71,7 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(smem);
   const int chunks = a.dim / 8;
+  const bool alike = a.k_ps == a.v_ps && a.k_ss == a.v_ss && a.k_hs == a.v_hs;  // one offset serves both caches
   const int ntiles = (it.k1 - it.k0 + kKeys - 1) / kKeys;
 
   // copies of tile i: warp w brings rows 16 w .. 16 w + 15; lane l holds the
@@ -83,15 +84,15 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
   auto copy_tile = [&](int i) {
     const int j = it.k0 + i * kKeys + warp * 16 + (lane & 15);
     KeyOffset off{0, 0};
-    const bool real = j < it.k1 && key_offset(a, it, j, page, &g_prefix_flags, &off);
+    if (!(j < it.k1 && key_offset(a, it, j, page, &g_prefix_flags, &off))) off.k = off.v = -1;
     const uint32_t ks = sbase + uint32_t(i % kStages) * (2 * kTile);
     const int c = lane % CPR;
 #pragma unroll
     for (int x = 0; x < 16 / RPI; ++x) {
       const int rl = x * RPI + lane / CPR;  // row within the warp's 16
       const int64_t ko = __shfl_sync(0xffffffffu, off.k, rl);
-      const int64_t vo = __shfl_sync(0xffffffffu, off.v, rl);
-      const bool there = __shfl_sync(0xffffffffu, int(real), rl) && c < chunks;
+      const int64_t vo = alike ? ko : __shfl_sync(0xffffffffu, off.v, rl);
+      const bool there = ko >= 0 && c < chunks;
       const int row = warp * 16 + rl;
       const uint32_t dst = ks + uint32_t(row) * (DP * 2) + uint32_t((c ^ (row & 7)) << 4);
       // what is not there is filled with zeros, from no address of the cache
@@ -194,11 +195,20 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
     }
     const float na = fmaxf(ma, xa * a.scale_log2), nb = fmaxf(mb, xb * a.scale_log2);
     const float ba = na == -INFINITY ? 0.0f : na, bb = nb == -INFINITY ? 0.0f : nb;
-    const float fa = ex2(ma - ba), fb = ex2(mb - bb);
-    ma = na;
-    mb = nb;
-    la *= fa;
-    lb *= fb;
+    if (__any_sync(0xffffffffu, na != ma || nb != mb)) {  // a maximum grew
+      const float fa = ex2(ma - ba), fb = ex2(mb - bb);
+      ma = na;
+      mb = nb;
+      la *= fa;
+      lb *= fb;
+#pragma unroll
+      for (int d = 0; d < DP / 8; ++d) {
+        o[d][0] *= fa;
+        o[d][1] *= fa;
+        o[d][2] *= fb;
+        o[d][3] *= fb;
+      }
+    }
     uint32_t pf[NB][2];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
@@ -208,13 +218,6 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
       lb += p2 + p3;
       pf[n][0] = H::down2(p0, p1);
       pf[n][1] = H::down2(p2, p3);
-    }
-#pragma unroll
-    for (int d = 0; d < DP / 8; ++d) {
-      o[d][0] *= fa;
-      o[d][1] *= fa;
-      o[d][2] *= fb;
-      o[d][3] *= fb;
     }
 #pragma unroll
     for (int n = 0; n < NB / 2; ++n) {
@@ -484,12 +487,16 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kMaxRanges = 152;  // per row, of the shared and of the own keys each
 
-// Keys per range of the mma kernel, in stages of 64: at least two stages,
-// about eight items per SM, at most kMaxRanges ranges.
-int64_t mma_range(int64_t tiles, int64_t stages) {
-  int64_t per = tiles * stages / (kSms * 8);
+// Keys per range of the mma kernel, in units of 64: at least two, and about
+// eight items per SM where there is that much, else one for each CTA that fits
+// on the SMs (128 sequences x 2000 keys of one head: 35.3 -> 31.9 us); at most
+// kMaxRanges ranges.
+int64_t mma_range(int64_t tiles, int64_t units, int dim) {
+  const int64_t total = tiles * units, resident = kSms * (dim <= 64 ? 10 : 6);
+  int64_t per = total / (kSms * 8);
+  if (per < 6) per = (total + resident - 1) / resident;
   per = per < 2 ? 2 : per;
-  return stages > per * kMaxRanges ? (stages + kMaxRanges - 1) / kMaxRanges : per;
+  return units > per * kMaxRanges ? (units + kMaxRanges - 1) / kMaxRanges : per;
 }
 
 // Keys per range of the tensor-core kernel (one CTA per SM), in stages of 64
@@ -526,22 +533,29 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
   p->prefix_len = int(a.prefix_len);
   p->suffix_max = a.batch > 0 ? int(a.suffix_pages_width * a.page_size) : 0;
   const int64_t rows = a.tokens * p->group;  // of a key/value head
-  p->prefix_rows = rows > 32 ? 256 : rows > 32 ? 64 : 16;
+  // The shared keys go to the tcgen05 kernel however few the rows: it streams
+  // them faster (one token, 12 heads over 2, 100000 keys: 26.7 us against 36 us)
+  // and no slower when they are few; only where they are few and so are the
+  // rows, the call is one launch fewer with everything on the other kernel.
+  p->prefix_rows = rows > 16 || p->prefix_len > 1024 ? 256 : 16;
   p->suffix_rows = rows > 64 * a.batch ? 256 : rows > 32 * a.batch ? 64 : 16;
   p->prefix_tiles = int((rows + p->prefix_rows - 1) / p->prefix_rows);
   // sum over sequences of ceil(rows / suffix_rows) is below both bounds
   const int64_t whole = rows / p->suffix_rows + a.batch;
   p->suffix_tiles = int(whole < rows ? whole : rows);
+  // as many as there are when the tokens are spread evenly (the ranges are made for these)
+  const int64_t likely = a.batch > 0 ? a.batch * ((rows / a.batch + p->suffix_rows - 1) / p->suffix_rows) : 0;
   const int64_t pk = (int64_t(p->prefix_len) + kUnit - 1) / kUnit, sk = (int64_t(p->suffix_max) + kUnit - 1) / kUnit;
   if (pk > 0) {
-    const int64_t per = p->prefix_rows == 256 ? tc_range(int64_t(p->prefix_tiles) * p->k_heads, (pk + 1) / 2, rows * p->k_heads)
-                                     : mma_range(int64_t(p->prefix_tiles) * p->k_heads, pk);
+    const int64_t per = p->prefix_rows == 256
+                            ? tc_range(int64_t(p->prefix_tiles) * p->k_heads, (pk + 1) / 2, rows * p->k_heads)
+                            : mma_range(int64_t(p->prefix_tiles) * p->k_heads, pk, p->dim);
     p->prefix_chunk = int(per * kUnit);
     p->prefix_splits = int((pk + per - 1) / per);
   }
   if (sk > 0) {
-    const int64_t per = p->suffix_rows == 256 ? tc_range(int64_t(p->suffix_tiles) * p->k_heads, (sk + 1) / 2, rows * p->k_heads)
-                                     : mma_range(int64_t(p->suffix_tiles) * p->k_heads, sk);
+    const int64_t per = p->suffix_rows == 256 ? tc_range(likely * p->k_heads, (sk + 1) / 2, rows * p->k_heads)
+                                              : mma_range(likely * p->k_heads, sk, p->dim);
     p->suffix_chunk = int(per * kUnit);
     p->suffix_splits = int((sk + per - 1) / per);
   }
