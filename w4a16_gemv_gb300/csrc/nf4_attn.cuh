@@ -23,8 +23,9 @@ cudaError_t launch_rope_table(const nf4_rope_table_args& a, cudaStream_t stream)
 cudaError_t launch_qk_rope(const nf4_qk_norm_rope_args& a, const nf4_kv_append_args* cache,
                            cudaStream_t stream);
 size_t prefix_attention_workspace_bytes(const nf4_prefix_attention_args& a);
-cudaError_t launch_prefix_attention(const nf4_prefix_attention_args& a, void* workspace,
-                                    cudaStream_t stream);
+// *enough is false, and nothing was launched, where the workspace does not do.
+cudaError_t launch_prefix_attention(const nf4_prefix_attention_args& a, void* workspace, size_t workspace_bytes,
+                                    bool* enough, cudaStream_t stream);
 
 // 16-bit element types: conversions to and from binary32.
 struct Bf16 {

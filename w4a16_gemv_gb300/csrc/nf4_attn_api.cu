@@ -140,9 +140,10 @@ nf4_status nf4_prefix_attention(const nf4_prefix_attention_args* args, void* wor
       !aligned(a.lse, 4) || !aligned(a.prefix_pages, 4) || !aligned(a.suffix_pages, 4) ||
       !aligned(a.suffix_lens, 4) || !aligned(a.cu_q, 4))
     return NF4_ERR_MISALIGNED;
-  const size_t need = nf4::prefix_attention_workspace_bytes(a);
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return NF4_ERR_WORKSPACE;
-  return nf4::status_of(nf4::launch_prefix_attention(a, workspace, reinterpret_cast<cudaStream_t>(stream)));
+  bool enough = false;
+  const cudaError_t e = nf4::launch_prefix_attention(a, workspace, workspace_bytes, &enough,
+                                                     reinterpret_cast<cudaStream_t>(stream));
+  return enough ? nf4::status_of(e) : NF4_ERR_WORKSPACE;
 }
 
 }  // extern "C"

@@ -17,6 +17,7 @@ namespace {
 
 __device__ unsigned int g_prefix_flags = 0;
 
+constexpr int kSms = 152;
 constexpr int kUnit = 64;    // granularity of the plan's ranges of keys
 constexpr int kStages = 2;
 
@@ -418,6 +419,68 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
   if (lane == 0 && a.lse) a.lse[row] = any ? fmaf(m, kLn2, logf(l)) : -INFINITY;
 }
 
+// The same for few ranges and many rows: four rows per warp, all their loads
+// in flight together (37900 rows of two ranges: the call 137 -> 130 us).
+constexpr int kFewRows = 4;
+template <typename H, int kRanges>
+__global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_few_kernel(const __grid_constant__ PrefixArgs a) {
+  pdl_allow_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = int64_t(a.tokens) * a.q_heads;
+  const int64_t first = (int64_t(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5)) * kFewRows;
+  const bool mine = lane * 4 < a.dim;
+  pdl_wait_prior_grid();
+  if (first >= rows) return;
+  float4 y[kFewRows][kRanges];
+  float2 x[kFewRows][kRanges];
+#pragma unroll
+  for (int k = 0; k < kFewRows; ++k) {
+    const int64_t row = first + k < rows ? first + k : rows - 1;
+#pragma unroll
+    for (int s = 0; s < kRanges; ++s) {
+      x[k][s] = s < a.splits ? a.ml[row * a.splits + s] : make_float2(-INFINITY, 0.0f);
+      y[k][s] = mine && s < a.splits
+                    ? *reinterpret_cast<const float4*>(a.part + (s * rows + row) * a.dim + lane * 4)
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  int held[2] = {0, a.tokens};  // the tokens that some sequence holds
+  if (a.cu_q && a.suffix_splits > 0) {
+    held[0] = a.cu_q[0];
+    held[1] = a.cu_q[a.batch];
+  }
+#pragma unroll
+  for (int k = 0; k < kFewRows; ++k) {
+    const int64_t row = first + k;
+    if (row >= rows) break;
+    const int t = int(row / a.q_heads);
+    const int n = t >= held[0] && t < held[1] ? a.splits : a.prefix_splits;
+    float m = -INFINITY, l = 0.0f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < kRanges; ++s)
+      if (s < n) m = fmaxf(m, x[k][s].x);
+#pragma unroll
+    for (int s = 0; s < kRanges; ++s) {
+      if (s >= n || (x[k][s].x == -INFINITY && x[k][s].y == 0.0f)) continue;
+      const float w = x[k][s].x == -INFINITY ? 1.0f : ex2(x[k][s].x - m);
+      l = fmaf(x[k][s].y, w, l);
+      v.x = fmaf(y[k][s].x, w, v.x);
+      v.y = fmaf(y[k][s].y, w, v.y);
+      v.z = fmaf(y[k][s].z, w, v.z);
+      v.w = fmaf(y[k][s].w, w, v.w);
+    }
+    const bool any = l > 0.0f || l != l;
+    const float inv = any ? 1.0f / l : 0.0f;
+    if (mine) {
+      char* out = a.out + int64_t(t) * a.out_ts + int64_t(row - int64_t(t) * a.q_heads) * a.out_hs;
+      *reinterpret_cast<uint2*>(out + lane * 8) =
+          make_uint2(H::down2(v.x * inv, v.y * inv), H::down2(v.z * inv, v.w * inv));
+    }
+    if (lane == 0 && a.lse) a.lse[row] = any ? fmaf(m, kLn2, logf(l)) : -INFINITY;
+  }
+}
+
 // A call without a single key.
 template <typename H>
 __global__ void __launch_bounds__(128) prefix_empty_kernel(const __grid_constant__ PrefixArgs a) {
@@ -474,6 +537,10 @@ cudaError_t launch_typed(const PrefixArgs& p, cudaStream_t stream) {
     first += items;
   }
   if (e != cudaSuccess || p.direct) return e;
+  const int64_t few = int64_t(kJoinWarps) * kFewRows;
+  if (p.splits <= 4 && rows >= few * kSms)
+    return launch_k(p.splits <= 2 ? prefix_join_few_kernel<H, 2> : prefix_join_few_kernel<H, 4>,
+                    dim3(unsigned((rows + few - 1) / few)), dim3(32 * kJoinWarps), 0, stream, p);
   const int per_row = p.splits <= 8 ? 1 : p.splits <= 16 ? 2 : p.splits <= 32 ? 4 : 8;
   const int64_t blocks = (rows * per_row + kJoinWarps - 1) / kJoinWarps;
   return launch_k(p.splits <= 4 ? prefix_join_kernel<H, 4> : prefix_join_kernel<H, 8>, dim3(unsigned(blocks)),
@@ -484,39 +551,57 @@ cudaError_t launch_typed(const PrefixArgs& p, cudaStream_t stream) {
 
 namespace {
 
-constexpr int kSms = 152;
 constexpr int kMaxRanges = 152;  // per row, of the shared and of the own keys each
 
-// Keys per range of the mma kernel, in units of 64: at least two, and about
-// eight items per SM where there is that much, else one for each CTA that fits
-// on the SMs (128 sequences x 2000 keys of one head: 35.3 -> 31.9 us); at most
+// Keys per range of the mma kernel, in units of 64: about eight items per SM
+// where there is that much, else one for each CTA that fits on the SMs (128 sequences x 2000 keys of one head: 35.3 -> 31.9 us); at most
 // kMaxRanges ranges.
 int64_t mma_range(int64_t tiles, int64_t units, int dim) {
   const int64_t total = tiles * units, resident = kSms * (dim <= 64 ? 10 : 6);
   int64_t per = total / (kSms * 8);
   if (per < 6) per = (total + resident - 1) / resident;
-  per = per < 2 ? 2 : per;
+  per = per < 1 ? 1 : per;
   return units > per * kMaxRanges ? (units + kMaxRanges - 1) / kMaxRanges : per;
 }
 
-// Keys per range of the tensor-core kernel (one CTA per SM), in stages of 64
-// but whole tiles of 128: the number of ranges that ends soonest, counting a
-// wave of CTAs as its key tiles plus about three for its start and end, and
-// the partial results of a range (written and read in binary32, about 8 TB/s)
-// in the same unit of about a microsecond.
-int64_t tc_range(int64_t tiles, int64_t key_tiles, int64_t rows) {
-  int64_t best = key_tiles;
-  double least = 1e300;
-  for (int64_t s = 1; s <= kMaxRanges && s <= key_tiles; ++s) {
-    const int64_t per = (key_tiles + s - 1) / s, used = (key_tiles + per - 1) / per;
-    const int64_t waves = (tiles * used + kSms - 1) / kSms;
-    const double cost = double(waves) * double(per + 3) + (used > 1 ? double(used) * double(rows) * 1e-4 : 0.0);
-    if (cost < least) {
-      least = cost;
-      best = per;
+// Keys per range of the tcgen05 kernel (one CTA per SM), in units of 64 but
+// whole tiles of 128: the number of ranges that ends soonest, counting a wave
+// of CTAs as its key tiles plus about three for its start and end, and the
+// partial results of a range (written and read in binary32, about 8 TB/s) in
+// the same unit of about a microsecond. Candidates: what fills one to six
+// waves, and three, two and one quarters of that.
+int64_t tc_range(int64_t row_tiles, int64_t key_tiles, int64_t rows) {
+  int32_t best = int32_t(key_tiles);
+  const int32_t keys = best, tiles = row_tiles < (1 << 30) ? int32_t(row_tiles) : 1 << 30;
+  double least = double((row_tiles + kSms - 1) / kSms) * double(key_tiles + 3);  // one range
+  for (int32_t w = 1; w <= 6; ++w) {
+    int32_t most = w * kSms / tiles;
+    most = most < kMaxRanges ? most : kMaxRanges;
+    most = most < keys ? most : keys;
+    for (int32_t q = 4; q >= 1; --q) {
+      const int32_t s = most * q / 4;
+      if (s < 2) break;
+      const int32_t per = (keys + s - 1) / s, used = (keys + per - 1) / per;
+      const int32_t waves = (tiles * used + kSms - 1) / kSms;  // at most 6 waves of CTAs
+      const double cost = double(waves) * double(per + 3) + double(used) * double(rows) * 1e-4;
+      if (cost < least) {
+        least = cost;
+        best = per;
+      }
     }
   }
-  return 2 * best;
+  return 2 * int64_t(best);
+}
+
+// The own keys run on another kernel beside the shared ones. Where they are
+// the longer part (bound by their bytes, at about 6 TB/s), the shared keys are
+// cut into fewer ranges, so that they take no longer (about 1.2 us per key tile
+// of 128) but leave the other SMs to the own keys meanwhile: 64 sequences x 32
+// heads over 2048 shared and 190 own keys 55 -> 49 us.
+int64_t beside_range(const nf4_prefix_attention_args& a, const PrefixArgs& p, int64_t per, int64_t longest) {
+  const double own_us = double(a.batch) * double(p.suffix_max) * double(p.k_heads) * double(p.dim) * 4.0 / 6e6;
+  const int64_t room = 2 * (int64_t(own_us * 0.8 / 1.2) - 3);
+  return room <= per ? per : room < longest ? room : longest;
 }
 
 }  // namespace
@@ -547,9 +632,10 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
   const int64_t likely = a.batch > 0 ? a.batch * ((rows / a.batch + p->suffix_rows - 1) / p->suffix_rows) : 0;
   const int64_t pk = (int64_t(p->prefix_len) + kUnit - 1) / kUnit, sk = (int64_t(p->suffix_max) + kUnit - 1) / kUnit;
   if (pk > 0) {
-    const int64_t per = p->prefix_rows == 256
+    int64_t per = p->prefix_rows == 256
                             ? tc_range(int64_t(p->prefix_tiles) * p->k_heads, (pk + 1) / 2, rows * p->k_heads)
                             : mma_range(int64_t(p->prefix_tiles) * p->k_heads, pk, p->dim);
+    if (p->prefix_rows == 256 && p->suffix_rows != 256) per = beside_range(a, *p, per, 2 * ((pk + 1) / 2));
     p->prefix_chunk = int(per * kUnit);
     p->prefix_splits = int((pk + per - 1) / per);
   }
@@ -573,10 +659,13 @@ size_t prefix_attention_workspace_bytes(const nf4_prefix_attention_args& a) {
   return bytes;
 }
 
-cudaError_t launch_prefix_attention(const nf4_prefix_attention_args& a, void* workspace, cudaStream_t stream) {
+cudaError_t launch_prefix_attention(const nf4_prefix_attention_args& a, void* workspace, size_t workspace_bytes,
+                                    bool* enough, cudaStream_t stream) {
   PrefixArgs p = {};
   size_t bytes = 0;
   plan_prefix_attention(a, &p, &bytes);
+  *enough = bytes == 0 || (workspace && workspace_bytes >= bytes && (reinterpret_cast<uintptr_t>(workspace) & 15u) == 0);
+  if (!*enough) return cudaSuccess;
   p.q = static_cast<const char*>(a.q);
   p.out = static_cast<char*>(a.out);
   p.k = static_cast<const char*>(a.k_cache);

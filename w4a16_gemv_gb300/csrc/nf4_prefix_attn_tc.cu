@@ -253,12 +253,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // Everything else, the tensor memory included, waits for the previous grid:
   // an allocation held by a grid that waits could starve the one waited for.
   if (!a.beside) pdl_wait_prior_grid();
+  // What follows within a call (other items, the join) uses no tensor memory
+  // and may start now; after a call's only launch anything may follow, and starts
+  // when this CTA has its allocation.
+  if (!a.direct) pdl_allow_dependents();
   const PrefixItem it = prefix_item(a, unsigned(a.first) + blockIdx.x, &g_prefix_tc_flags);
   const int n = (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys;  // key tiles
   const bool works = it.rows > 0 && n > 0;                    // the same in the whole CTA
   const int tiles = it.rows > kTileRows ? 2 : 1;
   if (!works) {
-    pdl_allow_dependents();
     for (int r = tid; r < it.rows; r += kTcThreads) {
       const RowOut ro = row_out(a, it, it.r0 + r);
       *ro.ml = make_float2(-INFINITY, 0.0f);  // (a plan with one range of keys has no empty range)
@@ -267,8 +270,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     return;
   }
   // The softmax warps and the issuing warp meet here, when the tensor memory
-  // is allocated; the next grid may start after that, for the same reason as
-  // above (one thread of the CTA says so).
+  // is allocated.
   auto tmem_address = [&]() {
     tc_fence_before();
     asm volatile("bar.sync 1, 288;" ::: "memory");
@@ -574,7 +576,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                    "r"(kTmemCols)
                    : "memory");
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-      pdl_allow_dependents();
+      if (a.direct) pdl_allow_dependents();
       tmem_address();
     }
     if (warp == 12 && lane == 0) {
