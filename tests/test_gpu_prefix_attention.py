@@ -138,6 +138,35 @@ def test_page_sizes_and_cache_orders(page, heads_first, batch):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("page", [12, 32])
+@pytest.mark.parametrize("batch", [2, 70])
+def test_keys_and_values_laid_out_apart(page, batch):
+    """k as [pages, heads, slots, dim], v as a slice of a wider [pages, slots, heads, dim]."""
+    c = Call(8, 2, 64, 300, [(b * 29) % 90 + 1 for b in range(batch)], [1] * batch, page=page, seed=18)
+    want = c.run()
+    c.k = c.k.transpose(1, 2).contiguous().transpose(1, 2)
+    wide = torch.full((c.v.shape[0], page + 3, 4, 64), float("nan"), dtype=c.v.dtype, device="cuda")
+    wide[:, 2:page + 2, 1:3] = c.v
+    c.v = wide[:, 2:page + 2, 1:3]
+    got = c.run()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    c.check(got)
+
+
+def test_one_cache_row_for_every_page():
+    """Strides of zero: all pages, slots and heads share one row, so that the output is that row."""
+    row = torch.randn(64, device="cuda").bfloat16()
+    cache = row.expand(9, 16, 2, 64)
+    q = torch.randn(40, 4, 64, device="cuda").bfloat16()
+    table = torch.arange(4, dtype=torch.int32, device="cuda")
+    own = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    lens = torch.tensor([17, 64], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 3, 40], dtype=torch.int32, device="cuda")
+    out = lib().nf4_prefix_attention(q, cache, cache, table, 60, own, lens, cu_q=cu)
+    # sums of equal values: within the weights' rounding (2^-8) and the result's own
+    assert ((out.double() - row.double()).abs() <= 2.0 ** -7 * row.double().abs() + 1e-30).all()
+
+
 @pytest.mark.parametrize("prefix", [1, 2, 15, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 513, 1025])
 @pytest.mark.parametrize("batch", [1, 30, 150])
 def test_prefix_lengths_around_tiles(prefix, batch):
