@@ -56,7 +56,7 @@ def _binding_command(out: str) -> list[str]:
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[a for d in dirs for a in ("-isystem", d)],
             os.path.join(CSRC, "attention_binding.cpp"), "-o", out, "-L", PKG, "-l:libnf4.so", "-L", libs, "-ltorch_python",
-            "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+            "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
 
 
 def build(force: bool = False, verbose: bool = False, extra: tuple[str, ...] = ()) -> str:

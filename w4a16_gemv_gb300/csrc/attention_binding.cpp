@@ -10,7 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -153,8 +153,9 @@ class Launch {
       stream_ = c10::cuda::getCurrentCUDAStream(dev_).stream();
     }
   }
-  at::Tensor empty(at::IntArrayRef shape, at::TensorOptions options) const {
-    at::Tensor t = at::empty(shape, options);
+  // (Through the dispatcher an allocation costs 1.3 us instead of 0.8.)
+  at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
+    at::Tensor t = at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, dev_), std::nullopt);
     if (other_ && t.numel() > 0) t.record_stream(c10::cuda::getStreamFromExternal(stream_, dev_).unwrap());
     return t;
   }
@@ -229,7 +230,7 @@ void fill_qk(const QkInputs& in, const Launch& on, bool append, nf4_qk_norm_rope
       *q_out = tensor(in.q_out, "q_out");
       check(*q_out, "q_out", type, shape, dev, false);
     } else {
-      *q_out = on.empty(shape, q.options());
+      *q_out = on.empty(shape, type);
     }
     a->q = q.data_ptr();
     a->q_token_stride = q.stride(0);
@@ -249,7 +250,7 @@ void fill_qk(const QkInputs& in, const Launch& on, bool append, nf4_qk_norm_rope
       *k_out = tensor(in.k_out, "k_out");
       check(*k_out, "k_out", type, k.sizes(), dev, false);
     } else {
-      *k_out = on.empty(k.sizes(), k.options());
+      *k_out = on.empty(k.sizes(), type);
     }
     a->k_out = k_out->data_ptr();
     a->k_out_token_stride = k_out->stride(0);
@@ -402,7 +403,7 @@ PyObject* py_prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t nargs
       out = tensor(v[9], "out");
       check(out, "out", q.scalar_type(), q.sizes(), dev, false);
     } else {
-      out = on.empty(q.sizes(), q.options());
+      out = on.empty(q.sizes(), q.scalar_type());
     }
     a.out = out.data_ptr();
     a.out_token_stride = out.stride(0);
@@ -411,7 +412,7 @@ PyObject* py_prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t nargs
     if (given(v[11]))
       a.lse = static_cast<float*>(flat(v[11], "lse", at::kFloat, {a.tokens, a.q_heads}, dev));
     else if (want_lse) {
-      lse = on.empty({a.tokens, a.q_heads}, q.options().dtype(at::kFloat));
+      lse = on.empty({a.tokens, a.q_heads}, at::kFloat);
       a.lse = lse.data_ptr<float>();
     }
     void* scratch = nullptr;
@@ -422,7 +423,7 @@ PyObject* py_prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t nargs
       scratch = ws.data_ptr();
       bytes = ws.nbytes();
     } else if ((bytes = nf4_prefix_attention_workspace_size(&a)) > 0) {
-      ws = on.empty({int64_t(bytes)}, q.options().dtype(at::kByte));
+      ws = on.empty({int64_t(bytes)}, at::kByte);
       scratch = ws.data_ptr();
     }
     const nf4_status st = nf4_prefix_attention(&a, scratch, bytes, on.stream());
