@@ -185,14 +185,16 @@ NF4_API size_t nf4_prefix_attention_workspace_size(const nf4_prefix_attention_ar
  * outputs of two identical calls are identical. Scores, the running maximum
  * and sum, and all partial outputs are binary32; the weights exp(s_j - m) are
  * rounded to dtype for the product with v; the result is rounded once.
+ * A NaN or infinity in k or v reaches every row that sees it; one in v of an
+ * own key may also reach rows of the same sequence that stand before it.
  * cu_q, lengths and pages are read on the device, so a recorded graph can be
  * replayed as sequences grow within suffix_pages_width. Lengths out of range
- * are clamped into it; rows that would read a page outside 0 .. num_pages - 1 are
- * undefined; both set bit 1 of the device error flags. Tokens that no sequence holds
- * attend to the prefix alone.
+ * are clamped into it; rows that would read a page outside 0 .. num_pages - 1
+ * are undefined; both set bit 1 of the device error flags. Tokens that no
+ * sequence holds attend to the prefix alone.
  *   workspace  device scratch of at least nf4_prefix_attention_workspace_size()
- *              bytes, 16-byte aligned; contents on entry are ignored. Calls that overlap
- *              in time need workspaces of their own.
+ *              bytes, 16-byte aligned; contents on entry are ignored. Calls
+ *              that overlap in time need workspaces of their own.
  * Errors: NF4_ERR_NULL, NF4_ERR_INVALID_SIZE, NF4_ERR_UNSUPPORTED_DTYPE,
  *   NF4_ERR_MISALIGNED (q, out or a cache not 16-byte aligned, a stride of
  *   theirs not a multiple of 8 elements, an index array not aligned to its element),
