@@ -161,7 +161,7 @@ typedef struct nf4_prefix_attention_args {
   int64_t batch;              /* 0 .. 2^20 */
   int64_t tokens;             /* 0 .. 2^24 */
   int64_t q_heads, k_heads;   /* k_heads >= 1 divides q_heads; query head h reads key/value head
-                                 h / (q_heads / k_heads) */
+                                 h / (q_heads / k_heads); tokens * q_heads at most 2^30 */
   int64_t head_dim;           /* a multiple of 8, 8 .. 128 */
   int64_t dtype;              /* NF4_BF16 or NF4_FP16: q, out and the cache */
   double scale;               /* of the scores, usually 1 / sqrt(head_dim); > 0 */

@@ -337,6 +337,26 @@ def test_indices_out_of_range():
     assert torch.equal(out[3], ref[0][3]) and torch.equal(lse[3], ref[1][3])
 
 
+@pytest.mark.parametrize("batch,tokens", [(5, 5), (300, 700), (40, 3000)])
+def test_any_cu_q(batch, tokens):
+    """Whatever stands in cu_q, nothing outside the tensors is read or written."""
+    nf4 = lib()
+    g = gen(19)
+    c = Call(6, 2, 64, 100, [1 + b % 40 for b in range(batch)], [0] * batch, seed=19, junk=0.0)
+    q = torch.randn(tokens, 6, 64, device="cuda", generator=g).bfloat16()
+    guard = torch.full((tokens + 2, 6, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    big = 2 ** 31 - 1
+    for cu in (torch.randint(-10, tokens + 10, (batch + 1,), device="cuda", generator=g),
+               torch.randint(-big, big, (batch + 1,), device="cuda", generator=g),
+               torch.tensor([0, big], device="cuda").repeat(batch)[:batch + 1],
+               torch.arange(batch + 1, device="cuda").flip(0)):
+        nf4.nf4_prefix_attention(q, c.k, c.v, c.prefix_pages, 100, c.suffix_pages, c.suffix_lens, cu_q=cu.int(),
+                                 out=guard[1:-1])
+        torch.cuda.synchronize()
+        assert (guard[0] == 7).all() and (guard[-1] == 7).all()
+        assert nf4.nf4_device_error_flags() == 2
+
+
 def test_cache_past_32_bits():
     """Pages whose offsets pass 2^32 elements."""
     page, hk, dim = 16, 2, 64

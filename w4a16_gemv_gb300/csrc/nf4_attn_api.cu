@@ -48,7 +48,7 @@ nf4_status check_attention_sizes(const nf4_prefix_attention_args& a) {
   if (!in(a.batch, 0, int64_t(1) << 20) || !in(a.tokens, 0, int64_t(1) << 24) || !in(a.k_heads, 1, 65535) ||
       !in(a.q_heads, 1, 65535) || a.q_heads % a.k_heads != 0)
     return NF4_ERR_INVALID_SIZE;
-  if (a.tokens * a.q_heads > kMaxIndex) return NF4_ERR_INVALID_SIZE;
+  if (a.tokens * a.q_heads > int64_t(1) << 30) return NF4_ERR_INVALID_SIZE;
   if (!in(a.head_dim, 8, 128) || a.head_dim % 8 != 0) return NF4_ERR_INVALID_SIZE;
   if (!in(a.num_pages, 0, kMaxIndex) || !in(a.page_size, 1, 65536)) return NF4_ERR_INVALID_SIZE;
   if (!in(a.prefix_len, 0, int64_t(1) << 30) || !in(a.suffix_pages_width, 0, (int64_t(1) << 30) / a.page_size) ||

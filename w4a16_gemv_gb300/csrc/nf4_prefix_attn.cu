@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(Shape<R>::kThreads) prefix_mma_kernel(const __
 // alone.
 constexpr int kJoinWarps = 8;
 template <typename H, int kBatch>
-__global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __grid_constant__ PrefixArgs a, int per_row) {
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    prefix_join_kernel(const __grid_constant__ PrefixArgs a, int per_row) {
   __shared__ float4 sv[kJoinWarps][32];
   __shared__ float sl[kJoinWarps];
   pdl_allow_dependents();
@@ -514,7 +515,8 @@ cudaError_t launch_mma(const PrefixArgs& p, unsigned items, cudaStream_t stream)
 
 template <typename H>
 cudaError_t launch_rows(const PrefixArgs& p, int rows, unsigned items, cudaStream_t stream) {
-  if (rows == 64) return p.dim <= 64 ? launch_mma<H, 64, 64>(p, items, stream) : launch_mma<H, 128, 64>(p, items, stream);
+  if (rows == 64)
+    return p.dim <= 64 ? launch_mma<H, 64, 64>(p, items, stream) : launch_mma<H, 128, 64>(p, items, stream);
   return p.dim <= 64 ? launch_mma<H, 64, 16>(p, items, stream) : launch_mma<H, 128, 16>(p, items, stream);
 }
 
@@ -561,8 +563,8 @@ namespace {
 constexpr int kMaxRanges = 152;  // per row, of the shared and of the own keys each
 
 // Keys per range of the mma kernel, in units of 64: about eight items per SM
-// where there is that much, else one for each CTA that fits on the SMs (128 sequences x 2000 keys of one head: 35.3 -> 31.9 us); at most
-// kMaxRanges ranges.
+// where there is that much, else one for each CTA that fits on the SMs (128
+// sequences x 2000 keys of one head: 35.3 -> 31.9 us); at most kMaxRanges ranges.
 int64_t mma_range(int64_t tiles, int64_t units, int dim) {
   const int64_t total = tiles * units, resident = kSms * (dim <= 64 ? 10 : 6);
   int64_t per = total / (kSms * 8);
@@ -671,7 +673,8 @@ cudaError_t launch_prefix_attention(const nf4_prefix_attention_args& a, void* wo
   PrefixArgs p = {};
   size_t bytes = 0;
   plan_prefix_attention(a, &p, &bytes);
-  *enough = bytes == 0 || (workspace && workspace_bytes >= bytes && (reinterpret_cast<uintptr_t>(workspace) & 15u) == 0);
+  *enough =
+      bytes == 0 || (workspace && workspace_bytes >= bytes && (reinterpret_cast<uintptr_t>(workspace) & 15u) == 0);
   if (!*enough) return cudaSuccess;
   p.q = static_cast<const char*>(a.q);
   p.out = static_cast<char*>(a.out);

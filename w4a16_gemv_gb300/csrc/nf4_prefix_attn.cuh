@@ -68,6 +68,8 @@ __device__ __forceinline__ int visible_keys(const PrefixItem& it, int i) {
   return it.own ? min(max(it.len - it.n + i + 1, 0), it.len) : it.len;
 }
 
+constexpr int kMostTiles = 1 << 30;
+
 // Item `index` of a launch that covers prefix items first (a key/value head's
 // tiles of one key range side by side, so that they meet in L2), then suffix
 // items. Tiles of the suffix are numbered along the batch; every warp finds
@@ -120,7 +122,7 @@ __device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, unsigned 
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += o;
+      if (lane >= d) upto = min(upto + o, kMostTiles);  // a falling cu_q must not overflow the sums
     }
     const unsigned past = __ballot_sync(0xffffffffu, before + upto > tile);
     if (past) {
@@ -129,7 +131,9 @@ __device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, unsigned 
       const int seq = b0 + src;
       it.t0 = __shfl_sync(0xffffffffu, lo, src);
       it.n = __shfl_sync(0xffffffffu, hi, src) - it.t0;
-      it.r0 = (tile - first) * a.suffix_rows;
+      const int64_t r0 = int64_t(tile - first) * a.suffix_rows;
+      if (r0 < 0 || r0 >= int64_t(it.n) * a.group) return it;  // (nor make a row where there is none)
+      it.r0 = int(r0);
       it.rows = min(a.suffix_rows, it.n * a.group - it.r0);
       const int len = __shfl_sync(0xffffffffu, length, src);
       it.len = min(max(len, 0), a.suffix_max);
@@ -140,7 +144,7 @@ __device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, unsigned 
       it.k1 = int(min(int64_t(it.k0) + a.suffix_chunk, int64_t(sees)));
       return it;
     }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    before = min(before + __shfl_sync(0xffffffffu, upto, 31), kMostTiles);
   }
   return it;
 }

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();  // the barriers exist; from here the warps start their parts as they can
   // Everything else, the tensor memory included, waits for the previous grid:
   // an allocation held by a grid that waits could starve the one waited for.
-  if (!a.beside) pdl_wait_prior_grid();
+  pdl_wait_prior_grid();
   // What follows within a call (other items, the join) uses no tensor memory
   // and may start now; after a call's only launch anything may follow, and starts
   // when this CTA has its allocation.
@@ -270,7 +270,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const RowOut ro = row_out(a, it, it.r0 + r);
       *ro.ml = make_float2(-INFINITY, 0.0f);  // (a plan with one range of keys has no empty range)
     }
-    if (a.beside && blockIdx.x + 1 == gridDim.x) pdl_wait_prior_grid();
     return;
   }
   // The softmax warps and the issuing warp meet here, when the tensor memory
@@ -304,7 +303,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int rl = x * kQStep + lane / kQChunks, row = (warp & 3) * 32 + rl;
         const int64_t o = __shfl_sync(0xffffffffu, off, rl);
         const bool there = warp * 32 + rl < it.rows && c * 8 < a.dim;
-        cp_async16(dst + uint32_t(row) * 128u + uint32_t(((c & 7) ^ (row & 7)) << 4), there ? a.q + o + c * 16 : a.q, there);
+        cp_async16(dst + uint32_t(row) * 128u + uint32_t(((c & 7) ^ (row & 7)) << 4),
+                   there ? a.q + o + c * 16 : a.q, there);
       }
       cp_async_commit();
     }
@@ -482,7 +482,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       fetch(0, &page, &slot0);
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
-        if (unsigned(page) > unsigned(a.num_pages) || (page == a.num_pages && mine && it.k0 + i * kTileKeys + box * rows < it.k1)) {
+        const bool used = mine && it.k0 + i * kTileKeys + box * rows < it.k1;
+        if (used && unsigned(page) >= unsigned(a.num_pages)) {
           atomicOr(&g_prefix_tc_flags, kFlagBadIndex);
           page = a.num_pages;
         }
@@ -496,7 +497,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 : clean && i + 1 == n ? tail : &go[i % kGo];
           if (lane == 0) mbar_arrive_expect_tx(bar, L::kTile);
           __syncwarp();
-          const uint32_t dst = sbase + L::kRing + uint32_t(slot) * L::kTile + uint32_t(block) * L::kBlock + uint32_t(box * rows) * 128u;
+          const uint32_t dst = sbase + L::kRing + uint32_t(slot) * L::kTile + uint32_t(block) * L::kBlock +
+                               uint32_t(box * rows) * 128u;
           if (mine) {
             if (kv == 0)
               tma_load_box(dst, &maps.k, block * 64, maps.k_slot, maps.k_head, slot0, it.head, page, bar);
@@ -556,7 +558,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int64_t o = __shfl_sync(0xffffffffu, mine, rl);
         const bool there = __shfl_sync(0xffffffffu, int(real), rl) && col;
         const int row = w * 32 + rl;
-        cp_async16(dst + uint32_t(row) * 128u + uint32_t(((c & 7) ^ (row & 7)) << 4), there ? src + o + c * 16 : a.q, there);
+        cp_async16(dst + uint32_t(row) * 128u + uint32_t(((c & 7) ^ (row & 7)) << 4),
+                   there ? src + o + c * 16 : a.q, there);
       }
       cp_async_commit();
       if (u >= L::kLag) {
@@ -616,8 +619,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int s = 0; s < kTileKeys / 16; ++s)  // 16 keys: two groups of eight rows
-            mma_ts(tbase + 256u + uint32_t(t) * 128u, tbase + uint32_t(t) * 128u + 8u * s, vd + uint64_t(s * (2048 >> 4)),
-                   kIdO, (i > 0 || s > 0) ? 1u : 0u);
+            mma_ts(tbase + 256u + uint32_t(t) * 128u, tbase + uint32_t(t) * 128u + 8u * s,
+                   vd + uint64_t(s * (2048 >> 4)), kIdO, (i > 0 || s > 0) ? 1u : 0u);
           const bool end = t + 1 == tiles;
           if (end) tc_commit(&empty[uv % L::kStages]);
           if (i + 1 < n) {
@@ -645,7 +648,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*s_taddr), "r"(kTmemCols) : "memory");
   }
-  if (a.beside && blockIdx.x + 1 == gridDim.x) pdl_wait_prior_grid();
 }
 
 template <typename H, int DP, bool kTma>
