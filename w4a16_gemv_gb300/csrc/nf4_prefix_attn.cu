@@ -28,17 +28,19 @@ constexpr int kSms = 152;
 constexpr int kUnit = 64;    // granularity of the plan's ranges of keys
 constexpr int kStages = 2;
 
-// Tiles of 64 rows: four warps with 16 rows each and all keys of a stage of
-// 64. Tiles of 16 rows: two warps that share the rows and have half the keys of
-// a stage of 32 each; small CTAs (48 KB at 128 elements), so that four are on an SM
-// and the start of one (three dependent loads before its first keys) hides
-// behind the keys of the others.
-template <int R>
+// R rows per tile, W warps. R = 64: a warp has 16 rows and all keys of a stage
+// of 64. R = 16: the warps share the rows and have 16 keys of a stage each.
+// Where there are enough items, two warps: small CTAs (32 KB at 128 elements), so
+// that six are on an SM and the start of one (three dependent loads before its
+// first keys) hides behind the keys of the others. Where all items fit on the
+// SMs at once, four: a short range is one stage (two sequences over 300 keys
+// 6.9 -> 5.8 us; 32 over 500 own keys each would take 12 instead of 10.4).
+template <int R, int W>
 struct Shape {
-  static constexpr int kWarps = R == 64 ? 4 : 2;
-  static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kKeys = R == 64 ? 64 : 32;  // keys per stage
+  static constexpr int kThreads = 32 * W;
+  static constexpr int kKeys = R == 64 ? 64 : 16 * W;  // keys per stage
 };
+constexpr int64_t kFewItems = kSms * 3;  // CTAs of four warps that fit on the SMs
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -68,9 +70,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 // One item with tiles of R rows. The warps' key shares of R = 16 are joined
 // through shared memory at the end.
-template <typename H, int DP, int R>
+template <typename H, int DP, int R, int W>
 __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it, unsigned char* smem) {
-  constexpr int kWarps = Shape<R>::kWarps, kThreads = Shape<R>::kThreads, kKeys = Shape<R>::kKeys;
+  constexpr int kWarps = W, kThreads = Shape<R, W>::kThreads, kKeys = Shape<R, W>::kKeys;
   constexpr int KW = R == 64 ? kKeys : kKeys / kWarps;  // keys of a stage per warp
   constexpr int NB = KW / 8;                            // score blocks of 8 keys
   constexpr int CPR = DP / 8;                           // 16-byte chunks per row
@@ -336,26 +338,27 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
 // ahead of letting this one start, so there is nothing to wait for here; but
 // what follows (the join) only waits for this launch, so its last CTA ends
 // after the other launch did.
-template <typename H, int DP, int R>
-__global__ void __launch_bounds__(Shape<R>::kThreads) prefix_mma_kernel(const __grid_constant__ PrefixArgs a) {
+template <typename H, int DP, int R, int W>
+__global__ void __launch_bounds__(Shape<R, W>::kThreads) prefix_mma_kernel(const __grid_constant__ PrefixArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   if (!a.beside) pdl_wait_prior_grid();
   pdl_allow_dependents();
   const PrefixItem it = prefix_item(a, unsigned(a.first) + blockIdx.x, &g_prefix_flags);
-  if (it.rows > 0) attend<H, DP, R>(a, it, smem);
+  if (it.rows > 0) attend<H, DP, R, W>(a, it, smem);
   if (a.beside && blockIdx.x + 1 == gridDim.x) pdl_wait_prior_grid();
 }
 
-// Joins a row's partial results: 1 to 8 warps per row (the more ranges, the
-// more), four elements per lane, kBatch ranges in flight per warp. The partial
-// outputs are asked for together with the maxima and sums, not after them
-// (those of ranges that hold nothing are read and dropped): one latency, which
-// is most of this kernel's time. The order of the sums depends on the plan
-// alone.
+// Joins a row's partial results: 1 to 8 warps per row, four elements per lane,
+// kBatch ranges per warp and round; the launch takes as many warps as make one
+// round (up to 128 ranges). The partial outputs are asked for together with the
+// maxima and sums, not after them (those of ranges that hold nothing are read and
+// dropped): one latency, which is most of this kernel's time. The order of
+// the sums depends on the plan alone.
 constexpr int kJoinWarps = 8;
 template <typename H, int kBatch>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     prefix_join_kernel(const __grid_constant__ PrefixArgs a, int per_row) {
+  static_assert(kBatch <= 32, "a lane per range of a round");
   __shared__ float4 sv[kJoinWarps][32];
   __shared__ float sl[kJoinWarps];
   pdl_allow_dependents();
@@ -370,10 +373,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   float l = 0.0f, m = -INFINITY;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (there) {
-    int n = a.splits;
     const float2* ml = a.ml + row * a.splits;
     const float* src = a.part + row * a.dim + lane * 4;
     const int64_t step = rows * a.dim;
+    int n = a.splits;
     float4 y[kBatch];
     auto load = [&](int s0) {
 #pragma unroll
@@ -382,23 +385,38 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     load(share * kBatch);
+    // this lane's range of the first round, and everybody's maxima
+    float2 x = share * kBatch + lane < n ? ml[share * kBatch + lane] : make_float2(-INFINITY, 0.0f);
+    float all[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) all[i] = 32 * i + lane < n ? ml[32 * i + lane].x : -INFINITY;
     if (a.cu_q && a.suffix_splits > 0 && (t < a.cu_q[0] || t >= a.cu_q[a.batch])) n = a.prefix_splits;
-    for (int s = lane; s < n; s += 32) m = fmaxf(m, ml[s].x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (32 * i + lane < n) m = fmaxf(m, all[i]);
+    for (int s = 128 + lane; s < n; s += 32) m = fmaxf(m, ml[s].x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     for (int s0 = share * kBatch; s0 < n; s0 += per_row * kBatch) {
-      if (s0 > share * kBatch) load(s0);
+      if (s0 > share * kBatch) {
+        load(s0);
+        x = s0 + lane < n ? ml[s0 + lane] : make_float2(-INFINITY, 0.0f);
+      }
+      // the range's weight; 0: it holds nothing, and its partial output is not to be looked at
+      const bool holds = s0 + lane < n && lane < kBatch && !(x.x == -INFINITY && x.y == 0.0f);
+      const float w = !holds ? 0.0f : x.x == -INFINITY ? 1.0f : ex2(x.x - m);
+      const unsigned which = __ballot_sync(0xffffffffu, holds);
+      const float part_l = holds ? x.y * w : 0.0f;
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const float2 x = s0 + u < n ? ml[s0 + u] : make_float2(-INFINITY, 0.0f);
-        // a range that holds nothing has no partial output to speak of
-        if (x.x == -INFINITY && x.y == 0.0f) continue;
-        const float w = x.x == -INFINITY ? 1.0f : ex2(x.x - m);
-        l = fmaf(x.y, w, l);
-        v.x = fmaf(y[u].x, w, v.x);
-        v.y = fmaf(y[u].y, w, v.y);
-        v.z = fmaf(y[u].z, w, v.z);
-        v.w = fmaf(y[u].w, w, v.w);
+        const float wu = __shfl_sync(0xffffffffu, w, u);
+        l += __shfl_sync(0xffffffffu, part_l, u);
+        if (which >> u & 1u) {
+          v.x = fmaf(y[u].x, wu, v.x);
+          v.y = fmaf(y[u].y, wu, v.y);
+          v.z = fmaf(y[u].z, wu, v.z);
+          v.w = fmaf(y[u].w, wu, v.w);
+        }
       }
     }
   }
@@ -503,21 +521,20 @@ __global__ void __launch_bounds__(128) prefix_empty_kernel(const __grid_constant
   if (lane == 0 && a.lse) a.lse[row] = -INFINITY;
 }
 
-template <typename H, int DP, int R>
+template <typename H, int DP, int R, int W>
 cudaError_t launch_mma(const PrefixArgs& p, unsigned items, cudaStream_t stream) {
-  auto kern = prefix_mma_kernel<H, DP, R>;
-  constexpr int smem = kStages * 2 * Shape<R>::kKeys * DP * 2;
+  auto kern = prefix_mma_kernel<H, DP, R, W>;
+  constexpr int smem = kStages * 2 * Shape<R, W>::kKeys * DP * 2;
   static PerDeviceCache attr_set;
   const cudaError_t e = set_max_dynamic_smem_once(kern, smem, attr_set);
   if (e != cudaSuccess) return e;
-  return launch_k(kern, dim3(items), dim3(Shape<R>::kThreads), smem, stream, p);
+  return launch_k(kern, dim3(items), dim3(Shape<R, W>::kThreads), smem, stream, p);
 }
 
-template <typename H>
+template <typename H, int DP>
 cudaError_t launch_rows(const PrefixArgs& p, int rows, unsigned items, cudaStream_t stream) {
-  if (rows == 64)
-    return p.dim <= 64 ? launch_mma<H, 64, 64>(p, items, stream) : launch_mma<H, 128, 64>(p, items, stream);
-  return p.dim <= 64 ? launch_mma<H, 64, 16>(p, items, stream) : launch_mma<H, 128, 16>(p, items, stream);
+  if (rows == 64) return launch_mma<H, DP, 64, 4>(p, items, stream);
+  return items <= kFewItems ? launch_mma<H, DP, 16, 4>(p, items, stream) : launch_mma<H, DP, 16, 2>(p, items, stream);
 }
 
 template <typename H>
@@ -542,7 +559,8 @@ cudaError_t launch_typed(const PrefixArgs& p, cudaStream_t stream) {
     q.first = int(first);
     q.beside = first > 0;
     e = tile == 256 ? launch_prefix_tc(q, H::kDtype, unsigned(items), stream)
-                    : launch_rows<H>(q, tile, unsigned(items), stream);
+        : p.dim <= 64 ? launch_rows<H, 64>(q, tile, unsigned(items), stream)
+                      : launch_rows<H, 128>(q, tile, unsigned(items), stream);
     first += items;
   }
   if (e != cudaSuccess || p.direct) return e;
@@ -550,10 +568,13 @@ cudaError_t launch_typed(const PrefixArgs& p, cudaStream_t stream) {
   if (p.splits <= 4 && rows >= few * kSms)
     return launch_k(p.splits <= 2 ? prefix_join_few_kernel<H, 2> : prefix_join_few_kernel<H, 4>,
                     dim3(unsigned((rows + few - 1) / few)), dim3(32 * kJoinWarps), 0, stream, p);
-  const int per_row = p.splits <= 8 ? 1 : p.splits <= 16 ? 2 : p.splits <= 32 ? 4 : 8;
+  int per_row = 1;
+  while (per_row < kJoinWarps && per_row * 8 < p.splits) per_row *= 2;
   const int64_t blocks = (rows * per_row + kJoinWarps - 1) / kJoinWarps;
-  return launch_k(p.splits <= 4 ? prefix_join_kernel<H, 4> : prefix_join_kernel<H, 8>, dim3(unsigned(blocks)),
-                  dim3(32 * kJoinWarps), 0, stream, p, per_row);
+  return launch_k(p.splits <= 4    ? prefix_join_kernel<H, 4>
+                  : p.splits <= 64 ? prefix_join_kernel<H, 8>
+                                   : prefix_join_kernel<H, 16>,
+                  dim3(unsigned(blocks)), dim3(32 * kJoinWarps), 0, stream, p, per_row);
 }
 
 }  // namespace
@@ -579,19 +600,19 @@ int64_t mma_range(int64_t tiles, int64_t units, int dim) {
 // partial results of a range (written and read in binary32, about 8 TB/s) in
 // the same unit of about a microsecond. Candidates: what fills one to six
 // waves, and three, two and one quarters of that.
-int64_t tc_range(int64_t row_tiles, int64_t key_tiles, int64_t rows) {
+int64_t tc_range(int64_t row_tiles, int64_t key_tiles, int64_t rows, int sms) {
   int32_t best = int32_t(key_tiles);
   const int32_t keys = best, tiles = row_tiles < (1 << 30) ? int32_t(row_tiles) : 1 << 30;
-  double least = double((row_tiles + kSms - 1) / kSms) * double(key_tiles + 3);  // one range
+  double least = double((row_tiles + sms - 1) / sms) * double(key_tiles + 3);  // one range
   for (int32_t w = 1; w <= 6; ++w) {
-    int32_t most = w * kSms / tiles;
+    int32_t most = w * sms / tiles;
     most = most < kMaxRanges ? most : kMaxRanges;
     most = most < keys ? most : keys;
     for (int32_t q = 4; q >= 1; --q) {
       const int32_t s = most * q / 4;
       if (s < 2) break;
       const int32_t per = (keys + s - 1) / s, used = (keys + per - 1) / per;
-      const int32_t waves = (tiles * used + kSms - 1) / kSms;  // at most 6 waves of CTAs
+      const int32_t waves = (tiles * used + sms - 1) / sms;  // at most 6 waves of CTAs
       const double cost = double(waves) * double(per + 3) + double(used) * double(rows) * 1e-4;
       if (cost < least) {
         least = cost;
@@ -611,6 +632,17 @@ int64_t beside_range(const nf4_prefix_attention_args& a, const PrefixArgs& p, in
   const double own_us = double(a.batch) * double(p.suffix_max) * double(p.k_heads) * double(p.dim) * 4.0 / 6e6;
   const int64_t room = 2 * (int64_t(own_us * 0.8 / 1.2) - 3);
   return room <= per ? per : room < longest ? room : longest;
+}
+
+// Where the shared keys would take every SM once, and the own keys are little
+// work: the SMs to leave to them, so that they end meanwhile (a CTA of theirs
+// takes about 5 us, three or six run on an SM; a key tile about 1.5 us). 0: none.
+int sms_for_own(const PrefixArgs& p, int64_t own_items, int64_t tiles, int64_t per, int64_t units) {
+  const int64_t ctas = tiles * ((units + per - 1) / per);
+  if (ctas > kSms) return 0;
+  const double own = double(own_items) * (own_items <= kFewItems ? 5.0 / 3.0 : 5.0 / 6.0);
+  const double keep = own / ((double(per) * 0.5 + 3.0) * 1.5) + 1.0;
+  return keep < kSms / 8 && ctas > kSms - int64_t(keep) ? int(keep) : 0;
 }
 
 }  // namespace
@@ -640,19 +672,28 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
   // as many as there are when the tokens are spread evenly (the ranges are made for these)
   const int64_t likely = a.batch > 0 ? a.batch * ((rows / a.batch + p->suffix_rows - 1) / p->suffix_rows) : 0;
   const int64_t pk = (int64_t(p->prefix_len) + kUnit - 1) / kUnit, sk = (int64_t(p->suffix_max) + kUnit - 1) / kUnit;
-  if (pk > 0) {
-    int64_t per = p->prefix_rows == 256
-                            ? tc_range(int64_t(p->prefix_tiles) * p->k_heads, (pk + 1) / 2, rows * p->k_heads)
-                            : mma_range(int64_t(p->prefix_tiles) * p->k_heads, pk, p->dim);
-    if (p->prefix_rows == 256 && p->suffix_rows != 256) per = beside_range(a, *p, per, 2 * ((pk + 1) / 2));
-    p->prefix_chunk = int(per * kUnit);
-    p->prefix_splits = int((pk + per - 1) / per);
-  }
   if (sk > 0) {
-    const int64_t per = p->suffix_rows == 256 ? tc_range(likely * p->k_heads, (sk + 1) / 2, rows * p->k_heads)
+    const int64_t per = p->suffix_rows == 256 ? tc_range(likely * p->k_heads, (sk + 1) / 2, rows * p->k_heads, kSms)
                                               : mma_range(likely * p->k_heads, sk, p->dim);
     p->suffix_chunk = int(per * kUnit);
     p->suffix_splits = int((sk + per - 1) / per);
+  }
+  if (pk > 0) {
+    const int64_t tiles = int64_t(p->prefix_tiles) * p->k_heads;
+    int64_t per;
+    if (p->prefix_rows != 256) {
+      per = mma_range(tiles, pk, p->dim);
+    } else {
+      const int64_t longest = (pk + 1) / 2;
+      per = tc_range(tiles, longest, rows * p->k_heads, kSms);
+      if (p->suffix_rows != 256 && sk > 0) {
+        per = beside_range(a, *p, per, 2 * longest);
+        const int keep = sms_for_own(*p, likely * p->k_heads * p->suffix_splits, tiles, per, pk);
+        if (keep > 0) per = tc_range(tiles, longest, rows * p->k_heads, kSms - keep);
+      }
+    }
+    p->prefix_chunk = int(per * kUnit);
+    p->prefix_splits = int((pk + per - 1) / per);
   }
   if (rows == 0) p->prefix_splits = p->suffix_splits = 0;
   p->splits = p->prefix_splits + p->suffix_splits;
