@@ -15,9 +15,10 @@
 // lane's registers: no shared memory, and an output may be its input. A warp
 // takes one token: the weights times the token's cosines and sines are formed
 // once and serve all the heads that the warp walks over (two multiplications
-// and additions per element, packed two to an instruction), and the next row
-// is asked for before the present one is worked on. 8192 tokens x 64 heads of
-// 128 in bf16 take 51.6 us (5.3 TB/s, 79% of measured copy bandwidth).
+// and additions per element, packed two to an instruction), and the next four
+// rows are under way in shared memory, each lane reading back only what it
+// brought. 8192 tokens x 64 heads of 128 in bf16 take 45.2 us (6.0 TB/s, 90% of
+// measured copy bandwidth), an append of 8000 x 96 heads 62.4 us (95%).
 #include <math.h>
 
 #include <initializer_list>
@@ -183,6 +184,15 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Where a token's key and value go: the first byte of (slot, head 0) of each
 // cache. False: nowhere (a negative slot, or one past the cache, which is
 // reported).
@@ -206,11 +216,14 @@ __device__ __forceinline__ bool slot_base(const RopeArgs& a, int64_t slot, int s
 }
 
 constexpr int kRopeThreads = 128;
-// Blocks of four warps, six on an SM (80 registers): more warps beat more rows
-// in flight per warp (8192 tokens x 64 heads of 128, bf16, us: 4 rows and 4
-// blocks 60.3, 2 and 5 54.3, 1 and 6 51.6, 1 and 8 55.9).
-constexpr int kRopeBlocks = 6;
-constexpr int kMaxPerWarp = 8;  // row groups that one warp walks over (16: 54.9 us)
+// Blocks of four warps, five on an SM (96 registers), four rows under way per
+// warp through shared memory. 8192 tokens x 64 heads of 128 in bf16, us: rows
+// under way in registers, the next one only, 51.6, four 60.3 (too few warps);
+// through shared memory two 48.0, four 45.2, six 46.1 (and with six blocks 46.0,
+// with eight, whose 64 registers spill, 51.4).
+constexpr int kRopeBlocks = 5;
+constexpr int kInFlight = 4;
+constexpr int kMaxPerWarp = 8;  // row groups that one warp walks over (16: 48 us, 4: 55 us)
 
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_rows_kernel(const __grid_constant__ RopeArgs a) {
@@ -252,19 +265,24 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_rows_kernel(co
     return Part{r.in + int64_t(t) * r.in_ts * E::kSize + c0, max(g - first, 0),
                 min(g_end - first, n), r.heads - 1, r.in_hs * E::kSize};
   };
-  uint4 x0 = {}, x1 = {};
+  // Rows under way, in shared memory; every lane reads back only what it brought.
+  __shared__ __align__(16) uint4 ring[kRopeThreads / 32][kInFlight][2][32];
+  auto& mine = ring[threadIdx.x >> 5];
   auto load = [&](const Part& s, int gi) {
     if (gi < s.to) {
       const char* p = s.src + int64_t(min(gi * rows + sub, s.last)) * s.head_step;
-      x0 = *reinterpret_cast<const uint4*>(p);
-      x1 = *reinterpret_cast<const uint4*>(p + c1);
+      const int slot = (gi - s.from) % kInFlight;
+      copy16(smem_u32(&mine[slot][0][lane]), p);
+      copy16(smem_u32(&mine[slot][1][lane]), p + c1);
     }
+    copy_commit();
   };
   // the first rows are on their way before the position and its table row are asked for
   const int kind0 = g < a.gq ? 0 : g < a.gq + a.gk ? 1 : 2;
   {
     const Part s = part_of(kind0);
-    load(s, s.from);
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) load(s, s.from + u);
   }
 
   const int64_t slot = a.slots ? a.slots[t] : 0;
@@ -279,7 +297,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_rows_kernel(co
   for (int kind = kind0; kind < 3; ++kind) {
     const Part s = part_of(kind);
     if (s.from >= s.to || (kind > 0 && !stored)) continue;
-    if (kind != kind0) load(s, s.from);
+    if (kind != kind0) {
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) load(s, s.from + u);
+    }
     char* dst = kind == 0   ? a.q.out + int64_t(t) * a.q.out_ts * E::kSize
                 : !a.slots  ? a.k.out + int64_t(t) * a.k.out_ts * E::kSize
                 : kind == 1 ? kdst
@@ -315,8 +336,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_rows_kernel(co
     }
 
     for (int gi = s.from; gi < s.to; ++gi) {
-      uint4 y0 = x0, y1 = x1;
-      load(s, gi + 1);
+      copy_wait<kInFlight - 1>();
+      const int slot = (gi - s.from) % kInFlight;
+      uint4 y0 = mine[slot][0][lane], y1 = mine[slot][1][lane];
       if (kind < 2) {
         float fa[P], fb[P];
         E::template up<kInterleaved>(y0, y1, fa, fb);
@@ -364,7 +386,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_rows_kernel(co
         *reinterpret_cast<uint4*>(p) = y0;
         *reinterpret_cast<uint4*>(p + c1) = y1;
       }
+      load(s, gi + kInFlight);
     }
+    copy_wait<0>();
   }
 }
 
@@ -459,13 +483,13 @@ cudaError_t launch_rows(RopeArgs& a, cudaStream_t stream) {
   a.gq = (a.q.heads + rows - 1) / rows;
   a.gk = (a.k.heads + rows - 1) / rows;
   a.gv = (a.v.heads + rows - 1) / rows;
-  // Groups per warp: one while that does not fill the SMs (24 warps each),
-  // more when there is plenty, so that a warp's table row and weights serve
-  // several groups.
+  // Warps per token: as many as fill the SMs twice, one per group at most; for
+  // many tokens as few as kMaxPerWarp allows, so that a warp's table row and
+  // weights serve several groups.
   const int groups = a.gq + a.gk + a.gv;
-  int64_t per = int64_t(a.tokens) * groups / (152 * 24);
-  per = per < 1 ? 1 : per > kMaxPerWarp ? kMaxPerWarp : per;
-  a.parts = int((groups + per - 1) / per);
+  const int64_t resident = 152 * kRopeBlocks * (kRopeThreads / 32);
+  const int64_t least = (groups + kMaxPerWarp - 1) / kMaxPerWarp, fit = 2 * resident / a.tokens;
+  a.parts = int(fit < least ? least : fit < groups ? fit : groups);
   a.per_warp = (groups + a.parts - 1) / a.parts;
   const int64_t blocks = (int64_t(a.tokens) * a.parts + per_block - 1) / per_block;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
