@@ -175,6 +175,58 @@ def test_in_place_one_weight_and_odd_strides(dim, rot, interleaved):
         assert torch.equal(buf[~touched], before[~touched])
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16, torch.float32], ids=["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("interleaved", [False, True], ids=["half", "interleaved"])
+@pytest.mark.parametrize("tokens,hq,hk,dim,rot,shift", [
+    (70, 10, 2, 80, 40, 0), (11, 3, 1, 8, 8, 0), (6, 5, 3, 24, 8, 0), (9, 4, 4, 256, 40, 0), (3, 2, 1, 264, 24, 0),
+    (13, 6, 2, 128, 128, 4), (13, 6, 2, 128, 64, 2), (900, 7, 3, 80, 40, 4), (3100, 2, 1, 40, 24, 0)])
+def test_rows_that_fit_smaller_chunks(dt, interleaved, tokens, hq, hk, dim, rot, shift):
+    """Rotated parts, offsets and strides that are multiples of 8 bytes only (and, shift 2, of 4 or 8)."""
+    _, _, _, pos, qw, kw = inputs(tokens, hq, hk, dim, dt, dim + rot, 700)
+    ts, hs = (hq + hk + 1) * (dim + shift) + shift, dim + shift
+    buf = torch.randn(tokens * ts + 2 * shift, device="cuda", generator=gen(rot)).to(dt)
+    q = buf.as_strided((tokens, hq, dim), (ts, hs, 1), shift)
+    k = buf.as_strided((tokens, hk, dim), (ts, hs, 1), shift + hq * hs)
+    before = buf.clone()
+    t = lib().nf4_rope_table(700, rot)
+    cos, sin = angles(pos, frequencies(rot))
+    for wq, wk in ((qw, kw), (None, kw)):
+        qo, ko = lib().nf4_qk_norm_rope(q, k, pos, t, q_weight=wq, k_weight=wk, interleaved=interleaved)
+        check(qo, expected(q, wq, cos, sin, interleaved, 1e-6), "q")
+        check(ko, expected(k, wk, cos, sin, interleaved, 1e-6), "k")
+    want = qo.clone(), ko.clone()
+    lib().nf4_qk_norm_rope(q, k, pos, t, k_weight=kw, interleaved=interleaved, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    touched = torch.zeros_like(buf, dtype=torch.bool)
+    for x in (q, k):
+        touched.as_strided(x.shape, x.stride(), x.storage_offset()).fill_(True)
+    assert torch.equal(buf[~touched], before[~touched])
+
+
+@pytest.mark.parametrize("shift", [0, 4, 1], ids=["16-byte", "8-byte", "2-byte"])
+@pytest.mark.parametrize("dim,rot", [(80, 40), (128, 64), (24, 24)])
+def test_append_at_smaller_alignments(dim, rot, shift):
+    """Caches whose slots are a multiple of 16, 8 or 2 bytes apart."""
+    nf4, dt, tokens, hk, page = lib(), torch.bfloat16, 50, 3, 16
+    _, k, v, pos, _, kw = inputs(tokens, 1, hk, dim, dt, dim, 900)
+    t = nf4.nf4_rope_table(900, rot)
+    base = torch.randn(2, 6, page, hk, dim + shift, device="cuda", generator=gen(2)).to(dt)
+    before = base.clone()
+    kc, vc = base[0, ..., shift:], base[1, ..., :dim]
+    slots = torch.randperm(6 * page, device="cuda", generator=gen(4))[:tokens].contiguous()
+    nf4.nf4_kv_append(kc, vc, slots, k, v, pos, t, k_weight=kw)
+    cos, sin = angles(pos, frequencies(rot))
+    check(kc[slots // page, slots % page], expected(k, kw, cos, sin, False, 1e-6), "k")
+    assert torch.equal(vc[slots // page, slots % page], v)
+    other = torch.ones(6, page, dtype=torch.bool, device="cuda")
+    other[slots // page, slots % page] = False
+    for i in range(2):
+        assert torch.equal(base[i][other], before[i][other])
+    if shift:
+        assert torch.equal(base[0, ..., :shift], before[0, ..., :shift])
+        assert torch.equal(base[1, ..., dim:], before[1, ..., dim:])
+
+
 def test_extreme_rows():
     """Rows of zeros, of the largest and of subnormal values, and rows with infinities and NaN (which stay in
     their row)."""

@@ -9,16 +9,19 @@
 // result).
 //
 // Split: a row is cut into units of two 16-byte chunks that hold whole pairs
-// (the chunks at i and i + rot_dim / 2 of the half layout, two neighbouring
-// chunks otherwise), one lane per unit, so that a row's norm is a butterfly
-// over the 2^k lanes that share it and both elements of a pair are in one
-// lane's registers: no shared memory, and an output may be its input. A warp
+// (one of each half of the rotated part, in either layout, and one of each half
+// of the rest), so that neighbouring lanes hold neighbouring chunks; with two
+// neighbouring chunks per lane for the interleaved layout, half a sector to
+// each instruction, the prompt below took 57 us. One lane per unit: a row's
+// norm is a butterfly over the 2^k lanes that share it, both elements of a pair
+// are in one lane's registers, and an output may be its input. A warp
 // takes one token: the weights times the token's cosines and sines are formed
 // once and serve all the heads that the warp walks over (two multiplications
 // and additions per element, packed two to an instruction), and the next four
 // rows are under way in shared memory, each lane reading back only what it
-// brought. 8192 tokens x 64 heads of 128 in bf16 take 45.2 us (6.0 TB/s, 90% of
-// measured copy bandwidth), an append of 8000 x 96 heads 62.4 us (95%).
+// brought. 8192 tokens x 64 heads of 128 in bf16 take 44.7 us (6.1 TB/s, 91% of
+// measured copy bandwidth; interleaved 44.2), an append of 8000 x 96 heads 62.4
+// us (95%).
 #include <math.h>
 
 #include <initializer_list>
@@ -88,39 +91,70 @@ struct RopeArgs {
   int per_warp, parts;        // groups a warp walks over; warps per token
 };
 
-// Two 16-byte chunks as P pairs (a_i, b_i) of binary32 and back: in the half
-// layout a comes from the first chunk and b from the second, in the
+// Two chunks of P elements as P pairs (a_i, b_i) of binary32 and back: in the
+// half layout a comes from the first chunk and b from the second, in the
 // interleaved layout they alternate.
-template <typename H>
-struct Elem16 {
-  static constexpr int kSize = 2, kPer = 8;
+template <int kBytes>
+struct ChunkOf;
+template <>
+struct ChunkOf<16> {
+  using type = uint4;
+  static __device__ __forceinline__ void get(const uint4& x, uint32_t* w) {
+    w[0] = x.x;
+    w[1] = x.y;
+    w[2] = x.z;
+    w[3] = x.w;
+  }
+  static __device__ __forceinline__ uint4 put(const uint32_t* w) { return make_uint4(w[0], w[1], w[2], w[3]); }
+  static __device__ __forceinline__ void copy(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  }
+};
+template <>
+struct ChunkOf<8> {
+  using type = uint2;
+  static __device__ __forceinline__ void get(const uint2& x, uint32_t* w) {
+    w[0] = x.x;
+    w[1] = x.y;
+  }
+  static __device__ __forceinline__ uint2 put(const uint32_t* w) { return make_uint2(w[0], w[1]); }
+  static __device__ __forceinline__ void copy(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+  }
+};
+
+template <typename H, int kBytes>
+struct Elem : ChunkOf<kBytes> {
+  static constexpr int kSize = 2, kPer = kBytes / 2;
+  using Chunk = typename ChunkOf<kBytes>::type;
   template <bool kInterleaved>
-  static __device__ __forceinline__ void up(const uint4& x0, const uint4& x1, float (&a)[8], float (&b)[8]) {
-    const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+  static __device__ __forceinline__ void up(const Chunk& x0, const Chunk& x1, float (&a)[kPer], float (&b)[kPer]) {
+    uint32_t w[kPer];
+    Elem::get(x0, w);
+    Elem::get(x1, w + kPer / 2);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kPer; ++i) {
       const float2 p = H::up2(w[i]);
       if (kInterleaved) {
         a[i] = p.x;
         b[i] = p.y;
       } else {
-        (i < 4 ? a : b)[2 * (i & 3)] = p.x;
-        (i < 4 ? a : b)[2 * (i & 3) + 1] = p.y;
+        float* to = i < kPer / 2 ? a + 2 * i : b + 2 * i - kPer;
+        to[0] = p.x;
+        to[1] = p.y;
       }
     }
   }
   template <bool kInterleaved>
-  static __device__ __forceinline__ void down(const float (&a)[8], const float (&b)[8], uint4& x0, uint4& x1) {
-    uint32_t w[8];
+  static __device__ __forceinline__ void down(const float (&a)[kPer], const float (&b)[kPer], Chunk& x0, Chunk& x1) {
+    uint32_t w[kPer];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (kInterleaved)
-        w[i] = H::down2(a[i], b[i]);
-      else
-        w[i] = i < 4 ? H::down2(a[2 * i], a[2 * i + 1]) : H::down2(b[2 * (i - 4)], b[2 * (i - 4) + 1]);
+    for (int i = 0; i < kPer; ++i) {
+      const float* from = i < kPer / 2 ? a + 2 * i : b + 2 * i - kPer;
+      w[i] = kInterleaved ? H::down2(a[i], b[i]) : H::down2(from[0], from[1]);
     }
-    x0 = make_uint4(w[0], w[1], w[2], w[3]);
-    x1 = make_uint4(w[4], w[5], w[6], w[7]);
+    x0 = Elem::put(w);
+    x1 = Elem::put(w + kPer / 2);
   }
   static __device__ __forceinline__ float load(const char* p) {
     return H::up2(*reinterpret_cast<const uint16_t*>(p)).x;
@@ -129,15 +163,10 @@ struct Elem16 {
     *reinterpret_cast<uint16_t*>(p) = uint16_t(H::down2(v, v) & 0xffffu);
   }
 };
-template <typename T>
-struct Elem;
 template <>
-struct Elem<Bf16> : Elem16<Bf16> {};
-template <>
-struct Elem<Fp16> : Elem16<Fp16> {};
-template <>
-struct Elem<float> {
+struct Elem<float, 16> : ChunkOf<16> {
   static constexpr int kSize = 4, kPer = 4;
+  using Chunk = uint4;
   template <bool kInterleaved>
   static __device__ __forceinline__ void up(const uint4& x0, const uint4& x1, float (&a)[4], float (&b)[4]) {
     const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
@@ -149,14 +178,14 @@ struct Elem<float> {
   }
   template <bool kInterleaved>
   static __device__ __forceinline__ void down(const float (&a)[4], const float (&b)[4], uint4& x0, uint4& x1) {
-    float w[8];
+    uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[kInterleaved ? 2 * i : i] = a[i];
-      w[kInterleaved ? 2 * i + 1 : i + 4] = b[i];
+      w[kInterleaved ? 2 * i : i] = __float_as_uint(a[i]);
+      w[kInterleaved ? 2 * i + 1 : i + 4] = __float_as_uint(b[i]);
     }
-    x0 = make_uint4(__float_as_uint(w[0]), __float_as_uint(w[1]), __float_as_uint(w[2]), __float_as_uint(w[3]));
-    x1 = make_uint4(__float_as_uint(w[4]), __float_as_uint(w[5]), __float_as_uint(w[6]), __float_as_uint(w[7]));
+    x0 = put(w);
+    x1 = put(w + 4);
   }
   static __device__ __forceinline__ float load(const char* p) { return *reinterpret_cast<const float*>(p); }
   static __device__ __forceinline__ void store(char* p, float v) { *reinterpret_cast<float*>(p) = v; }
@@ -184,9 +213,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -225,10 +251,11 @@ constexpr int kRopeBlocks = 5;
 constexpr int kInFlight = 4;
 constexpr int kMaxPerWarp = 8;  // row groups that one warp walks over (16: 48 us, 4: 55 us)
 
-template <typename T, bool kInterleaved>
+template <typename E, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_rows_kernel(const __grid_constant__ RopeArgs a) {
-  using E = Elem<T>;
+  using Chunk = typename E::Chunk;
   constexpr int P = E::kPer;  // elements per chunk = pairs per unit
+  constexpr int kBytes = sizeof(Chunk);
   pdl_allow_dependents();
   const int64_t w = int64_t(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -243,9 +270,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_rows_kernel(co
   const bool active = unit < a.dim / (2 * P);
   const bool turned = unit < rot_units;
   // byte offset of the unit's first chunk, and from there to the second (a lane
-  // past the row's end takes the first unit, and stores nothing)
-  const int c0 = !active ? 0 : turned && !kInterleaved ? 16 * unit : 32 * unit;
-  const int c1 = turned && !kInterleaved ? 16 * rot_units : 16;
+  // past the row's end takes the row's first chunk, and stores nothing)
+  const int c0 = !active ? 0 : kBytes * (turned ? unit : unit + rot_units);
+  const int c1 = kBytes * (turned ? rot_units : a.dim / (2 * P) - rot_units);
   // this warp's row groups: q's, then k's, then v's
   const int g = part * a.per_warp;
   const int g_end = min(g + a.per_warp, a.gq + a.gk + a.gv);
@@ -266,14 +293,14 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_rows_kernel(co
                 min(g_end - first, n), r.heads - 1, r.in_hs * E::kSize};
   };
   // Rows under way, in shared memory; every lane reads back only what it brought.
-  __shared__ __align__(16) uint4 ring[kRopeThreads / 32][kInFlight][2][32];
+  __shared__ __align__(16) Chunk ring[kRopeThreads / 32][kInFlight][2][32];
   auto& mine = ring[threadIdx.x >> 5];
   auto load = [&](const Part& s, int gi) {
     if (gi < s.to) {
       const char* p = s.src + int64_t(min(gi * rows + sub, s.last)) * s.head_step;
       const int slot = (gi - s.from) % kInFlight;
-      copy16(smem_u32(&mine[slot][0][lane]), p);
-      copy16(smem_u32(&mine[slot][1][lane]), p + c1);
+      E::copy(smem_u32(&mine[slot][0][lane]), p);
+      E::copy(smem_u32(&mine[slot][1][lane]), p + c1);
     }
     copy_commit();
   };
@@ -314,19 +341,22 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_rows_kernel(co
     if (kind < 2) {
       float wa[P], wb[P];
       if (wt) {
-        E::template up<kInterleaved>(__ldg(reinterpret_cast<const uint4*>(wt + c0)),
-                                     __ldg(reinterpret_cast<const uint4*>(wt + c0 + c1)), wa, wb);
+        E::template up<kInterleaved>(__ldg(reinterpret_cast<const Chunk*>(wt + c0)),
+                                     __ldg(reinterpret_cast<const Chunk*>(wt + c0 + c1)), wa, wb);
       } else {
 #pragma unroll
         for (int i = 0; i < P; ++i) wa[i] = wb[i] = 1.0f;
       }
       // a position out of the table: NaN in every element, turned or not
-      const float4* src = reinterpret_cast<const float4*>(a.cs + (good ? pos : 0) * (a.rot / 2) + unit * P);
+      // (interleaved, half of the unit's pairs are in each chunk)
+      const float4* src = reinterpret_cast<const float4*>(a.cs + (good ? pos : 0) * (a.rot / 2)) +
+                          unit * (kInterleaved ? P / 4 : P / 2);
+      const int far = kInterleaved ? rot_units * (P / 4) - P / 4 : 0;
       const float none = good ? 1.0f : __uint_as_float(0x7fc00000u);
 #pragma unroll
       for (int i = 0; i < P / 2; ++i) {
         float4 f = make_float4(none, 0.0f, none, 0.0f);
-        if (turned && good) f = __ldg(src + i);
+        if (turned && good) f = __ldg(src + (i < P / 4 ? i : i + far));
         const uint64_t c = pack2(f.x, f.z);
         ac[i] = mul2(pack2(wa[2 * i], wa[2 * i + 1]), c);
         bc[i] = mul2(pack2(wb[2 * i], wb[2 * i + 1]), c);
@@ -338,7 +368,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_rows_kernel(co
     for (int gi = s.from; gi < s.to; ++gi) {
       copy_wait<kInFlight - 1>();
       const int slot = (gi - s.from) % kInFlight;
-      uint4 y0 = mine[slot][0][lane], y1 = mine[slot][1][lane];
+      Chunk y0 = mine[slot][0][lane], y1 = mine[slot][1][lane];
       if (kind < 2) {
         float fa[P], fb[P];
         E::template up<kInterleaved>(y0, y1, fa, fb);
@@ -383,8 +413,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_rows_kernel(co
       const int h = gi * rows + sub;
       if (active && h <= s.last) {
         char* p = dst + int64_t(h) * out_step;
-        *reinterpret_cast<uint4*>(p) = y0;
-        *reinterpret_cast<uint4*>(p + c1) = y1;
+        *reinterpret_cast<Chunk*>(p) = y0;
+        *reinterpret_cast<Chunk*>(p + c1) = y1;
       }
       load(s, gi + kInFlight);
     }
@@ -394,9 +424,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_rows_kernel(co
 
 // Any head size, alignment and rotated part: one warp per row, a lane per
 // pair, then the rest of the row.
-template <typename T>
+template <typename E>
 __global__ void __launch_bounds__(kRopeThreads) rope_rows_any_kernel(const __grid_constant__ RopeArgs a) {
-  using E = Elem<T>;
   pdl_allow_dependents();
   const int heads = a.q.heads + a.k.heads + a.v.heads;
   const int64_t w = int64_t(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
@@ -456,45 +485,69 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_any_kernel(const __gri
   for (int i = a.rot + lane; i < a.dim; i += 32) E::store(out + i * E::kSize, good ? value(i) : nan);
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-template <typename T>
-cudaError_t launch_rows(RopeArgs& a, cudaStream_t stream) {
-  using E = Elem<T>;
-  const int P = E::kPer;
+// Whether chunks of E hold every row: whole units, and all rows, weights and
+// strides on a chunk's boundary.
+template <typename E>
+bool in_chunks(const RopeArgs& a) {
+  constexpr int P = E::kPer;
+  auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % sizeof(typename E::Chunk) == 0; };
   auto fits = [&](const RowSet& r) {
-    return r.heads == 0 || (aligned16(r.in) && aligned16(r.out) && r.in_ts % P == 0 && r.in_hs % P == 0 &&
+    return r.heads == 0 || (aligned(r.in) && aligned(r.out) && r.in_ts % P == 0 && r.in_hs % P == 0 &&
                             r.out_ts % P == 0 && r.out_hs % P == 0);
   };
-  const bool wide = a.dim % (2 * P) == 0 && a.rot % (2 * P) == 0 && a.dim / (2 * P) <= 32 && fits(a.q) &&
-                    fits(a.k) && fits(a.v) && aligned16(a.qw) && aligned16(a.kw) && aligned16(a.cs) &&
-                    a.k_page_stride % P == 0 && a.k_slot_stride % P == 0 && a.v_page_stride % P == 0 &&
-                    a.v_slot_stride % P == 0;
+  return a.dim % (2 * P) == 0 && a.rot % (2 * P) == 0 && a.dim / (2 * P) <= 32 && fits(a.q) && fits(a.k) &&
+         fits(a.v) && aligned(a.qw) && aligned(a.kw) && reinterpret_cast<uintptr_t>(a.cs) % 16 == 0 &&
+         a.k_page_stride % P == 0 && a.k_slot_stride % P == 0 && a.v_page_stride % P == 0 &&
+         a.v_slot_stride % P == 0;
+}
+
+template <typename E>
+cudaError_t launch_chunks(RopeArgs& a, cudaStream_t stream) {
+  const int P = E::kPer;
   const int per_block = kRopeThreads / 32;
-  if (!wide) {
-    const int64_t warps = int64_t(a.tokens) * (a.q.heads + a.k.heads + a.v.heads);
-    const int64_t blocks = (warps + per_block - 1) / per_block;
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    return launch_k(rope_rows_any_kernel<T>, dim3(unsigned(blocks)), dim3(kRopeThreads), 0, stream, a);
-  }
   a.lane_bits = 0;
   while ((1 << a.lane_bits) < a.dim / (2 * P)) ++a.lane_bits;
   const int rows = 32 >> a.lane_bits;
   a.gq = (a.q.heads + rows - 1) / rows;
   a.gk = (a.k.heads + rows - 1) / rows;
   a.gv = (a.v.heads + rows - 1) / rows;
-  // Warps per token: as many as fill the SMs twice, one per group at most; for
-  // many tokens as few as kMaxPerWarp allows, so that a warp's table row and
-  // weights serve several groups.
+  // Warps per token: as many as the SMs hold at a time, one per group at most
+  // (64 heads of 128 in bf16, us: 400 tokens 4.9, twice as many 6.1, half as many
+  // 6.6; 1000 tokens 7.2, 8.8 and 8.0); for many tokens as few as kMaxPerWarp
+  // allows, so that a warp's table row and weights serve several groups.
   const int groups = a.gq + a.gk + a.gv;
   const int64_t resident = 152 * kRopeBlocks * (kRopeThreads / 32);
-  const int64_t least = (groups + kMaxPerWarp - 1) / kMaxPerWarp, fit = 2 * resident / a.tokens;
+  const int64_t least = (groups + kMaxPerWarp - 1) / kMaxPerWarp, fit = resident / a.tokens;
   a.parts = int(fit < least ? least : fit < groups ? fit : groups);
   a.per_warp = (groups + a.parts - 1) / a.parts;
   const int64_t blocks = (int64_t(a.tokens) * a.parts + per_block - 1) / per_block;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  return launch_k(a.interleaved ? rope_rows_kernel<T, true> : rope_rows_kernel<T, false>, dim3(unsigned(blocks)),
+  return launch_k(a.interleaved ? rope_rows_kernel<E, true> : rope_rows_kernel<E, false>, dim3(unsigned(blocks)),
                   dim3(kRopeThreads), 0, stream, a);
+}
+
+template <typename E>
+cudaError_t launch_any(RopeArgs& a, cudaStream_t stream) {
+  const int per_block = kRopeThreads / 32;
+  const int64_t warps = int64_t(a.tokens) * (a.q.heads + a.k.heads + a.v.heads);
+  const int64_t blocks = (warps + per_block - 1) / per_block;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  return launch_k(rope_rows_any_kernel<E>, dim3(unsigned(blocks)), dim3(kRopeThreads), 0, stream, a);
+}
+
+// 16-byte chunks; 8-byte chunks where 16-byte ones do not hold whole units (a
+// rotated part of 40 elements, say: 8000 tokens x 12 heads of 80 in bf16 take
+// 15.2 us, element by element 30.3), which binary32 leaves to its four-element
+// chunks of 16 bytes; elements otherwise.
+template <typename H>
+cudaError_t launch_half(RopeArgs& a, cudaStream_t stream) {
+  if (in_chunks<Elem<H, 16>>(a)) return launch_chunks<Elem<H, 16>>(a, stream);
+  if (in_chunks<Elem<H, 8>>(a)) return launch_chunks<Elem<H, 8>>(a, stream);
+  return launch_any<Elem<H, 16>>(a, stream);
+}
+cudaError_t launch_float(RopeArgs& a, cudaStream_t stream) {
+  if (in_chunks<Elem<float, 16>>(a)) return launch_chunks<Elem<float, 16>>(a, stream);
+  return launch_any<Elem<float, 16>>(a, stream);
 }
 
 }  // namespace
@@ -582,9 +635,9 @@ cudaError_t launch_qk_rope(const nf4_qk_norm_rope_args& q, const nf4_kv_append_a
   a.inv_dim = 1.0f / float(q.head_dim);
   a.tokens = int(q.tokens);
   switch (q.dtype) {
-    case NF4_BF16: return launch_rows<Bf16>(a, stream);
-    case NF4_FP16: return launch_rows<Fp16>(a, stream);
-    default: return launch_rows<float>(a, stream);
+    case NF4_BF16: return launch_half<Bf16>(a, stream);
+    case NF4_FP16: return launch_half<Fp16>(a, stream);
+    default: return launch_float(a, stream);
   }
 }
 
