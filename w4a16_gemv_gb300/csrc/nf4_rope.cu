@@ -242,17 +242,19 @@ __device__ __forceinline__ bool slot_base(const RopeArgs& a, int64_t slot, int s
 }
 
 constexpr int kRopeThreads = 128;
-// Blocks of four warps, five on an SM (96 registers), four rows under way per
+// Blocks of four warps, five on an SM (96 registers; six where a chunk has four
+// elements and 80 do), four rows under way per
 // warp through shared memory. 8192 tokens x 64 heads of 128 in bf16, us: rows
 // under way in registers, the next one only, 51.6, four 60.3 (too few warps);
 // through shared memory two 48.0, four 45.2, six 46.1 (and with six blocks 46.0,
 // with eight, whose 64 registers spill, 51.4).
-constexpr int kRopeBlocks = 5;
+template <typename E>
+constexpr int kRopeBlocks = E::kPer == 8 ? 5 : 6;
 constexpr int kInFlight = 4;
 constexpr int kMaxPerWarp = 8;  // row groups that one warp walks over (16: 48 us, 4: 55 us)
 
 template <typename E, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_rows_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<E>) rope_rows_kernel(const __grid_constant__ RopeArgs a) {
   using Chunk = typename E::Chunk;
   constexpr int P = E::kPer;  // elements per chunk = pairs per unit
   constexpr int kBytes = sizeof(Chunk);
@@ -516,7 +518,7 @@ cudaError_t launch_chunks(RopeArgs& a, cudaStream_t stream) {
   // 6.6; 1000 tokens 7.2, 8.8 and 8.0); for many tokens as few as kMaxPerWarp
   // allows, so that a warp's table row and weights serve several groups.
   const int groups = a.gq + a.gk + a.gv;
-  const int64_t resident = 152 * kRopeBlocks * (kRopeThreads / 32);
+  const int64_t resident = 152 * kRopeBlocks<E> * (kRopeThreads / 32);
   const int64_t least = (groups + kMaxPerWarp - 1) / kMaxPerWarp, fit = resident / a.tokens;
   a.parts = int(fit < least ? least : fit < groups ? fit : groups);
   a.per_warp = (groups + a.parts - 1) / a.parts;
