@@ -251,7 +251,7 @@ constexpr int kRopeThreads = 128;
 template <typename E>
 constexpr int kRopeBlocks = E::kPer == 8 ? 5 : 6;
 constexpr int kInFlight = 4;
-constexpr int kMaxPerWarp = 8;  // row groups that one warp walks over (16: 48 us, 4: 55 us)
+constexpr int kPerWarp = 8;  // row groups that one warp walks over at least, where there are many tokens (4: 54 us)
 
 template <typename E, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<E>) rope_rows_kernel(const __grid_constant__ RopeArgs a) {
@@ -513,13 +513,17 @@ cudaError_t launch_chunks(RopeArgs& a, cudaStream_t stream) {
   a.gq = (a.q.heads + rows - 1) / rows;
   a.gk = (a.k.heads + rows - 1) / rows;
   a.gv = (a.v.heads + rows - 1) / rows;
-  // Warps per token: as many as the SMs hold at a time, one per group at most
-  // (64 heads of 128 in bf16, us: 400 tokens 4.9, twice as many 6.1, half as many
-  // 6.6; 1000 tokens 7.2, 8.8 and 8.0); for many tokens as few as kMaxPerWarp
-  // allows, so that a warp's table row and weights serve several groups.
+  // Warps per token. Few tokens: as many as the SMs hold at a time, one per
+  // group at most (64 heads of 128 in bf16, us: 400 tokens 4.9, twice as many 6.1,
+  // half as many 6.6; 1000 tokens 7.2, 8.8 and 8.0), and two rather than one
+  // that would leave a third of the places empty (1700 tokens x 40 heads 9.1, one
+  // 10.1). Many: one for every 8 to 15 groups, since a warp's table row and
+  // weights serve all of them (8192 tokens x 40 heads, ten groups: 30.6, two
+  // warps of five 35.8).
   const int groups = a.gq + a.gk + a.gv;
   const int64_t resident = 152 * kRopeBlocks<E> * (kRopeThreads / 32);
-  const int64_t least = (groups + kMaxPerWarp - 1) / kMaxPerWarp, fit = resident / a.tokens;
+  const int64_t least = groups < 2 * kPerWarp ? 1 : groups / kPerWarp;
+  const int64_t fit = 10 * int64_t(a.tokens) < 7 * resident && a.tokens * 2 > resident ? 2 : resident / a.tokens;
   a.parts = int(fit < least ? least : fit < groups ? fit : groups);
   a.per_warp = (groups + a.parts - 1) / a.parts;
   const int64_t blocks = (int64_t(a.tokens) * a.parts + per_block - 1) / per_block;
