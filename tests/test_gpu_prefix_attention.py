@@ -8,6 +8,8 @@ subnormal step, of weights at most 1). Sums of N terms add N e. With A = sum p |
 |out - exact| <= u |exact| + (u + 2 r + 2 N e) A + [fp16] 2^-24 sum |v| + tiny,
 |lse - exact| <= r + N e + 4 e |exact|.
 """
+import copy
+
 import pytest
 import torch
 
@@ -191,6 +193,43 @@ def test_prefix_lengths_around_tiles(prefix, batch):
 def test_ragged_tokens(dt, hq, hk, dim, prefix, counts, lens):
     c = Call(hq, hk, dim, prefix, lens, counts, dt=dt, seed=sum(counts) + prefix)
     c.check(c.run())
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("hq,hk,dim", [(12, 2, 128), (4, 4, 64), (10, 2, 80)])
+@pytest.mark.parametrize("prefix", [0, 1, 200, 700])
+@pytest.mark.parametrize("counts,lens", [
+    ([40, 0, 90, 13, 1], [40, 5, 300, 200, 1]),   # many rows per sequence
+    ([300, 70], [0, 70]),                         # a sequence without keys of its own
+    ([200, 100, 130], [150, 100, 700]),           # tokens before the first own key
+    ([8] * 9, [8 + 11 * i for i in range(9)]), ([1] * 40, [i for i in range(40)])])
+def test_tokens_that_no_sequence_holds(dt, hq, hk, dim, prefix, counts, lens):
+    """Tokens before the first and after the last sequence see the shared keys only."""
+    c = Call(hq, hk, dim, prefix, lens, counts, dt=dt, seed=prefix + len(lens), junk=0.0)
+    c.check(c.run(), "all held")
+    extra = (torch.randn(27, hq, dim, device="cuda", generator=gen(5)) * 1.5).to(dt)
+    other = copy.copy(c)
+    other.q, other.cu_q = torch.cat((extra[:7], c.q, extra[7:])), c.cu_q + 7
+    out, lse = other.run()
+    n = sum(counts)
+    c.check((out[7:7 + n].contiguous(), lse[7:7 + n].contiguous()), "held")
+    rest = copy.copy(c)
+    rest.q, rest.counts, rest.lens = extra, [27], [0]
+    rest.check(tuple(torch.cat((x[:7], x[7 + n:])) for x in (out, lse)), "not held")
+    again = other.run()
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_own_keys_alone_keep_infinities_out_of_rows_without_keys():
+    """Without shared keys: a token before the first own key gives zeros whatever the keys hold."""
+    for n, extra in ((3, 0), (9, 0), (100, 60)):
+        c = Call(12, 2, 128, 0, [n - 2, n + 200], [n, n], seed=n)
+        c.v[c.suffix_pages[0, 0].long(), 0] = float("inf")
+        out, lse = c.run()
+        assert not out[:2].any() and (lse[:2] == float("-inf")).all()
+        assert out[2:n].isinf().all() and lib().nf4_device_error_flags() == 0
+        out[2:n], lse[2:n] = 0, 0
+        assert out[n:].isfinite().all()
 
 
 def test_one_long_sequence_among_many():

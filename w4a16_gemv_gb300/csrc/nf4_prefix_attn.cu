@@ -299,10 +299,8 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
         *reinterpret_cast<float4*>(ro.part + col) = v;
         if (col == 0) *ro.ml = make_float2(m, l);
       } else {
-        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-        *reinterpret_cast<uint2*>(ro.out + col * 2) =
-            make_uint2(H::down2(v.x * inv, v.y * inv), H::down2(v.z * inv, v.w * inv));
-        if (col == 0 && ro.lse) *ro.lse = l > 0.0f || l != l ? fmaf(m, kLn2, logf(l)) : -INFINITY;
+        if (!part_holds(make_float2(m, l))) v = make_float4(0.f, 0.f, 0.f, 0.f);
+        write_row<H>(ro.out, ro.lse, col, m, l, v);
       }
     }
   } else {
@@ -325,7 +323,8 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
         for (int d = 0; d < DP / 8; ++d) {
           const int col = d * 8 + (lane & 3) * 2;
           if (col < a.dim)
-            *reinterpret_cast<uint32_t*>(ro.out + col * 2) = H::down2(o[d][2 * x] * inv, o[d][2 * x + 1] * inv);
+            *reinterpret_cast<uint32_t*>(ro.out + col * 2) =
+                part_holds(make_float2(m, l)) ? H::down2(o[d][2 * x] * inv, o[d][2 * x + 1] * inv) : 0u;
         }
         if ((lane & 3) == 0 && ro.lse) *ro.lse = l > 0.0f || l != l ? fmaf(m, kLn2, logf(l)) : -INFINITY;
       }
@@ -345,6 +344,7 @@ __global__ void __launch_bounds__(Shape<R, W>::kThreads) prefix_mma_kernel(const
   pdl_allow_dependents();
   const PrefixItem it = prefix_item(a, unsigned(a.first) + blockIdx.x, &g_prefix_flags);
   if (it.rows > 0) attend<H, DP, R, W>(a, it, smem);
+  if (a.fused) unheld_rows<H>(a, W);
   if (a.beside && blockIdx.x + 1 == gridDim.x) pdl_wait_prior_grid();
 }
 
@@ -540,7 +540,7 @@ cudaError_t launch_rows(const PrefixArgs& p, int rows, unsigned items, cudaStrea
 template <typename H>
 cudaError_t launch_typed(const PrefixArgs& p, cudaStream_t stream) {
   const int64_t rows = int64_t(p.tokens) * p.q_heads;
-  if (p.splits == 0)
+  if (p.splits == 0 && !p.fused)
     return launch_k(prefix_empty_kernel<H>, dim3(unsigned((rows + 3) / 4)), dim3(128), 0, stream, p);
   const int64_t prefix_items = int64_t(p.prefix_tiles) * p.prefix_splits * p.k_heads;
   const int64_t suffix_items = int64_t(p.suffix_tiles) * p.suffix_splits * p.k_heads;
@@ -553,17 +553,19 @@ cudaError_t launch_typed(const PrefixArgs& p, cudaStream_t stream) {
   for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
     int64_t items = counts[i];
     const int tile = tile_rows[i];
-    if (i == 0 && tile == tile_rows[1]) items += counts[1];
+    if (i == 0 && tile == tile_rows[1] && !p.fused) items += counts[1];
     if (items == 0 || first == prefix_items + suffix_items) continue;
     PrefixArgs q = p;
     q.first = int(first);
     q.beside = first > 0;
+    q.fused = p.fused && i == 1;
+    q.direct = p.direct || q.fused;
     e = tile == 256 ? launch_prefix_tc(q, H::kDtype, unsigned(items), stream)
         : p.dim <= 64 ? launch_rows<H, 64>(q, tile, unsigned(items), stream)
                       : launch_rows<H, 128>(q, tile, unsigned(items), stream);
     first += items;
   }
-  if (e != cudaSuccess || p.direct) return e;
+  if (e != cudaSuccess || p.direct || p.fused) return e;
   const int64_t few = int64_t(kJoinWarps) * kFewRows;
   if (p.splits <= 4 && rows >= few * kSms)
     return launch_k(p.splits <= 2 ? prefix_join_few_kernel<H, 2> : prefix_join_few_kernel<H, 4>,
@@ -686,7 +688,15 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
     } else {
       const int64_t longest = (pk + 1) / 2;
       per = tc_range(tiles, longest, rows * p->k_heads, kSms);
-      if (p->suffix_rows != 256 && sk > 0) {
+      // One range of each and many rows: the items of own keys join the shared
+      // part themselves, in place of a launch that reads both parts again (8 prompts
+      // of 257 to 512 tokens over 8190 + 700 keys 131 -> 125 us, 4 of 300 over 1000 +
+      // 400 with 32 heads over 8 41.4 -> 35.2; 20 of 50 33.1 and 33.5). Not with the
+      // few-row kernel, whose items would hold their SMs waiting for the shared part:
+      // 64 sequences x 32 heads over 2048 + 190 took 56 us instead of 49; nor with two
+      // ranges and more to read back: 16 prompts of 100 35 instead of 29.
+      p->fused = p->suffix_splits == 1 && p->suffix_rows == 256 && pk <= per;
+      if (!p->fused && p->suffix_rows != 256 && sk > 0) {
         per = beside_range(a, *p, per, 2 * longest);
         const int keep = sms_for_own(*p, likely * p->k_heads * p->suffix_splits, tiles, per, pk);
         if (keep > 0) per = tc_range(tiles, longest, rows * p->k_heads, kSms - keep);
@@ -695,8 +705,9 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
     p->prefix_chunk = int(per * kUnit);
     p->prefix_splits = int((pk + per - 1) / per);
   }
-  if (rows == 0) p->prefix_splits = p->suffix_splits = 0;
-  p->splits = p->prefix_splits + p->suffix_splits;
+  if (pk == 0) p->fused = p->suffix_splits == 1;  // own keys in one range are all there is
+  if (rows == 0) p->prefix_splits = p->suffix_splits = p->fused = 0;
+  p->splits = p->prefix_splits + (p->fused ? 0 : p->suffix_splits);
   const int64_t all = a.tokens * a.q_heads;
   p->direct = p->prefix_splits == 1 && p->suffix_splits == 0;
   *bytes = p->splits > 0 && !p->direct ? size_t(all) * size_t(p->splits) * (size_t(a.head_dim) * 4 + 8) : 0;

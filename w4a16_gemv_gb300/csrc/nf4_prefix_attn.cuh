@@ -10,7 +10,8 @@ namespace nf4 {
 // pair: row r of a segment of tokens is token r / group, query head
 // k_head * group + r % group. A work item is a tile of rows against a range of
 // keys; it leaves an unscaled partial output (binary32), the running maximum
-// (of scores times log2 e) and the running sum, and a last kernel joins them.
+// (of scores times log2 e) and the running sum, and a last kernel joins them,
+// or, where a row has one item of own keys, that item.
 struct PrefixArgs {
   const char* q;
   char* out;
@@ -35,7 +36,9 @@ struct PrefixArgs {
   int prefix_splits, suffix_splits;                // ranges of keys, of this many each:
   int prefix_chunk, suffix_chunk;
   int splits;                                      // prefix_splits + suffix_splits
-  int direct;                                      // 1: one range of shared keys is all; its items write the output
+  int direct;                                      // 1: the items write the output
+  int fused;                                       // 1: one range of own keys, whose items write the output, with
+                                                   // the one range of shared keys, if any, joined in
   int first;                                       // first item of the launch
   int beside;                                      // 1: runs beside the launch before it of the same call
   float* part;                                     // [splits][tokens * q_heads][dim]
@@ -177,9 +180,9 @@ __device__ __forceinline__ float ex2(float x) {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Where a finished row goes: the partial results, or, when one range of keys
-// is all there is, the output itself.
+// Where a finished row goes: the partial results, or the output itself.
 struct RowOut {
+  int64_t row;
   float* part;
   float2* ml;
   char* out;
@@ -190,11 +193,53 @@ __device__ __forceinline__ RowOut row_out(const PrefixArgs& a, const PrefixItem&
   const int h = it.head * a.group + r % a.group;
   const int64_t row = int64_t(t) * a.q_heads + h;
   RowOut o;
+  o.row = row;
   o.part = a.part + (int64_t(it.split) * a.tokens * a.q_heads + row) * a.dim;
   o.ml = a.ml + row * a.splits + it.split;
   o.out = a.out + int64_t(t) * a.out_ts + int64_t(h) * a.out_hs;
   o.lse = a.lse ? a.lse + row : nullptr;
   return o;
+}
+
+// Four columns of an output row from its sum l, its maximum m and v.
+template <typename H>
+__device__ __forceinline__ void write_row(char* out, float* lse, int col, float m, float l, const float4& v) {
+  const bool any = l > 0.0f || l != l;
+  const float inv = any ? 1.0f / l : 0.0f;
+  *reinterpret_cast<uint2*>(out + col * 2) =
+      make_uint2(H::down2(v.x * inv, v.y * inv), H::down2(v.z * inv, v.w * inv));
+  if (col == 0 && lse) *lse = any ? fmaf(m, kLn2, logf(l)) : -INFINITY;
+}
+
+// Whether a part (maximum, sum) holds a key, and its weight when the row's
+// maximum is m. (A maximum of -inf with a sum: of NaN.)
+__device__ __forceinline__ bool part_holds(const float2& x) { return !(x.x == -INFINITY && x.y == 0.0f); }
+__device__ __forceinline__ float part_weight(const float2& x, float m) { return x.x == -INFINITY ? 1.0f : ex2(x.x - m); }
+
+// Row `row` with shared keys only (one range of them, or none), by a whole warp.
+template <typename H>
+__device__ __forceinline__ void shared_row(const PrefixArgs& a, int64_t row) {
+  const int col = int(threadIdx.x & 31u) * 4;
+  if (col >= a.dim) return;
+  float2 x = make_float2(-INFINITY, 0.0f);
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.splits > 0) {
+    x = a.ml[row];
+    if (part_holds(x)) v = *reinterpret_cast<const float4*>(a.part + row * a.dim + col);
+  }
+  const int64_t t = row / a.q_heads;
+  write_row<H>(a.out + t * a.out_ts + (row - t * a.q_heads) * a.out_hs, a.lse ? a.lse + row : nullptr, col, x.x, x.y, v);
+}
+
+// The rows of tokens that no sequence holds, dealt out to the first `warps`
+// warps of every CTA of a launch of own items.
+template <typename H>
+__device__ __forceinline__ void unheld_rows(const PrefixArgs& a, int warps) {
+  if (!a.cu_q) return;
+  const int lo = min(max(a.cu_q[0], 0), a.tokens), hi = min(max(a.cu_q[a.batch], lo), a.tokens);
+  const int64_t rows = int64_t(lo + a.tokens - hi) * a.q_heads;
+  for (int64_t r = int64_t(blockIdx.x) * warps + (threadIdx.x >> 5); r < rows; r += int64_t(gridDim.x) * warps)
+    shared_row<H>(a, r < int64_t(lo) * a.q_heads ? r : r + int64_t(hi - lo) * a.q_heads);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {

@@ -256,7 +256,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();  // the barriers exist; from here the warps start their parts as they can
   // Everything else, the tensor memory included, waits for the previous grid:
   // an allocation held by a grid that waits could starve the one waited for.
-  pdl_wait_prior_grid();
+  // (Own items that join the shared keys' parts run beside the launch that makes
+  // these and wait for it at their end. That launch let this one start when all
+  // its CTAs were on their SMs, and one of these, with nearly all of an SM's
+  // shared memory, is never beside one of those.)
+  if (!a.beside) pdl_wait_prior_grid();
   // What follows within a call (other items, the join) uses no tensor memory
   // and may start now; after a call's only launch anything may follow, and starts
   // when this CTA has its allocation.
@@ -266,9 +270,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const bool works = it.rows > 0 && n > 0;                    // the same in the whole CTA
   const int tiles = it.rows > kTileRows ? 2 : 1;
   if (!works) {
+    if (a.fused) {
+      if (a.beside) pdl_wait_prior_grid();
+      for (int r = warp; r < it.rows; r += kTcThreads / 32) shared_row<H>(a, row_out(a, it, it.r0 + r).row);
+      if (warp < 8) unheld_rows<H>(a, 8);
+      return;
+    }
     for (int r = tid; r < it.rows; r += kTcThreads) {
       const RowOut ro = row_out(a, it, it.r0 + r);
-      *ro.ml = make_float2(-INFINITY, 0.0f);  // (a plan with one range of keys has no empty range)
+      *ro.ml = make_float2(-INFINITY, 0.0f);  // (a plan with one range of shared keys has no empty range)
     }
     return;
   }
@@ -389,16 +399,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(tile == 0 ? &go[i % kGo] : psecond);
       }
-      wait(&sfull[tile], uint32_t(n) & 1u);  // the last product is in O
-      __syncwarp();
-      tc_fence_after();
-      const float l = l2[0].x + l2[0].y + (l2[1].x + l2[1].y);
-      const bool any = l > 0.0f || l != l;
-      const float inv = any ? 1.0f / l : 0.0f;
       const bool mine = r < it.rows;
       const RowOut ro = row_out(a, it, it.r0 + (mine ? r : 0));
-      const float bad = ok ? 0.0f : __uint_as_float(0x7fc00000u);
-      // 128 bytes of every row at a time through this warp's part of the Q
+      // 128 bytes of every row at a time go through this warp's part of the Q
       // tile (its products are done), so that rows leave in whole sectors:
       // 32 columns of partial results, or 64 of the 16-bit output.
       unsigned char* const stage = smem + tile * L::kTile + (warp & 3) * 4096;
@@ -412,7 +415,82 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             0xffffffffu, reinterpret_cast<uint64_t>(a.direct ? ro.out : reinterpret_cast<char*>(ro.part)), rl));
         if (tile * kTileRows + (warp & 3) * 32 + rl >= it.rows) dst[j] = nullptr;
       }
-      const int passes = a.direct ? DP / 64 : DP / 32;
+      const bool joins = a.fused && a.splits > 0;
+      float2 shared = make_float2(-INFINITY, 0.0f);  // the row's shared keys: maximum and sum,
+      float4 z[8];                                   // and 32 columns of their output, of the rows in dst
+      auto shared_part = [&](int c) {
+        const int row = int(ro.row);  // below 2^30
+        const bool there = part_holds(shared);
+        const float* src = a.part + c * 32 + ch * 4;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int rl = 4 * j + (lane >> 3);
+          const int at = __shfl_sync(0xffffffffu, row, rl);
+          const bool here = __shfl_sync(0xffffffffu, int(there), rl) && dst[j] && c * 32 + ch * 4 < a.dim;
+          z[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (here) z[j] = *reinterpret_cast<const float4*>(src + int64_t(at) * a.dim);
+        }
+      };
+      if (joins) {
+        if (a.beside) pdl_wait_prior_grid();
+        shared = a.ml[ro.row];
+        shared_part(0);
+      }
+      wait(&sfull[tile], uint32_t(n) & 1u);  // the last product is in O
+      __syncwarp();
+      tc_fence_after();
+      float l = l2[0].x + l2[0].y + (l2[1].x + l2[1].y);
+      float own = 1.0f, other = 0.0f;  // weights of this item and of the shared keys
+      const bool holds = part_holds(make_float2(m, l));
+      if (joins) {
+        const float top = fmaxf(m, shared.x);
+        own = part_weight(make_float2(m, l), top);
+        l *= own;
+        if (part_holds(shared)) {
+          other = part_weight(shared, top);
+          l = fmaf(shared.y, other, l);
+        }
+        m = top;
+      }
+      const bool any = l > 0.0f || l != l;
+      const float inv = any ? 1.0f / l : 0.0f;
+      const float bad = ok ? 0.0f : __uint_as_float(0x7fc00000u);
+      if (a.fused) {
+        own *= inv;
+        other *= inv;
+#pragma unroll 1
+        for (int c = 0; c < DP / 32; ++c) {
+          float o[32];
+          tmem_ld32(o_col + 32u * c, o);
+          tmem_ld_wait(o, 32);
+          __syncwarp();  // the stage's last pass has been read
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float4 w = make_float4(bad, bad, bad, bad);
+            if (holds)
+              w = make_float4(o[4 * j] * own + bad, o[4 * j + 1] * own + bad, o[4 * j + 2] * own + bad,
+                              o[4 * j + 3] * own + bad);
+            *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = w;
+          }
+          __syncwarp();
+          uint2 y[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int rl = 4 * j + (lane >> 3);
+            const float4 w = *reinterpret_cast<const float4*>(stage + rl * 128 + ((ch ^ (rl & 7)) << 4));
+            const float f = __shfl_sync(0xffffffffu, other, rl);
+            y[j] = joins ? make_uint2(H::down2(fmaf(z[j].x, f, w.x), fmaf(z[j].y, f, w.y)),
+                                      H::down2(fmaf(z[j].z, f, w.z), fmaf(z[j].w, f, w.w)))
+                         : make_uint2(H::down2(w.x, w.y), H::down2(w.z, w.w));
+          }
+          if (joins && c + 1 < DP / 32) shared_part(c + 1);
+          const int col = c * 32 + ch * 4;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (dst[j] && col < a.dim) *reinterpret_cast<uint2*>(dst[j] + col * 2) = y[j];
+        }
+      }
+      const int passes = a.fused ? 0 : a.direct ? DP / 64 : DP / 32;
       float o[32];
       if (!a.direct) tmem_ld32(o_col, o);
 #pragma unroll 1
@@ -457,6 +535,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         else if (ro.lse)
           *ro.lse = any ? fmaf(m, kLn2, logf(l)) : -INFINITY;
       }
+    }
+    if (a.fused) {
+      if (a.beside) pdl_wait_prior_grid();
+      unheld_rows<H>(a, 8);
     }
   } else if (kTma && warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
