@@ -85,13 +85,12 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
   const int ntiles = (it.k1 - it.k0 + kKeys - 1) / kKeys;
 
   // copies of tile i: warp w brings rows 16 w .. 16 w + 15; lane l holds the
-  // offsets of row 16 w + (l & 15), looked up one tile ahead
-  int page = 0;
+  // offsets of row 16 w + (l & 15), its page looked up ahead of that
   auto fetch_page = [&](int i) {
     const int j = it.k0 + i * kKeys + warp * 16 + (lane & 15);
-    if (j < it.k1) page = key_page(a, it, j);
+    return j < it.k1 ? key_page(a, it, j) : 0;
   };
-  auto copy_tile = [&](int i) {
+  auto copy_tile = [&](int i, int page) {
     const int j = it.k0 + i * kKeys + warp * 16 + (lane & 15);
     KeyOffset off{0, 0};
     if (!(j < it.k1 && key_offset(a, it, j, page, &g_prefix_flags, &off))) off.k = off.v = -1;
@@ -110,6 +109,18 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
       cp_async16(dst + kTile, there ? a.v + vo + c * 16 : a.q, there);
     }
   };
+
+  // R = 16: a warp reads only what it brought, so that both stages are under
+  // way from the start and no warp waits for another
+  constexpr int kAhead = R == 64 ? kStages - 1 : kStages;
+  int pages[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) pages[i] = fetch_page(i);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    if (i < ntiles) copy_tile(i, pages[i]);
+    cp_async_commit();
+  }
 
   // the item's rows of Q as A fragments
   const int rbase = R == 64 ? warp * 16 : 0;
@@ -146,23 +157,22 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
     for (int x = 0; x < 4; ++x) o[i][x] = 0.0f;
   float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;
 
-  fetch_page(0);
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    if (i < ntiles) {
-      copy_tile(i);
-      fetch_page(i + 1);
+  int page = fetch_page(kAhead);
+  auto copy_next = [&](int i) {
+    if (i + kAhead < ntiles) {
+      copy_tile(i + kAhead, page);
+      page = fetch_page(i + kAhead + 1);
     }
     cp_async_commit();
-  }
+  };
   for (int i = 0; i < ntiles; ++i) {
-    cp_async_wait<kStages - 2>();
-    __syncthreads();  // tile i landed for every warp; everyone is done with tile i - 1's stage
-    if (i + kStages - 1 < ntiles) {
-      copy_tile(i + kStages - 1);
-      fetch_page(i + kStages);
+    cp_async_wait<kAhead - 1>();
+    if constexpr (R == 64) {
+      __syncthreads();  // tile i landed for every warp; everyone is done with tile i - 1's stage
+      copy_next(i);
+    } else {
+      __syncwarp();
     }
-    cp_async_commit();
     const uint32_t ks = sbase + uint32_t(i % kStages) * (2 * kTile);
     const uint32_t vs = ks + kTile;
     const int kw = R == 64 ? 0 : warp * KW;  // first key of the stage for this warp
@@ -242,6 +252,10 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
         mma16816<H>(o[2 * d + 1], pa, b[2], b[3]);
       }
     }
+    if constexpr (R != 64) {
+      __syncwarp();  // every lane is done with the stage
+      copy_next(i);
+    }
   }
 #pragma unroll
   for (int d = 1; d < 4; d <<= 1) {
@@ -272,14 +286,16 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
 #pragma unroll
     for (int d = 0; d < DP / 8; ++d) {
       const int col = d * 8 + (lane & 3) * 2;
-      *reinterpret_cast<float2*>(so + (warp * 16 + ra) * kPitch + col) = make_float2(o[d][0] * fa, o[d][1] * fa);
-      *reinterpret_cast<float2*>(so + (warp * 16 + rb) * kPitch + col) = make_float2(o[d][2] * fb, o[d][3] * fb);
+      if (ra < it.rows)
+        *reinterpret_cast<float2*>(so + (warp * 16 + ra) * kPitch + col) = make_float2(o[d][0] * fa, o[d][1] * fa);
+      if (rb < it.rows)
+        *reinterpret_cast<float2*>(so + (warp * 16 + rb) * kPitch + col) = make_float2(o[d][2] * fb, o[d][3] * fb);
     }
     __syncthreads();
     // four lanes of a chunk of 4 elements each: thread -> (row, 4 columns)
-    for (int e = threadIdx.x; e < 16 * (DP / 4); e += kThreads) {
+    for (int e = threadIdx.x; e < it.rows * (DP / 4); e += kThreads) {
       const int r = e / (DP / 4), col = (e % (DP / 4)) * 4;
-      if (r >= it.rows || col >= a.dim) continue;
+      if (col >= a.dim) continue;
       float m = -INFINITY, l = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sml[w * 16 + r].x);
