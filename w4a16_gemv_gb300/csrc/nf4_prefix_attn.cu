@@ -40,6 +40,9 @@ struct Shape {
   static constexpr int kThreads = 32 * W;
   static constexpr int kKeys = R == 64 ? 64 : 16 * W;  // keys per stage
 };
+// A row of a stage in shared memory: 16 bytes on, so that eight rows' chunks lie in different banks.
+template <int DP>
+constexpr uint32_t kPitch = DP * 2 + 16;
 constexpr int64_t kFewItems = kSms * 3;  // CTAs of four warps that fit on the SMs
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -77,36 +80,70 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
   constexpr int NB = KW / 8;                            // score blocks of 8 keys
   constexpr int CPR = DP / 8;                           // 16-byte chunks per row
   constexpr int RPI = 32 / CPR;                         // rows per copy instruction of a warp
-  constexpr uint32_t kTile = kKeys * DP * 2;
+  constexpr uint32_t kTile = kKeys * kPitch<DP>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(smem);
-  const int chunks = a.dim / 8;
-  const bool alike = a.k_ps == a.v_ps && a.k_ss == a.v_ss && a.k_hs == a.v_hs;  // one offset serves both caches
   const int ntiles = (it.k1 - it.k0 + kKeys - 1) / kKeys;
 
-  // copies of tile i: warp w brings rows 16 w .. 16 w + 15; lane l holds the
-  // offsets of row 16 w + (l & 15), its page looked up ahead of that
+  // Copies of tile i: warp w brings rows 16 w .. 16 w + 15, lane l chunk l % CPR
+  // of rows l / CPR, l / CPR + RPI, .. What is not there is filled with zeros,
+  // from no address of the cache. Where 16 rows are sure to lie in one page, a
+  // lane's addresses are a slot's stride apart; otherwise lane l looks up row
+  // l & 15 and hands out its offsets. (Instructions bound items of few keys.
+  // One bulk copy per row, no addresses to speak of, is slower all the same: 256
+  // bytes at a time, 64 sequences x 32 heads x 187 keys took 47 us instead of NEW.)
+  const bool whole = a.page_size % 16 == 0;  // (ranges of keys begin at multiples of 64)
+  const int copy_row = lane / CPR, copy_chunk = lane % CPR;
+  const bool column = copy_chunk < a.dim / 8;
+  const uint32_t copy_to = sbase + uint32_t(warp * 16 + copy_row) * kPitch<DP> + uint32_t(copy_chunk) * 16u;
+  const char* const k_head = a.k + int64_t(it.head) * a.k_hs + copy_chunk * 16;
+  const char* const v_head = a.v + int64_t(it.head) * a.v_hs + copy_chunk * 16;
   auto fetch_page = [&](int i) {
-    const int j = it.k0 + i * kKeys + warp * 16 + (lane & 15);
+    const int j = it.k0 + i * kKeys + warp * 16 + (whole ? 0 : lane & 15);
     return j < it.k1 ? key_page(a, it, j) : 0;
   };
   auto copy_tile = [&](int i, int page) {
-    const int j = it.k0 + i * kKeys + warp * 16 + (lane & 15);
+    const int j0 = it.k0 + i * kKeys + warp * 16;
+    const uint32_t dst = copy_to + uint32_t(i % kStages) * (2 * kTile);
+    if (whole) {
+      int valid = min(it.k1 - j0, 16);
+      if (unsigned(page) >= unsigned(a.num_pages)) {
+        if (valid > 0) atomicOr(&g_prefix_flags, kFlagBadIndex);
+        valid = 0;
+      }
+      const int slot = (a.page_shift >= 0 ? j0 & (a.page_size - 1) : j0 % a.page_size) + copy_row;
+      const char* ks = k_head + int64_t(page) * a.k_ps + int64_t(slot) * a.k_ss;
+      const char* vs = v_head + int64_t(page) * a.v_ps + int64_t(slot) * a.v_ss;
+      if (valid == 16 && a.dim == DP) {
+#pragma unroll
+        for (int x = 0; x < 16 / RPI; ++x) {
+          cp_async16(dst + uint32_t(x * RPI) * kPitch<DP>, ks, true);
+          cp_async16(dst + uint32_t(x * RPI) * kPitch<DP> + kTile, vs, true);
+          ks += RPI * a.k_ss;
+          vs += RPI * a.v_ss;
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 16 / RPI; ++x) {
+          const bool there = x * RPI + copy_row < valid && column;
+          cp_async16(dst + uint32_t(x * RPI) * kPitch<DP>, there ? ks : a.q, there);
+          cp_async16(dst + uint32_t(x * RPI) * kPitch<DP> + kTile, there ? vs : a.q, there);
+          ks += RPI * a.k_ss;
+          vs += RPI * a.v_ss;
+        }
+      }
+      return;
+    }
+    const int j = j0 + (lane & 15);
     KeyOffset off{0, 0};
     if (!(j < it.k1 && key_offset(a, it, j, page, &g_prefix_flags, &off))) off.k = off.v = -1;
-    const uint32_t ks = sbase + uint32_t(i % kStages) * (2 * kTile);
-    const int c = lane % CPR;
 #pragma unroll
     for (int x = 0; x < 16 / RPI; ++x) {
-      const int rl = x * RPI + lane / CPR;  // row within the warp's 16
-      const int64_t ko = __shfl_sync(0xffffffffu, off.k, rl);
-      const int64_t vo = alike ? ko : __shfl_sync(0xffffffffu, off.v, rl);
-      const bool there = ko >= 0 && c < chunks;
-      const int row = warp * 16 + rl;
-      const uint32_t dst = ks + uint32_t(row) * (DP * 2) + uint32_t((c ^ (row & 7)) << 4);
-      // what is not there is filled with zeros, from no address of the cache
-      cp_async16(dst, there ? a.k + ko + c * 16 : a.q, there);
-      cp_async16(dst + kTile, there ? a.v + vo + c * 16 : a.q, there);
+      const int64_t ko = __shfl_sync(0xffffffffu, off.k, x * RPI + copy_row);
+      const int64_t vo = __shfl_sync(0xffffffffu, off.v, x * RPI + copy_row);
+      const bool there = ko >= 0 && column;
+      cp_async16(dst + uint32_t(x * RPI) * kPitch<DP>, there ? a.k + ko + copy_chunk * 16 : a.q, there);
+      cp_async16(dst + uint32_t(x * RPI) * kPitch<DP> + kTile, there ? a.v + vo + copy_chunk * 16 : a.q, there);
     }
   };
 
@@ -125,6 +162,7 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
   // the item's rows of Q as A fragments
   const int rbase = R == 64 ? warp * 16 : 0;
   const int ra = rbase + (lane >> 2), rb = ra + 8;  // this thread's two rows of the tile
+  const bool two = R == 64 || it.rows > 8;          // there is a second one
   uint32_t qf[DP / 16][4];
   {
     const char* qp[2];
@@ -133,16 +171,24 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
     for (int x = 0; x < 2; ++x) {
       const int rl = x ? rb : ra;
       there[x] = rl < it.rows;
+      qp[x] = a.q;
+      if (x && !two) break;
       const int r = it.r0 + (there[x] ? rl : 0);
       qp[x] = a.q + int64_t(it.t0 + r / a.group) * a.q_ts + int64_t(it.head * a.group + r % a.group) * a.q_hs;
     }
 #pragma unroll
-    for (int s = 0; s < DP / 16; ++s)
+    for (int x = 0; x < 2; ++x) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int d = s * 16 + (x >> 1) * 8 + (lane & 3) * 2;
-        qf[s][x] = there[x & 1] && d < a.dim ? __ldg(reinterpret_cast<const uint32_t*>(qp[x & 1] + d * 2)) : 0u;
-      }
+      for (int s = 0; s < DP / 16; ++s) qf[s][x] = qf[s][x + 2] = 0u;
+      if (x && !two) break;
+#pragma unroll
+      for (int s = 0; s < DP / 16; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int d = s * 16 + h * 8 + (lane & 3) * 2;
+          if (there[x] && d < a.dim) qf[s][x + 2 * h] = __ldg(reinterpret_cast<const uint32_t*>(qp[x] + d * 2));
+        }
+    }
   }
   // keys (within the segment) that the two rows see
   const int lima = ra < it.rows ? min(visible_keys(it, (it.r0 + ra) / a.group), it.k1) : 0;
@@ -165,6 +211,10 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
     }
     cp_async_commit();
   };
+  const int kw = R == 64 ? 0 : warp * KW;  // first key of a stage for this warp
+  const uint32_t klane = sbase + uint32_t(kw + (lane & 7) + ((lane >> 4) << 3)) * kPitch<DP> + ((lane & 8) << 1);
+  const uint32_t vlane = sbase + kTile + uint32_t(kw + (lane & 15)) * kPitch<DP> + (lane & 16);
+  bool first = true;
   for (int i = 0; i < ntiles; ++i) {
     cp_async_wait<kAhead - 1>();
     if constexpr (R == 64) {
@@ -173,83 +223,89 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
     } else {
       __syncwarp();
     }
-    const uint32_t ks = sbase + uint32_t(i % kStages) * (2 * kTile);
-    const uint32_t vs = ks + kTile;
-    const int kw = R == 64 ? 0 : warp * KW;  // first key of the stage for this warp
-
-    float s[NB][4];
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) s[n][x] = 0.0f;
-#pragma unroll
-    for (int st = 0; st < DP / 16; ++st)
-#pragma unroll
-      for (int n = 0; n < NB / 2; ++n) {
-        const int key = kw + n * 16 + (lane & 7) + ((lane >> 4) << 3);
-        const int c = st * 2 + ((lane >> 3) & 1);
-        uint32_t b[4];
-        ldsm4(ks + uint32_t(key) * (DP * 2) + uint32_t((c ^ (key & 7)) << 4), b);
-        mma16816<H>(s[2 * n], qf[st], b[0], b[1]);
-        mma16816<H>(s[2 * n + 1], qf[st], b[2], b[3]);
-      }
-
-    const int j0 = it.k0 + i * kKeys + kw + (lane & 3) * 2;
-    if (it.k0 + (i + 1) * kKeys > free_to) {
+    const uint32_t stage = uint32_t(i % kStages) * (2 * kTile);
+    if (it.k0 + i * kKeys + kw < it.k1) {  // some of this warp's keys are there
+      float s[NB][4];
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (j0 + n * 8 + (x & 1) >= (x < 2 ? lima : limb)) s[n][x] = -INFINITY;
-    }
-    float xa = -INFINITY, xb = -INFINITY;
+        for (int x = 0; x < 4; ++x) s[n][x] = 0.0f;
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      xa = fmaxf(xa, fmaxf(s[n][0], s[n][1]));
-      xb = fmaxf(xb, fmaxf(s[n][2], s[n][3]));
-    }
+      for (int st = 0; st < DP / 16; ++st)
 #pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-      xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, d));
-      xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, d));
-    }
-    const float na = fmaxf(ma, xa * a.scale_log2), nb = fmaxf(mb, xb * a.scale_log2);
-    const float ba = na == -INFINITY ? 0.0f : na, bb = nb == -INFINITY ? 0.0f : nb;
-    if (__any_sync(0xffffffffu, na != ma || nb != mb)) {  // a maximum grew
-      const float fa = ex2(ma - ba), fb = ex2(mb - bb);
-      ma = na;
-      mb = nb;
-      la *= fa;
-      lb *= fb;
+        for (int n = 0; n < NB / 2; ++n) {
+          uint32_t b[4];
+          ldsm4(klane + stage + uint32_t(n * 16) * kPitch<DP> + uint32_t(st * 32), b);
+          mma16816<H>(s[2 * n], qf[st], b[0], b[1]);
+          mma16816<H>(s[2 * n + 1], qf[st], b[2], b[3]);
+        }
+
+      const int j0 = it.k0 + i * kKeys + kw + (lane & 3) * 2;
+      if (it.k0 + (i + 1) * kKeys > free_to) {
 #pragma unroll
-      for (int d = 0; d < DP / 8; ++d) {
-        o[d][0] *= fa;
-        o[d][1] *= fa;
-        o[d][2] *= fb;
-        o[d][3] *= fb;
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (j0 + n * 8 + (x & 1) >= (x < 2 ? lima : limb)) s[n][x] = -INFINITY;
       }
-    }
-    uint32_t pf[NB][2];
+      float xa = -INFINITY, xb = -INFINITY;
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const float p0 = ex2(fmaf(s[n][0], a.scale_log2, -ba)), p1 = ex2(fmaf(s[n][1], a.scale_log2, -ba));
-      const float p2 = ex2(fmaf(s[n][2], a.scale_log2, -bb)), p3 = ex2(fmaf(s[n][3], a.scale_log2, -bb));
-      la += p0 + p1;
-      lb += p2 + p3;
-      pf[n][0] = H::down2(p0, p1);
-      pf[n][1] = H::down2(p2, p3);
-    }
+      for (int n = 0; n < NB; ++n) xa = fmaxf(xa, fmaxf(s[n][0], s[n][1]));
+      if (two) {
 #pragma unroll
-    for (int n = 0; n < NB / 2; ++n) {
-      const uint32_t pa[4] = {pf[2 * n][0], pf[2 * n][1], pf[2 * n + 1][0], pf[2 * n + 1][1]};
+        for (int n = 0; n < NB; ++n) xb = fmaxf(xb, fmaxf(s[n][2], s[n][3]));
+      }
 #pragma unroll
-      for (int d = 0; d < DP / 16; ++d) {
-        const int key = kw + n * 16 + (lane & 7) + (((lane >> 3) & 1) << 3);
-        const int c = d * 2 + (lane >> 4);
-        uint32_t b[4];
-        ldsm4t(vs + uint32_t(key) * (DP * 2) + uint32_t((c ^ (key & 7)) << 4), b);
-        mma16816<H>(o[2 * d], pa, b[0], b[1]);
-        mma16816<H>(o[2 * d + 1], pa, b[2], b[3]);
+      for (int d = 1; d < 4; d <<= 1) {
+        xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, d));
+        if (two) xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, d));
+      }
+      xa *= a.scale_log2;
+      xb *= a.scale_log2;
+      // m is the maximum at the time of the last rescale; l and o share it
+      if (first) {
+        ma = xa;
+        mb = xb;
+        first = false;
+      } else if (__any_sync(0xffffffffu, xa > ma + kGrowth || xb > mb + kGrowth)) {
+        const float na = fmaxf(ma, xa), nb = fmaxf(mb, xb);
+        const float fa = na == -INFINITY ? 1.0f : ex2(ma - na), fb = nb == -INFINITY ? 1.0f : ex2(mb - nb);
+        ma = na;
+        mb = nb;
+        la *= fa;
+        lb *= fb;
+#pragma unroll
+        for (int d = 0; d < DP / 8; ++d) {
+          o[d][0] *= fa;
+          o[d][1] *= fa;
+          o[d][2] *= fb;
+          o[d][3] *= fb;
+        }
+      }
+      const float ba = ma == -INFINITY ? 0.0f : ma, bb = mb == -INFINITY ? 0.0f : mb;
+      uint32_t pf[NB][2];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const float p0 = ex2(fmaf(s[n][0], a.scale_log2, -ba)), p1 = ex2(fmaf(s[n][1], a.scale_log2, -ba));
+        la += p0 + p1;
+        pf[n][0] = H::down2(p0, p1);
+        pf[n][1] = 0u;
+        if (two) {
+          const float p2 = ex2(fmaf(s[n][2], a.scale_log2, -bb)), p3 = ex2(fmaf(s[n][3], a.scale_log2, -bb));
+          lb += p2 + p3;
+          pf[n][1] = H::down2(p2, p3);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NB / 2; ++n) {
+        const uint32_t pa[4] = {pf[2 * n][0], pf[2 * n][1], pf[2 * n + 1][0], pf[2 * n + 1][1]};
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) {
+          uint32_t b[4];
+          ldsm4t(vlane + stage + uint32_t(n * 16) * kPitch<DP> + uint32_t(d * 32), b);
+          mma16816<H>(o[2 * d], pa, b[0], b[1]);
+          mma16816<H>(o[2 * d + 1], pa, b[2], b[3]);
+        }
       }
     }
     if constexpr (R != 64) {
@@ -270,7 +326,7 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
     __syncthreads();  // the stages are free
     float2* sml = reinterpret_cast<float2*>(smem);             // [warp][16]
     float* so = reinterpret_cast<float*>(smem + 512);          // [warp][16][DP + 4]
-    constexpr int kPitch = DP + 4;
+    constexpr int kStep = DP + 4;
     if ((lane & 3) == 0) {
       sml[warp * 16 + ra] = make_float2(ma, la);
       sml[warp * 16 + rb] = make_float2(mb, lb);
@@ -287,9 +343,9 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
     for (int d = 0; d < DP / 8; ++d) {
       const int col = d * 8 + (lane & 3) * 2;
       if (ra < it.rows)
-        *reinterpret_cast<float2*>(so + (warp * 16 + ra) * kPitch + col) = make_float2(o[d][0] * fa, o[d][1] * fa);
+        *reinterpret_cast<float2*>(so + (warp * 16 + ra) * kStep + col) = make_float2(o[d][0] * fa, o[d][1] * fa);
       if (rb < it.rows)
-        *reinterpret_cast<float2*>(so + (warp * 16 + rb) * kPitch + col) = make_float2(o[d][2] * fb, o[d][3] * fb);
+        *reinterpret_cast<float2*>(so + (warp * 16 + rb) * kStep + col) = make_float2(o[d][2] * fb, o[d][3] * fb);
     }
     __syncthreads();
     // four lanes of a chunk of 4 elements each: thread -> (row, 4 columns)
@@ -304,7 +360,7 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
       for (int w = 0; w < kWarps; ++w) {
         const float2 x = sml[w * 16 + r];
         l += x.x == -INFINITY ? x.y : x.y * ex2(x.x - m);  // x.y is 0, or NaN
-        const float4 y = *reinterpret_cast<const float4*>(so + (w * 16 + r) * kPitch + col);
+        const float4 y = *reinterpret_cast<const float4*>(so + (w * 16 + r) * kStep + col);
         v.x += y.x;
         v.y += y.y;
         v.z += y.z;
@@ -354,7 +410,8 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
 // what follows (the join) only waits for this launch, so its last CTA ends
 // after the other launch did.
 template <typename H, int DP, int R, int W>
-__global__ void __launch_bounds__(Shape<R, W>::kThreads) prefix_mma_kernel(const __grid_constant__ PrefixArgs a) {
+__global__ void __launch_bounds__(Shape<R, W>::kThreads, R == 64 ? 2 : (DP == 64 ? 20 : 12) / W)
+    prefix_mma_kernel(const __grid_constant__ PrefixArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   if (!a.beside) pdl_wait_prior_grid();
   pdl_allow_dependents();
@@ -540,7 +597,7 @@ __global__ void __launch_bounds__(128) prefix_empty_kernel(const __grid_constant
 template <typename H, int DP, int R, int W>
 cudaError_t launch_mma(const PrefixArgs& p, unsigned items, cudaStream_t stream) {
   auto kern = prefix_mma_kernel<H, DP, R, W>;
-  constexpr int smem = kStages * 2 * Shape<R, W>::kKeys * DP * 2;
+  constexpr int smem = kStages * 2 * Shape<R, W>::kKeys * int(kPitch<DP>);
   static PerDeviceCache attr_set;
   const cudaError_t e = set_max_dynamic_smem_once(kern, smem, attr_set);
   if (e != cudaSuccess) return e;
@@ -641,15 +698,32 @@ int64_t tc_range(int64_t row_tiles, int64_t key_tiles, int64_t rows, int sms) {
   return 2 * int64_t(best);
 }
 
-// The own keys run on another kernel beside the shared ones. Where they are
-// the longer part (bound by their bytes, at about 6 TB/s), the shared keys are
-// cut into fewer ranges, so that they take no longer (about 1.2 us per key tile
-// of 128) but leave the other SMs to the own keys meanwhile: 64 sequences x 32
-// heads over 2048 shared and 190 own keys 55 -> 49 us.
-int64_t beside_range(const nf4_prefix_attention_args& a, const PrefixArgs& p, int64_t per, int64_t longest) {
-  const double own_us = double(a.batch) * double(p.suffix_max) * double(p.k_heads) * double(p.dim) * 4.0 / 6e6;
-  const int64_t room = 2 * (int64_t(own_us * 0.8 / 1.2) - 3);
-  return room <= per ? per : room < longest ? room : longest;
+// The own keys run on another kernel beside the shared ones. Where they are the
+// longer part (bound by their bytes, at about 6 TB/s; sequences hold some 80% of
+// the longest on average), the shared keys are cut into fewer ranges, which
+// cost less start and partial results and leave the other SMs to the own keys:
+// the number that lets both end soonest. A key tile takes about 1.7 us beside
+// own keys (2.0 with two tiles of rows; 0.8 of that at 64 elements), a range
+// three more. 64 sequences x 32 heads over 2048 shared and 187 own keys take 45
+// us, 53 with ranges for every SM; 128 x 32 heads over 8, 4000 and 300: 44 and 55.
+int64_t beside_range(const nf4_prefix_attention_args& a, const PrefixArgs& p, int64_t tiles, int64_t key_tiles,
+                     int64_t rows, int64_t per) {
+  const double own = double(a.batch) * double(p.suffix_max) * double(p.k_heads) * double(p.dim) * 4.0 * 0.8 / 6e6;
+  const double tile = (rows <= 128 ? 1.7 : 2.0) * (p.dim <= 64 ? 0.8 : 1.0);
+  if (own < (double(per) * 0.5 + 3.0) * 1.2) return per;
+  double least = 0.0;
+  for (int64_t s = 1; s * tiles <= kSms && s <= key_tiles; ++s) {
+    const int64_t each = (key_tiles + s - 1) / s, ctas = tiles * ((key_tiles + each - 1) / each);
+    const double shared = double(each + 3) * tile;
+    const double alone = shared * double(kSms - ctas);  // of the SMs left to the own keys
+    const double cost = (own * kSms <= alone ? shared : own + shared - alone / kSms) +
+                        double(s) * double(rows) * double(p.k_heads) * 1e-4;
+    if (least == 0.0 || cost < least) {
+      least = cost;
+      per = 2 * each;
+    }
+  }
+  return per;
 }
 
 // Where the shared keys would take every SM once, and the own keys are little
@@ -713,7 +787,7 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
       // ranges and more to read back: 16 prompts of 100 35 instead of 29.
       p->fused = p->suffix_splits == 1 && p->suffix_rows == 256 && pk <= per;
       if (!p->fused && p->suffix_rows != 256 && sk > 0) {
-        per = beside_range(a, *p, per, 2 * longest);
+        per = beside_range(a, *p, tiles, longest, rows, per);
         const int keep = sms_for_own(*p, likely * p->k_heads * p->suffix_splits, tiles, per, pk);
         if (keep > 0) per = tc_range(tiles, longest, rows * p->k_heads, kSms - keep);
       }

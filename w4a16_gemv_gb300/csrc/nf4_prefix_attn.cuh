@@ -179,6 +179,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGrowth = 8.0f;  // log2 of the growth of a row's maximum that is let pass
 
 // Where a finished row goes: the partial results, or the output itself.
 struct RowOut {

@@ -55,7 +55,6 @@ constexpr int kTileRows = 128;
 constexpr int kTileKeys = 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kGo = 4;  // key tiles whose loads may be under way (a ring of 8 tiles holds less than 4 pairs)
-constexpr float kGrowth = 8.0f;  // log2 of the growth of a row's maximum that is let pass
 // Registers: 512 threads launch with 128 each (65536); the two softmax
 // warpgroups take 184, the others keep 72: 256 x 184 + 256 x 72 = 65536. (With
 // 192 and 64 the loading and issuing warps spill, and a spill's reload behind
