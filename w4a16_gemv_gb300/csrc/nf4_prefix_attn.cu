@@ -123,7 +123,7 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
           vs += RPI * a.v_ss;
         }
       } else {
-#pragma unroll
+#pragma unroll 2
         for (int x = 0; x < 16 / RPI; ++x) {
           const bool there = x * RPI + copy_row < valid && column;
           cp_async16(dst + uint32_t(x * RPI) * kPitch<DP>, there ? ks : a.q, there);
@@ -137,7 +137,7 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
     const int j = j0 + (lane & 15);
     KeyOffset off{0, 0};
     if (!(j < it.k1 && key_offset(a, it, j, page, &g_prefix_flags, &off))) off.k = off.v = -1;
-#pragma unroll
+#pragma unroll 2
     for (int x = 0; x < 16 / RPI; ++x) {
       const int64_t ko = __shfl_sync(0xffffffffu, off.k, x * RPI + copy_row);
       const int64_t vo = __shfl_sync(0xffffffffu, off.v, x * RPI + copy_row);
@@ -150,13 +150,13 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
   // R = 16: a warp reads only what it brought, so that both stages are under
   // way from the start and no warp waits for another
   constexpr int kAhead = R == 64 ? kStages - 1 : kStages;
-  int pages[kAhead];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) pages[i] = fetch_page(i);
-#pragma unroll
+  int page = fetch_page(0), next_page = fetch_page(1);
+#pragma unroll 1
   for (int i = 0; i < kAhead; ++i) {
-    if (i < ntiles) copy_tile(i, pages[i]);
+    if (i < ntiles) copy_tile(i, page);
     cp_async_commit();
+    page = next_page;
+    if (i + 1 < kAhead) next_page = fetch_page(i + 2);
   }
 
   // the item's rows of Q as A fragments
@@ -203,7 +203,6 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
     for (int x = 0; x < 4; ++x) o[i][x] = 0.0f;
   float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;
 
-  int page = fetch_page(kAhead);
   auto copy_next = [&](int i) {
     if (i + kAhead < ntiles) {
       copy_tile(i + kAhead, page);
