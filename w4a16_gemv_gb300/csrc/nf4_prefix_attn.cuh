@@ -39,6 +39,7 @@ struct PrefixArgs {
   int direct;                                      // 1: the items write the output
   int fused;                                       // 1: one range of own keys, whose items write the output, with
                                                    // the one range of shared keys, if any, joined in
+  int stream;                                      // 1: the shared keys leave L2 first
   int first;                                       // first item of the launch
   int beside;                                      // 1: runs beside the launch before it of the same call
   float* part;                                     // [splits][tokens * q_heads][dim]
@@ -215,7 +216,9 @@ __device__ __forceinline__ void write_row(char* out, float* lse, int col, float 
 // Whether a part (maximum, sum) holds a key, and its weight when the row's
 // maximum is m. (A maximum of -inf with a sum: of NaN.)
 __device__ __forceinline__ bool part_holds(const float2& x) { return !(x.x == -INFINITY && x.y == 0.0f); }
-__device__ __forceinline__ float part_weight(const float2& x, float m) { return x.x == -INFINITY ? 1.0f : ex2(x.x - m); }
+__device__ __forceinline__ float part_weight(const float2& x, float m) {
+  return x.x == -INFINITY ? 1.0f : ex2(x.x - m);
+}
 
 // Row `row` with shared keys only (one range of them, or none), by a whole warp.
 template <typename H>
@@ -229,7 +232,8 @@ __device__ __forceinline__ void shared_row(const PrefixArgs& a, int64_t row) {
     if (part_holds(x)) v = *reinterpret_cast<const float4*>(a.part + row * a.dim + col);
   }
   const int64_t t = row / a.q_heads;
-  write_row<H>(a.out + t * a.out_ts + (row - t * a.q_heads) * a.out_hs, a.lse ? a.lse + row : nullptr, col, x.x, x.y, v);
+  char* const out = a.out + t * a.out_ts + (row - t * a.q_heads) * a.out_hs;
+  write_row<H>(out, a.lse ? a.lse + row : nullptr, col, x.x, x.y, v);
 }
 
 // The rows of tokens that no sequence holds, dealt out to the first `warps`

@@ -190,16 +190,25 @@ struct CacheMaps {
   int k_slot, k_head, v_slot, v_head;
 };
 
+// One box; `leave_first`: its lines leave L2 before others.
 __device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, int x, int slot_at, int head_at,
-                                             int slot, int head, int page, uint64_t* bar) {
+                                             int slot, int head, int page, uint64_t* bar, bool leave_first) {
   const int c1 = slot_at == 0 ? slot : head_at == 0 ? head : page;
   const int c2 = slot_at == 1 ? slot : head_at == 1 ? head : page;
   const int c3 = slot_at == 2 ? slot : head_at == 2 ? head : page;
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-      : "memory");
+  if (leave_first)
+    asm volatile(
+        "{\n\t.reg .b64 p;\n\tcreatepolicy.fractional.L2::evict_first.b64 p, 1.0;\n\t"
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+        "[%1, {%2, %3, %4, %5}], [%6], p;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
 }
 
 template <int DP>
@@ -548,6 +557,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int per_tile = (kTileKeys / rows) * L::kBlocks;  // boxes of a tile: up to 32
       const int box = lane / L::kBlocks, block = lane % L::kBlocks;
       const bool mine = lane < per_tile;
+      const bool leave_first = !it.own && a.stream;
       // (page, first slot) of this lane's box of key tile i; past the range, or
       // on a page that does not exist, the first page past the end
       int page = a.num_pages, slot0 = 0;
@@ -582,9 +592,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                uint32_t(box * rows) * 128u;
           if (mine) {
             if (kv == 0)
-              tma_load_box(dst, &maps.k, block * 64, maps.k_slot, maps.k_head, slot0, it.head, page, bar);
+              tma_load_box(dst, &maps.k, block * 64, maps.k_slot, maps.k_head, slot0, it.head, page, bar,
+                           leave_first);
             else
-              tma_load_box(dst, &maps.v, block * 64, maps.v_slot, maps.v_head, slot0, it.head, page, bar);
+              tma_load_box(dst, &maps.v, block * 64, maps.v_slot, maps.v_head, slot0, it.head, page, bar,
+                           leave_first);
           }
         }
         page = next_page;
