@@ -13,10 +13,13 @@
 //
 // Here: the plan, the kernel for items of few rows and the join. Few rows (a
 // token and its group of query heads) make every key and value used by a
-// handful of rows only: the bytes of the cache bound them (256 sequences x 32
-// heads x 2048 keys: 6.9 to 7.1 TB/s; 64 x 32 x 250 keys, ranges of a few stages:
-// 4.8 TB/s), and the 16 x 8 x 16 tensor instruction does the arithmetic, since
-// the 128 rows of the 5th-generation ones would be empty.
+// handful of rows only: the bytes of the cache bound them, and the 16 x 8 x 16
+// tensor instruction does the arithmetic, since the 128 rows of the
+// 5th-generation ones would be empty. Own keys alone, 32 heads of 128: 128
+// sequences of 187 keys take 64-66 us (6.1 TB/s, 90% of measured copy
+// bandwidth), 64 of 750 keys 129 us (93%). Short sequences are bound by a
+// warp's instructions (start, addresses, epilogue: 2200 of them for 75 keys before
+// the addresses were made cheaper): 128 x 75 keys 35 us (67%).
 #include "nf4_prefix_attn.cuh"
 
 namespace nf4 {
@@ -30,7 +33,7 @@ constexpr int kStages = 2;
 
 // R rows per tile, W warps. R = 64: a warp has 16 rows and all keys of a stage
 // of 64. R = 16: the warps share the rows and have 16 keys of a stage each.
-// Where there are enough items, two warps: small CTAs (32 KB at 128 elements), so
+// Where there are enough items, two warps: small CTAs (34 KB at 128 elements), so
 // that six are on an SM and the start of one (three dependent loads before its
 // first keys) hides behind the keys of the others. Where all items fit on the
 // SMs at once, four: a short range is one stage (two sequences over 300 keys
@@ -91,7 +94,7 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
   // lane's addresses are a slot's stride apart; otherwise lane l looks up row
   // l & 15 and hands out its offsets. (Instructions bound items of few keys.
   // One bulk copy per row, no addresses to speak of, is slower all the same: 256
-  // bytes at a time, 64 sequences x 32 heads x 187 keys took 47 us instead of NEW.)
+  // bytes at a time, 64 sequences x 32 heads x 187 keys took 47 us instead of 37.)
   const bool whole = a.page_size % 16 == 0;  // (ranges of keys begin at multiples of 64)
   const int copy_row = lane / CPR, copy_chunk = lane % CPR;
   const bool column = copy_chunk < a.dim / 8;

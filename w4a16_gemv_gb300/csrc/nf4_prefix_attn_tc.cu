@@ -31,6 +31,8 @@
 //   * warp 12: issues the products. S of the next keys follows O += P V of a
 //     tile in issue order, so P is read before S overwrites it, and the signal
 //     that S is complete also says that O is at rest.
+// An item leaves its partial result, or the output; an item of own keys of a call
+// with one range of each joins the shared keys' part of its rows on the way out.
 // Tensor memory: S (and P) of the tiles in columns 0 and 128, O in 256 and 384.
 // Measured: 4864 tokens x 8 query heads over 16384 keys of 2 heads x 128 in
 // bf16 take 193 us (1690 TFLOP/s, 89% of measured bf16 peak; head_dim 64: 172 us,

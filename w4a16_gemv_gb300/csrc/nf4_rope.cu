@@ -243,11 +243,11 @@ __device__ __forceinline__ bool slot_base(const RopeArgs& a, int64_t slot, int s
 
 constexpr int kRopeThreads = 128;
 // Blocks of four warps, five on an SM (96 registers; six where a chunk has four
-// elements and 80 do), four rows under way per
-// warp through shared memory. 8192 tokens x 64 heads of 128 in bf16, us: rows
-// under way in registers, the next one only, 51.6, four 60.3 (too few warps);
-// through shared memory two 48.0, four 45.2, six 46.1 (and with six blocks 46.0,
-// with eight, whose 64 registers spill, 51.4).
+// elements and 80 do), four rows under way per warp through shared memory. 8192
+// tokens x 64 heads of 128 in bf16, us: rows under way in registers, the next one
+// only, 51.6, four 60.3 (too few warps); through shared memory two 48.0, four
+// 45.2, six 46.1 (and with six blocks 46.0, with eight, whose 64 registers spill,
+// 51.4).
 template <typename E>
 constexpr int kRopeBlocks = E::kPer == 8 ? 5 : 6;
 constexpr int kInFlight = 4;
