@@ -264,17 +264,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
   }
   __syncthreads();  // the barriers exist; from here the warps start their parts as they can
-  // Everything else, the tensor memory included, waits for the previous grid:
-  // an allocation held by a grid that waits could starve the one waited for.
-  // (Own items that join the shared keys' parts run beside the launch that makes
-  // these and wait for it at their end. That launch let this one start when all
-  // its CTAs were on their SMs, and one of these, with nearly all of an SM's
-  // shared memory, is never beside one of those.)
-  if (!a.beside) pdl_wait_prior_grid();
-  // What follows within a call (other items, the join) uses no tensor memory
-  // and may start now; after a call's only launch anything may follow, and starts
-  // when this CTA has its allocation.
-  if (!a.direct) pdl_allow_dependents();
+  // Reads and writes of device memory, and the tensor memory, wait for the previous
+  // grid (an allocation held by a grid that waits could starve the one waited
+  // for); an item of shared keys is known before that, and each part waits when it
+  // has worked out its addresses. (Own items that join the shared keys' parts run
+  // beside the launch that makes these and wait for it at their end. That launch
+  // let this one start when all its CTAs were on their SMs, and one of these, with
+  // nearly all of an SM's shared memory, is never beside one of those.)
+  auto begin = [&]() {
+    if (!a.beside) pdl_wait_prior_grid();
+  };
+  if (unsigned(a.first) + blockIdx.x >= unsigned(a.prefix_tiles) * unsigned(a.k_heads) * unsigned(a.prefix_splits))
+    begin();
   const PrefixItem it = prefix_item(a, unsigned(a.first) + blockIdx.x, &g_prefix_tc_flags);
   const int n = (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys;  // key tiles
   const bool works = it.rows > 0 && n > 0;                    // the same in the whole CTA
@@ -286,6 +287,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (warp < 8) unheld_rows<H>(a, 8);
       return;
     }
+    begin();
     for (int r = tid; r < it.rows; r += kTcThreads) {
       const RowOut ro = row_out(a, it, it.r0 + r);
       *ro.ml = make_float2(-INFINITY, 0.0f);  // (a plan with one range of shared keys has no empty range)
@@ -309,7 +311,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int tile = warp >> 2;
     // Q: each warp asks for its 32 rows first
-    if (tile < tiles) {
+    if (tile >= tiles) {
+      begin();
+    } else {
       constexpr int kQChunks = DP / 8, kQStep = 32 / kQChunks;
       const int r = warp * 32 + lane, c = lane % kQChunks;
       int64_t off = 0;
@@ -318,6 +322,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         off = int64_t(it.t0 + t) * a.q_ts + int64_t(it.head * a.group + (it.r0 + r - t * a.group)) * a.q_hs;
       }
       const uint32_t dst = sbase + uint32_t(tile) * L::kTile + uint32_t(c >> 3) * L::kBlock;
+      begin();
 #pragma unroll
       for (int x = 0; x < 32 / kQStep; ++x) {
         const int rl = x * kQStep + lane / kQChunks, row = (warp & 3) * 32 + rl;
@@ -572,6 +577,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           *sl = a.page_shift >= 0 ? j & (a.page_size - 1) : j % a.page_size;
         }
       };
+      begin();
       fetch(0, &page, &slot0);
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
@@ -634,6 +640,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (j < it.k1) page = key_page(a, it, j);
     };
     auto landed = [&](int u) { return u == 0 ? kfirst : &go[((u - 1) >> 1) % kGo]; };
+    begin();
     fetch_page(0);
 #pragma unroll 1
     for (int u = 0; u < 2 * n; ++u) {
@@ -674,6 +681,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 12) {
+      begin();
+      // What follows within a call (other items, the join) uses no tensor memory
+      // and may start now; after a call's only launch anything may follow, and
+      // starts when this CTA has its allocation.
+      if (!a.direct) pdl_allow_dependents();
       asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_taddr)),
                    "r"(kTmemCols)
                    : "memory");
