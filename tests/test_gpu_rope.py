@@ -227,6 +227,25 @@ def test_append_at_smaller_alignments(dim, rot, shift):
         assert torch.equal(base[1, ..., dim:], before[1, ..., dim:])
 
 
+def test_heads_far_apart():
+    """A head stride whose offsets pass 32 bits, of the inputs and of the outputs."""
+    dt, step = torch.bfloat16, (1 << 30) + 16
+    g = gen(3)
+    buf = torch.empty(2 * step + 3 * 128, dtype=dt, device="cuda")
+    far = buf.as_strided((3, 3, 128), (128, step, 1))
+    near = torch.randn(3, 3, 128, device="cuda", generator=g).to(dt)
+    far.copy_(near)
+    pos = torch.tensor([5, 0, 29], device="cuda")
+    t = lib().nf4_rope_table(30, 128)
+    w = (1 + 0.2 * torch.randn(128, device="cuda", generator=g)).to(dt)
+    cos, sin = angles(pos, frequencies(128))
+    a, b = lib().nf4_qk_norm_rope(far, near, pos, t, q_weight=w, k_weight=w)
+    check(a, expected(near, w, cos, sin, False, 1e-6), "q")
+    out = lib().nf4_qk_norm_rope(near, near, pos, t, q_weight=w, k_weight=w, q_out=far)
+    check(out[0], expected(near, w, cos, sin, False, 1e-6), "q")
+    assert torch.equal(out[1], b)
+
+
 def test_extreme_rows():
     """Rows of zeros, of the largest and of subnormal values, and rows with infinities and NaN (which stay in
     their row)."""

@@ -285,21 +285,21 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<E>) rope_rows_kernel
     const char* src;   // this lane's first chunk of head 0
     int from, to;
     int last;          // the last head
-    int64_t head_step;
+    int head_step;     // bytes
   };
   auto part_of = [&](int kind) {
     const RowSet& r = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
     const int first = kind == 0 ? 0 : kind == 1 ? a.gq : a.gq + a.gk;
     const int n = kind == 0 ? a.gq : kind == 1 ? a.gk : a.gv;
     return Part{r.in + int64_t(t) * r.in_ts * E::kSize + c0, max(g - first, 0),
-                min(g_end - first, n), r.heads - 1, r.in_hs * E::kSize};
+                min(g_end - first, n), r.heads - 1, int(r.in_hs) * E::kSize};
   };
   // Rows under way, in shared memory; every lane reads back only what it brought.
   __shared__ __align__(16) Chunk ring[kRopeThreads / 32][kInFlight][2][32];
   auto& mine = ring[threadIdx.x >> 5];
   auto load = [&](const Part& s, int gi) {
     if (gi < s.to) {
-      const char* p = s.src + int64_t(min(gi * rows + sub, s.last)) * s.head_step;
+      const char* p = s.src + min(gi * rows + sub, s.last) * s.head_step;
       const int slot = (gi - s.from) % kInFlight;
       E::copy(smem_u32(&mine[slot][0][lane]), p);
       E::copy(smem_u32(&mine[slot][1][lane]), p + c1);
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<E>) rope_rows_kernel
                 : kind == 1 ? kdst
                             : vdst;
     dst += c0;
-    const int64_t out_step = (kind == 0 ? a.q.out_hs : kind == 1 ? a.k.out_hs : a.v.out_hs) * E::kSize;
+    const int out_step = int(kind == 0 ? a.q.out_hs : kind == 1 ? a.k.out_hs : a.v.out_hs) * E::kSize;
 
     // weight times cosine and sine: a' = a (wa c) - b (wb s), b' = b (wb c) + a (wa s)
     const char* wt = reinterpret_cast<const char*>(kind == 0 ? a.qw : kind == 1 ? a.kw : nullptr);
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<E>) rope_rows_kernel
       }
       const int h = gi * rows + sub;
       if (active && h <= s.last) {
-        char* p = dst + int64_t(h) * out_step;
+        char* p = dst + h * out_step;
         *reinterpret_cast<Chunk*>(p) = y0;
         *reinterpret_cast<Chunk*>(p + c1) = y1;
       }
@@ -493,9 +493,15 @@ template <typename E>
 bool in_chunks(const RopeArgs& a) {
   constexpr int P = E::kPer;
   auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % sizeof(typename E::Chunk) == 0; };
+  // offsets of heads are of 32 bits (64 took up to 3% longer: instructions count here)
+  auto near = [](int64_t heads, int64_t step) {
+    const int64_t most = ((int64_t(1) << 31) - 1) / (E::kSize * heads);
+    return -most <= step && step <= most;
+  };
   auto fits = [&](const RowSet& r) {
-    return r.heads == 0 || (aligned(r.in) && aligned(r.out) && r.in_ts % P == 0 && r.in_hs % P == 0 &&
-                            r.out_ts % P == 0 && r.out_hs % P == 0);
+    return r.heads == 0 ||
+           (near(r.heads, r.in_hs) && near(r.heads, r.out_hs) && aligned(r.in) && aligned(r.out) &&
+            r.in_ts % P == 0 && r.in_hs % P == 0 && r.out_ts % P == 0 && r.out_hs % P == 0);
   };
   return a.dim % (2 * P) == 0 && a.rot % (2 * P) == 0 && a.dim / (2 * P) <= 32 && fits(a.q) && fits(a.k) &&
          fits(a.v) && aligned(a.qw) && aligned(a.kw) && reinterpret_cast<uintptr_t>(a.cs) % 16 == 0 &&
