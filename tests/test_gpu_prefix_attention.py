@@ -140,6 +140,16 @@ def test_page_sizes_and_cache_orders(page, heads_first, batch):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("page", [8, 24, 40, 56, 72, 120, 136])
+@pytest.mark.parametrize("hq,hk,dim", [(8, 2, 128), (3, 3, 64), (10, 2, 80)])
+@pytest.mark.parametrize("prefix,counts,lens", [
+    (1000, [1] * 40, [1 + 7 * b for b in range(40)]), (2641, [90, 160, 7], [90, 500, 333]), (119, [300], [480]),
+    (0, [250, 130], [250, 401]), (6000, [70] * 3, [71, 120, 121])])
+def test_pages_of_odd_multiples_of_eight(page, hq, hk, dim, prefix, counts, lens):
+    c = Call(hq, hk, dim, prefix, lens, counts, page=page, seed=page + prefix)
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("page", [12, 32])
 @pytest.mark.parametrize("batch", [2, 70])
 def test_keys_and_values_laid_out_apart(page, batch):

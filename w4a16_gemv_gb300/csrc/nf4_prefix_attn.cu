@@ -28,7 +28,7 @@ namespace {
 __device__ unsigned int g_prefix_flags = 0;
 
 constexpr int kSms = 152;
-constexpr int kUnit = 64;    // granularity of the plan's ranges of keys
+constexpr int kUnit = 64;    // granularity of the ranges of keys of the few-row kernel
 constexpr int kStages = 2;
 
 // R rows per tile, W warps. R = 64: a warp has 16 rows and all keys of a stage
@@ -672,8 +672,8 @@ int64_t mma_range(int64_t tiles, int64_t units, int dim) {
   return units > per * kMaxRanges ? (units + kMaxRanges - 1) / kMaxRanges : per;
 }
 
-// Keys per range of the tcgen05 kernel (one CTA per SM), in units of 64 but
-// whole tiles of 128: the number of ranges that ends soonest, counting a wave
+// Keys per range of the tcgen05 kernel (one CTA per SM), in half tiles but
+// whole tiles of them: the number of ranges that ends soonest, counting a wave
 // of CTAs as its key tiles plus about three for its start and end, and the
 // partial results of a range (written and read in binary32, about 8 TB/s) in
 // the same unit of about a microsecond. Candidates: what fills one to six
@@ -766,11 +766,14 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
   p->suffix_tiles = int(whole < rows ? whole : rows);
   // as many as there are when the tokens are spread evenly (the ranges are made for these)
   const int64_t likely = a.batch > 0 ? a.batch * ((rows / a.batch + p->suffix_rows - 1) / p->suffix_rows) : 0;
-  const int64_t pk = (int64_t(p->prefix_len) + kUnit - 1) / kUnit, sk = (int64_t(p->suffix_max) + kUnit - 1) / kUnit;
+  // units of both, of which the tcgen05 kernel's ranges have an even number: whole tiles
+  const int64_t half = prefix_tile_keys(a.page_size) / 2;
+  const int64_t pu = p->prefix_rows == 256 ? half : kUnit, su = p->suffix_rows == 256 ? half : kUnit;
+  const int64_t pk = (int64_t(p->prefix_len) + pu - 1) / pu, sk = (int64_t(p->suffix_max) + su - 1) / su;
   if (sk > 0) {
     const int64_t per = p->suffix_rows == 256 ? tc_range(likely * p->k_heads, (sk + 1) / 2, rows * p->k_heads, kSms)
                                               : mma_range(likely * p->k_heads, sk, p->dim);
-    p->suffix_chunk = int(per * kUnit);
+    p->suffix_chunk = int(per * su);
     p->suffix_splits = int((sk + per - 1) / per);
   }
   if (pk > 0) {
@@ -795,7 +798,7 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
         if (keep > 0) per = tc_range(tiles, longest, rows * p->k_heads, kSms - keep);
       }
     }
-    p->prefix_chunk = int(per * kUnit);
+    p->prefix_chunk = int(per * pu);
     p->prefix_splits = int((pk + per - 1) / per);
   }
   // A long stream of shared keys that one tile of rows reads leaves L2 first, and

@@ -46,6 +46,17 @@ struct PrefixArgs {
   float2* ml;                                      // [tokens * q_heads][splits]: (maximum, sum)
 };
 
+// Keys of a tile of the tcgen05 kernel: 128, or the whole pages that nearly fill
+// that (120 for pages of 24, 40 or 120, 112 for 56), whose largest power of two,
+// eight, would make a tile of 16 or 32 copies (about 100 cycles each: 6 sequences
+// of 160 tokens x 32 heads over 4188 keys in pages of 24 took 115 us, now 80; in
+// pages of 32 71).
+inline int prefix_tile_keys(int64_t page_size) {
+  if (page_size % 16 != 8 || page_size > 128) return 128;
+  const int keys = int(128 / page_size * page_size);
+  return page_size > 8 && keys >= 112 ? keys : 128;
+}
+
 // The sizes and the plan of a call, and the bytes of its workspace.
 void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, size_t* bytes);
 

@@ -188,7 +188,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // their strides).
 struct CacheMaps {
   CUtensorMap k, v;
-  int box_rows;
+  int box_rows, tile_keys;
   int k_slot, k_head, v_slot, v_head;
 };
 
@@ -247,6 +247,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* const tail = qfull + 2;                                     // the last tile of V landed, to be cleaned
   uint32_t* const s_taddr = reinterpret_cast<uint32_t*>(tail + 1);
 
+  // Keys of a tile; the rows of a ring tile past them stay zero.
+  const int step = kTma ? maps.tile_keys : kTileKeys;
+  if (kTma && step < kTileKeys) {
+    const int past = (kTileKeys - step) * 8;  // 16 bytes each
+    for (int block = 0; block < L::kStages * L::kBlocks; ++block)
+      for (int e = tid; e < past; e += kTcThreads)
+        *reinterpret_cast<uint4*>(smem + L::kRing + block * L::kBlock + step * 128 + e * 16) =
+            make_uint4(0u, 0u, 0u, 0u);
+    fence_async_smem();
+  }
   if (tid == 0) {
     for (int i = 0; i < kGo; ++i) mbar_init(&go[i], 4 + 2 * kLoaders);
     for (int i = 0; i < L::kStages; ++i) mbar_init(&empty[i], 1);
@@ -277,8 +287,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (unsigned(a.first) + blockIdx.x >= unsigned(a.prefix_tiles) * unsigned(a.k_heads) * unsigned(a.prefix_splits))
     begin();
   const PrefixItem it = prefix_item(a, unsigned(a.first) + blockIdx.x, &g_prefix_tc_flags);
-  const int n = (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys;  // key tiles
-  const bool works = it.rows > 0 && n > 0;                    // the same in the whole CTA
+  const int n = (it.k1 - it.k0 + step - 1) / step;  // key tiles
+  const bool works = it.rows > 0 && n > 0;          // the same in the whole CTA
   const int tiles = it.rows > kTileRows ? 2 : 1;
   if (!works) {
     if (a.fused) {
@@ -345,7 +355,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int r = tile * kTileRows + (warp & 3) * 32 + lane;
       const int limit = r < it.rows ? min(visible_keys(it, (it.r0 + r) / a.group), it.k1) - it.k0 : 0;
       // key tiles below this one need no mask in this warp
-      int free_tiles = limit / kTileKeys;
+      int free_tiles = limit / step;
       if (r >= it.rows) free_tiles = n;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) free_tiles = min(free_tiles, __shfl_xor_sync(0xffffffffu, free_tiles, d));
@@ -364,7 +374,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (i >= free_tiles) {
 #pragma unroll
           for (int j = 0; j < 128; ++j)
-            if (i * kTileKeys + j >= limit) s[j] = -INFINITY;
+            if (i * step + j >= limit) s[j] = -INFINITY;
+        }
+        if (kTma && step < kTileKeys) {
+#pragma unroll
+          for (int j = 112; j < 128; ++j)
+            if (j >= step) s[j] = -INFINITY;
         }
         float mx[4];
 #pragma unroll
@@ -558,10 +573,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (kTma && warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int rows = maps.box_rows;
-    const int valid = it.k1 - it.k0 - (n - 1) * kTileKeys;  // keys of the last tile
+    const int valid = it.k1 - it.k0 - (n - 1) * step;  // keys of the last tile
     const bool clean = valid % rows != 0;                   // its last box reaches past them
     if (warp == 8) {
-      const int per_tile = (kTileKeys / rows) * L::kBlocks;  // boxes of a tile: up to 32
+      const int per_tile = (step / rows) * L::kBlocks;  // boxes of a tile: up to 32
       const int box = lane / L::kBlocks, block = lane % L::kBlocks;
       const bool mine = lane < per_tile;
       const bool leave_first = !it.own && a.stream;
@@ -569,7 +584,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // on a page that does not exist, the first page past the end
       int page = a.num_pages, slot0 = 0;
       auto fetch = [&](int i, int* pg, int* sl) {
-        const int j = it.k0 + i * kTileKeys + box * rows;
+        const int j = it.k0 + i * step + box * rows;
         *pg = a.num_pages;
         *sl = 0;
         if (mine && j < it.k1) {
@@ -581,7 +596,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       fetch(0, &page, &slot0);
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
-        const bool used = mine && it.k0 + i * kTileKeys + box * rows < it.k1;
+        const bool used = mine && it.k0 + i * step + box * rows < it.k1;
         if (used && unsigned(page) >= unsigned(a.num_pages)) {
           atomicOr(&g_prefix_tc_flags, kFlagBadIndex);
           page = a.num_pages;
@@ -594,7 +609,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (u >= L::kStages) wait(&empty[slot], uint32_t(u / L::kStages - 1) & 1u);
           uint64_t* const bar = kv == 0 ? (i == 0 ? kfirst : &go[(i - 1) % kGo])
                                 : clean && i + 1 == n ? tail : &go[i % kGo];
-          if (lane == 0) mbar_arrive_expect_tx(bar, L::kTile);
+          if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(step * L::kBlocks) * 128u);
           __syncwarp();
           const uint32_t dst = sbase + L::kRing + uint32_t(slot) * L::kTile + uint32_t(block) * L::kBlock +
                                uint32_t(box * rows) * 128u;
@@ -832,6 +847,9 @@ cudaError_t launch_prefix_tc(const PrefixArgs& p, nf4_dtype dtype, unsigned item
   // starts at a multiple of it stays in one page), 8 to 128.
   maps.box_rows = p.page_size & -p.page_size;
   if (maps.box_rows > kTileKeys) maps.box_rows = kTileKeys;
+  // Or whole pages, where a tile is made of these.
+  maps.tile_keys = prefix_tile_keys(p.page_size);
+  if (maps.tile_keys < kTileKeys) maps.box_rows = p.page_size;
   if (maps.box_rows >= 8 && p.num_pages > 0 &&
       encode_cache(p, dtype, p.k, p.k_ps, p.k_ss, p.k_hs, maps.box_rows, &maps.k, &maps.k_slot,
                    &maps.k_head) &&
