@@ -35,9 +35,9 @@
 // with one range of each joins the shared keys' part of its rows on the way out.
 // Tensor memory: S (and P) of the tiles in columns 0 and 128, O in 256 and 384.
 // Measured: 4864 tokens x 8 query heads over 16384 keys of 2 heads x 128 in
-// bf16 take 193 us (1690 TFLOP/s, 89% of measured bf16 peak; head_dim 64: 172 us,
-// 950); 12 heads of one to sixteen tokens stream 2^20 keys at 6.3 TB/s; a call
-// over 8192 keys takes 9 us of start, two key tiles and partial results.
+// bf16 take 195 us (1670 TFLOP/s, 88% of measured bf16 peak; head_dim 64: 170 us,
+// 960); 12 heads of sixteen tokens stream 2^20 keys at 6.7 TB/s; a call over 8192
+// keys takes 8.5 us of start, two key tiles and partial results.
 // Waits are bounded; one that runs out sets bit 0 of the device error flags.
 #include <cuda.h>
 #include <cudaTypedefs.h>
