@@ -184,7 +184,10 @@ NF4_API size_t nf4_prefix_attention_workspace_size(const nf4_prefix_attention_ar
  * partial results of key ranges are joined in a fixed order, so that the
  * outputs of two identical calls are identical. Scores, the running maximum
  * and sum, and all partial outputs are binary32; the weights exp(s_j - m) are
- * rounded to dtype for the product with v; the result is rounded once.
+ * rounded to dtype for the product with v (in fp16 times 2^7, so that those
+ * down to 2^-31 of the largest count); ranges are of at most 2^17 keys, so that
+ * binary32 sums lose at most 2^-8 of them to keys of no weight to speak of; the
+ * result is rounded once.
  * A NaN or infinity in k or v reaches every row that sees it; one in v of an
  * own key may also reach rows of the same sequence that stand before it.
  * cu_q, lengths and pages are read on the device, so a recorded graph can be

@@ -284,7 +284,7 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
           o[d][3] *= fb;
         }
       }
-      const float ba = ma == -INFINITY ? 0.0f : ma, bb = mb == -INFINITY ? 0.0f : mb;
+      const float ba = ma == -INFINITY ? 0.0f : ma - kLift<H>, bb = mb == -INFINITY ? 0.0f : mb - kLift<H>;
       uint32_t pf[NB][2];
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
@@ -315,6 +315,8 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
       copy_next(i);
     }
   }
+  ma -= kLift<H>;  // from here what l and o are relative to
+  mb -= kLift<H>;
 #pragma unroll
   for (int d = 1; d < 4; d <<= 1) {
     la += __shfl_xor_sync(0xffffffffu, la, d);
@@ -770,9 +772,16 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
   const int64_t half = prefix_tile_keys(a.page_size) / 2;
   const int64_t pu = p->prefix_rows == 256 ? half : kUnit, su = p->suffix_rows == 256 ? half : kUnit;
   const int64_t pk = (int64_t(p->prefix_len) + pu - 1) / pu, sk = (int64_t(p->suffix_max) + su - 1) / su;
+  // (whole tiles: units are 56, 60 or 64 keys)
+  auto bounded = [&](int64_t per, int64_t unit) {
+    const int64_t most = kMostKeys / (2 * unit) * 2;
+    return per < most ? per : most;
+  };
   if (sk > 0) {
-    const int64_t per = p->suffix_rows == 256 ? tc_range(likely * p->k_heads, (sk + 1) / 2, rows * p->k_heads, kSms)
-                                              : mma_range(likely * p->k_heads, sk, p->dim);
+    const int64_t per =
+        bounded(p->suffix_rows == 256 ? tc_range(likely * p->k_heads, (sk + 1) / 2, rows * p->k_heads, kSms)
+                                      : mma_range(likely * p->k_heads, sk, p->dim),
+                su);
     p->suffix_chunk = int(per * su);
     p->suffix_splits = int((sk + per - 1) / per);
   }
@@ -780,10 +789,10 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
     const int64_t tiles = int64_t(p->prefix_tiles) * p->k_heads;
     int64_t per;
     if (p->prefix_rows != 256) {
-      per = mma_range(tiles, pk, p->dim);
+      per = mma_range(tiles, pk, p->dim);  // (at most 1024 keys)
     } else {
       const int64_t longest = (pk + 1) / 2;
-      per = tc_range(tiles, longest, rows * p->k_heads, kSms);
+      per = bounded(tc_range(tiles, longest, rows * p->k_heads, kSms), pu);
       // One range of each and many rows: the items of own keys join the shared
       // part themselves, in place of a launch that reads both parts again (8 prompts
       // of 257 to 512 tokens over 8190 + 700 keys 131 -> 125 us, 4 of 300 over 1000 +
@@ -796,6 +805,7 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
         per = beside_range(a, *p, tiles, longest, rows, per);
         const int keep = sms_for_own(*p, likely * p->k_heads * p->suffix_splits, tiles, per, pk);
         if (keep > 0) per = tc_range(tiles, longest, rows * p->k_heads, kSms - keep);
+        per = bounded(per, pu);
       }
     }
     p->prefix_chunk = int(per * pu);

@@ -193,6 +193,19 @@ __device__ __forceinline__ float ex2(float x) {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrowth = 8.0f;  // log2 of the growth of a row's maximum that is let pass
 
+// Weights are 2^(s - m + kLift<H>), s and m (the maximum) times log2 e. In
+// binary16 a weight rounds to a multiple of 2^-24, so that without a lift all
+// below 2^-25 would be lost to the product with v while the sum counts them.
+// Lifted by 7 bits, a weight stays below 2^(7 + kGrowth) = 2^15.
+template <typename H>
+constexpr float kLift = H::kDtype == NF4_FP16 ? 7.0f : 0.0f;
+
+// Keys of a range. Its sums are binary32, and one that holds a large weight loses
+// what is added below 2^-25 of it (the tensor cores align every product with the
+// accumulator and cut it off there): up to 2^17 x 2^-25 = 2^-8 of the range, one
+// rounding of bf16, and with the lift 2^17 x 2^-32 more in binary16.
+constexpr int64_t kMostKeys = int64_t(1) << 17;
+
 // Where a finished row goes: the partial results, or the output itself.
 struct RowOut {
   int64_t row;

@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tmem_st32(o_col + 32u * c, w);
           }
         }
-        const float base = m == -INFINITY ? 0.0f : m;
+        const float base = m == -INFINITY ? 0.0f : m - kLift<H>;
         const float2 nb2 = make_float2(-base, -base);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -429,6 +429,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(tile == 0 ? &go[i % kGo] : psecond);
       }
+      m -= kLift<H>;  // from here what l and O are relative to
       const bool mine = r < it.rows;
       const RowOut ro = row_out(a, it, it.r0 + (mine ? r : 0));
       // 128 bytes of every row at a time go through this warp's part of the Q
