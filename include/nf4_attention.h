@@ -164,7 +164,8 @@ typedef struct nf4_prefix_attention_args {
                                  h / (q_heads / k_heads); tokens * q_heads at most 2^30 */
   int64_t head_dim;           /* a multiple of 8, 8 .. 128 */
   int64_t dtype;              /* NF4_BF16 or NF4_FP16: q, out and the cache */
-  double scale;               /* of the scores, usually 1 / sqrt(head_dim); > 0 */
+  double scale;               /* of the scores, usually 1 / sqrt(head_dim); > 0, and scale * log2(e) a normal binary32
+                                 number (about 8.2e-39 .. 2.3e38) */
 } nf4_prefix_attention_args;
 
 /* Bytes of device workspace that nf4_prefix_attention needs for these

@@ -47,3 +47,14 @@ def test_ranges_are_bounded(lib, kw, rows):
     kw.update(k_heads=1, head_dim=8, page_size=1 << 16)
     for dtype in (BF16, FP16):
         assert lib.nf4_prefix_attention_workspace_size(args(dtype=dtype, **kw)) == rows * 4 * (8 * 4 + 8)
+
+
+def test_scales_that_binary32_does_not_hold(lib):
+    """The kernels work with scale * log2(e) in binary32, where it must neither vanish nor overflow."""
+    log2e = 1.4426950408889634
+    least, most = 2.0 ** -126 / log2e, (2.0 - 2.0 ** -23) * 2.0 ** 127 / log2e
+    for scale in (5e-324, 1e-60, 1e-46, least * 0.999, most * 1.001, 1e300):
+        assert lib.nf4_prefix_attention(args(scale=scale), A, 1 << 30, None) == ERR_SIZE, scale
+        assert lib.nf4_prefix_attention_workspace_size(args(scale=scale)) == 0, scale
+    for scale in (least * 1.001, 0.1, most * 0.999):
+        assert lib.nf4_prefix_attention_workspace_size(args(scale=scale)) > 0, scale

@@ -1,5 +1,6 @@
 // nf4_attn_api.cu -- the C ABI of include/nf4_attention.h: host-side argument
 // checks, then the launches on the caller's stream.
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -58,7 +59,9 @@ nf4_status check_attention_sizes(const nf4_prefix_attention_args& a) {
       !strides_ok(a.k_page_stride, a.k_slot_stride, a.k_head_stride) ||
       !strides_ok(a.v_page_stride, a.v_slot_stride, a.v_head_stride))
     return NF4_ERR_INVALID_SIZE;
-  if (!(a.scale > 0.0) || !isfinite(a.scale)) return NF4_ERR_INVALID_SIZE;
+  // the kernels use it times log2 e in binary32: 0 there would make a masked score (-inf) NaN
+  const double scale_log2 = a.scale * 1.4426950408889634;
+  if (!(scale_log2 >= double(FLT_MIN) && scale_log2 <= double(FLT_MAX))) return NF4_ERR_INVALID_SIZE;
   if (a.dtype != NF4_BF16 && a.dtype != NF4_FP16) return NF4_ERR_UNSUPPORTED_DTYPE;
   return NF4_OK;
 }
