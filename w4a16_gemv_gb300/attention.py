@@ -42,13 +42,15 @@ _lib.nf4_rope_table.argtypes = [ctypes.POINTER(_RopeTableArgs), ctypes.c_void_p]
 _lib.nf4_rope_table.restype = ctypes.c_int
 
 _SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "ramp": 3}
+_HIGH = {"ramp": 32.0}  # default of `high` (4 for the others), as published
 
 
 def nf4_rope_table(positions: int, rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
-                   low: float = 1.0, high: float = 4.0, original_positions: float = 8192.0, magnitude: float = 1.0,
+                   low: float = 1.0, high: float | None = None, original_positions: float = 8192.0, magnitude: float = 1.0,
                    out: torch.Tensor | None = None, device=None, stream=None) -> torch.Tensor:
     """(cos, sin) of every position's angles, float32 [positions, rot_dim / 2, 2]; ``scaling`` is plain, linear,
-    bands (by wavelength) or ramp (by index), with the parameters of nf4_rope_scaling."""
+    bands (by wavelength) or ramp (by index), with the parameters of nf4_rope_scaling. ``high`` defaults to 4 for
+    bands and to 32 for ramp."""
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
     shape = (max(positions, 0), max(rot_dim, 0) // 2, 2)
@@ -58,7 +60,7 @@ def nf4_rope_table(positions: int, rot_dim: int, base: float = 10000.0, scaling:
         raise TypeError(f"out must be torch.float32, got {out.dtype}")
     if not out.is_cuda or out.shape != shape or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous CUDA tensor of shape {shape}")
-    args = _RopeTableArgs(out.data_ptr(), positions, rot_dim, _SCALINGS[scaling], base, factor, low, high,
-                          original_positions, magnitude)
+    args = _RopeTableArgs(out.data_ptr(), positions, rot_dim, _SCALINGS[scaling], base, factor, low,
+                          _HIGH.get(scaling, 4.0) if high is None else high, original_positions, magnitude)
     _check(_lib.nf4_rope_table(ctypes.byref(args), _stream(stream)), "nf4_rope_table")
     return out
