@@ -25,20 +25,46 @@ class Table:
     def data_ptr(self):
         return 0x100000
 
+    def numel(self):
+        return self.shape.numel()
+
+    def record_stream(self, stream):
+        self.kept_for = stream
+
+
+class Stream:
+    def __init__(self, handle, device=None):
+        self.cuda_stream, self.device = handle, device
+
 
 @pytest.fixture
 def calls(attention, monkeypatch):
-    """nf4_rope_table's argument structures, instead of the call."""
-    seen = []
+    """nf4_rope_table's argument structures, the stream and the current device, instead of the call, on a machine
+    of two GPUs of which device 0 is current and whose current streams are 100 and 101."""
+    seen, current = [], [0]
 
     class Lib:
         @staticmethod
         def nf4_rope_table(args, stream):
             a = args._obj
-            seen.append({f: getattr(a, f) for f, _ in a._fields_})
+            seen.append({**{f: getattr(a, f) for f, _ in a._fields_}, "stream": stream, "device": current[-1]})
             return 0
 
+    class Device:
+        def __init__(self, device):
+            self.index = torch.device(device).index
+
+        def __enter__(self):
+            current.append(self.index)
+
+        def __exit__(self, *_):
+            current.pop()
+
     monkeypatch.setattr(attention, "_lib", Lib)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(100 + current[-1]))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: Stream(0, device))
     return seen
 
 
@@ -49,3 +75,17 @@ def test_rope_table_defaults(attention, calls, scaling, high):
     attention.nf4_rope_table(64, 32, scaling=scaling, factor=4.0, out=out, stream=7)
     attention.nf4_rope_table(64, 32, scaling=scaling, factor=4.0, high=9.0, out=out, stream=7)
     assert [(c["low"], c["high"]) for c in calls] == [(1.0, high), (1.0, 9.0)]
+
+
+def test_rope_table_goes_to_the_device_of_its_output(attention, calls, monkeypatch):
+    out = Table((64, 16, 2), "cuda:1")
+    assert attention.nf4_rope_table(64, 32, out=out) is out
+    attention.nf4_rope_table(64, 32, out=out, stream=7)
+    assert [(c["stream"], c["device"]) for c in calls] == [(101, 1), (7, 1)]
+    assert not hasattr(out, "kept_for")  # a given output is the caller's to keep
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype, device: Table(shape, device))
+    made = attention.nf4_rope_table(64, 32, device="cuda:1", stream=7)
+    assert (calls[-1]["stream"], calls[-1]["device"]) == (7, 1)
+    assert (made.kept_for.cuda_stream, made.kept_for.device) == (7, torch.device("cuda:1"))
+    assert attention.nf4_rope_table(64, 32, device="cuda:1", stream=0).kept_for.cuda_stream == 0
+    assert not hasattr(attention.nf4_rope_table(64, 32, device="cuda:1"), "kept_for")

@@ -54,7 +54,8 @@ def nf4_rope_table(positions: int, rot_dim: int, base: float = 10000.0, scaling:
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
     shape = (max(positions, 0), max(rot_dim, 0) // 2, 2)
-    if out is None:
+    fresh = out is None
+    if fresh:
         out = torch.empty(shape, dtype=torch.float32, device=device or "cuda")
     if out.dtype != torch.float32:
         raise TypeError(f"out must be torch.float32, got {out.dtype}")
@@ -62,5 +63,10 @@ def nf4_rope_table(positions: int, rot_dim: int, base: float = 10000.0, scaling:
         raise ValueError(f"out must be a contiguous CUDA tensor of shape {shape}")
     args = _RopeTableArgs(out.data_ptr(), positions, rot_dim, _SCALINGS[scaling], base, factor, low,
                           _HIGH.get(scaling, 4.0) if high is None else high, original_positions, magnitude)
-    _check(_lib.nf4_rope_table(ctypes.byref(args), _stream(stream)), "nf4_rope_table")
+    with torch.cuda.device(out.device):  # its stream is the default, and the launch goes to the current device
+        handle = _stream(stream)
+        if fresh and stream is not None and out.numel() > 0:  # kept from reuse until that stream is done with it
+            out.record_stream(torch.cuda.ExternalStream(handle, device=out.device) if handle
+                              else torch.cuda.default_stream(out.device))
+        _check(_lib.nf4_rope_table(ctypes.byref(args), handle), "nf4_rope_table")
     return out
