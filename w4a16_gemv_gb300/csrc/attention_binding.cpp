@@ -420,6 +420,7 @@ PyObject* py_prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t nargs
     if (given(v[12])) {
       ws = tensor(v[12], "workspace");
       if (!ws.is_cuda() || !ws.is_contiguous()) throw ValueError("workspace must be a contiguous CUDA tensor");
+      if (ws.get_device() != dev) throw ValueError("workspace must be on the same device as the others");
       scratch = ws.data_ptr();
       bytes = ws.nbytes();
     } else if ((bytes = nf4_prefix_attention_workspace_size(&a)) > 0) {
