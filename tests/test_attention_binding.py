@@ -1,4 +1,9 @@
 """The Python side of the attention binding without a GPU: what reaches the C calls."""
+import os
+import shutil
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -89,3 +94,40 @@ def test_rope_table_goes_to_the_device_of_its_output(attention, calls, monkeypat
     assert (made.kept_for.cuda_stream, made.kept_for.device) == (7, torch.device("cuda:1"))
     assert attention.nf4_rope_table(64, 32, device="cuda:1", stream=0).kept_for.cuda_stream == 0
     assert not hasattr(attention.nf4_rope_table(64, 32, device="cuda:1"), "kept_for")
+
+
+def test_the_rest_of_the_package_without_the_compiled_half(attention, tmp_path):
+    """Without _attention.so, or with one that does not load, the other entry points are as they were, and the calls of
+    the attention side say what is missing."""
+    package = os.path.dirname(attention.__file__)
+    copy = tmp_path / os.path.basename(package)
+    shutil.copytree(package, copy, ignore=shutil.ignore_patterns("_build", "csrc", "__pycache__", "_attention.so"))
+    code = """if True:
+        from w4a16_gemv_gb300 import *
+        import w4a16_gemv_gb300 as nf4
+        assert nf4.__file__.startswith({here!r}), nf4.__file__
+        assert nf4_version() > 0 and nf4_status_string(0) and nf4.DecodeStep and nf4_gemv and nf4_dequant
+        for call in (nf4_rope_table, nf4_qk_norm_rope, nf4_kv_append, nf4_prefix_attention,
+                     nf4_prefix_attention_workspace_size):
+            try:
+                call(1, 2)
+            except ImportError as e:
+                assert call.__name__ in str(e) and "_attention" in str(e), e
+            else:
+                raise AssertionError(call)
+        """.format(here=str(tmp_path))
+    for content in (None, b"not a shared object"):
+        if content is not None:
+            (copy / "_attention.so").write_bytes(content)
+        p = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
+        assert p.returncode == 0, p.stderr
+
+
+def test_another_torch_or_interpreter_asks_for_a_build(monkeypatch):
+    import __graft_entry__
+    b = __graft_entry__._build_module()
+    b.build()
+    assert not b._stale()
+    key = b._binding_key()
+    monkeypatch.setattr(b, "_binding_key", lambda: key + "1")
+    assert b._stale()

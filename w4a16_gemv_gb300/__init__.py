@@ -4,7 +4,8 @@ Argument marshalling only: tensors are checked for device, dtype, size and
 contiguity, then their device pointers and the current CUDA stream go to the C
 ABI declared in ``include/nf4.h``. Every step of the computation runs in the
 library's CUDA kernels; there is no fallback. Importing this package fails
-loudly if ``libnf4.so`` has not been built (``__graft_entry__.build()``).
+loudly if ``libnf4.so`` has not been built (``__graft_entry__.build()``); the
+calls of the attention side do so where its compiled half has not.
 """
 from __future__ import annotations
 
@@ -343,5 +344,18 @@ def gemv(wt: NF4Weight, x: torch.Tensor, y=None, stream=None, bias=None, out_dty
                        s2_blocksize=wt.s2_blocksize, stream=stream)
 
 
-from .attention import (nf4_kv_append, nf4_prefix_attention,  # noqa: E402
-                        nf4_prefix_attention_workspace_size, nf4_qk_norm_rope, nf4_rope_table)
+# The attention side's compiled half is built against one torch and needs its headers; where it is missing or does not
+# load, the calls above work all the same and those of the attention side say what is missing.
+try:
+    from .attention import (nf4_kv_append, nf4_prefix_attention,  # noqa: E402
+                            nf4_prefix_attention_workspace_size, nf4_qk_norm_rope, nf4_rope_table)
+except ImportError as _error:
+    def _without(name, error=_error):
+        def call(*args, **kwargs):
+            raise ImportError(f"{name}: the attention side of the binding is not available: {error}") from error
+        call.__name__ = call.__qualname__ = name
+        return call
+
+    for _name in ("nf4_rope_table", "nf4_qk_norm_rope", "nf4_kv_append", "nf4_prefix_attention",
+                  "nf4_prefix_attention_workspace_size"):
+        globals()[_name] = _without(_name)

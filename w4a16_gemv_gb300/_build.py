@@ -14,6 +14,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnf4.so")
 BINDING = os.path.join(PKG, "_attention.so")
+BINDING_KEY = os.path.join(OBJDIR, "binding.txt")
 SOURCES = ("nf4_api.cu", "nf4_dequant.cu", "nf4_gemv.cu", "nf4_gemv_b1.cu", "nf4_gemv_stream.cu",
            "nf4_quantize.cu", "nf4_step.cu", "nf4_gemm_tc.cu", "nf4_attn_api.cu", "nf4_rope.cu",
            "nf4_prefix_attn.cu", "nf4_prefix_attn_tc.cu")
@@ -34,8 +35,26 @@ def nvcc_flags(extra: tuple[str, ...] = ()) -> list[str]:
             "-I", INCLUDE, "-I", CSRC, *extra]
 
 
+def _binding_key() -> str:
+    """What the Python entry points are built against: the interpreter and torch."""
+    from importlib import metadata
+    try:
+        torch = metadata.version("torch")
+    except metadata.PackageNotFoundError:
+        torch = "none"
+    return f"{sys.version} torch {torch}"
+
+
+def _built_against() -> str | None:
+    try:
+        with open(BINDING_KEY) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING) or _built_against() != _binding_key():
         return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     deps = ([os.path.join(CSRC, f) for f in os.listdir(CSRC)] +
@@ -96,6 +115,8 @@ def build(force: bool = False, verbose: bool = False, extra: tuple[str, ...] = (
     if p.returncode != 0:
         raise RuntimeError(f"g++ failed:\n{p.stdout.decode(errors='replace')}")
     os.replace(tmp, BINDING)
+    with open(BINDING_KEY, "w") as f:
+        f.write(_binding_key())
     return LIB
 
 
