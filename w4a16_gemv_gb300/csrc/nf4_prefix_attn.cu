@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(Shape<R, W>::kThreads, R == 64 ? 2 : (DP == 64
   pdl_allow_dependents();
   const PrefixItem it = prefix_item(a, unsigned(a.first) + blockIdx.x, &g_prefix_flags);
   if (it.rows > 0) attend<H, DP, R, W>(a, it, smem);
-  if (a.fused) unheld_rows<H>(a, W);
+  if (a.fused) unheld_rows<H>(a, W, &g_prefix_flags);
   if (a.beside && blockIdx.x + 1 == gridDim.x) pdl_wait_prior_grid();
 }
 
@@ -433,8 +433,7 @@ __global__ void __launch_bounds__(Shape<R, W>::kThreads, R == 64 ? 2 : (DP == 64
 // the sums depends on the plan alone.
 constexpr int kJoinWarps = 8;
 template <typename H, int kBatch>
-__global__ void __launch_bounds__(32 * kJoinWarps)
-    prefix_join_kernel(const __grid_constant__ PrefixArgs a, int per_row) {
+__device__ __forceinline__ void join_rows(const PrefixArgs& a, int per_row) {
   static_assert(kBatch <= 32, "a lane per range of a round");
   __shared__ float4 sv[kJoinWarps][32];
   __shared__ float sl[kJoinWarps];
@@ -526,7 +525,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 // in flight together (37900 rows of two ranges: the call 137 -> 130 us).
 constexpr int kFewRows = 4;
 template <typename H, int kRanges>
-__global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_few_kernel(const __grid_constant__ PrefixArgs a) {
+__device__ __forceinline__ void join_rows_few(const PrefixArgs& a) {
   pdl_allow_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t rows = int64_t(a.tokens) * a.q_heads;
@@ -584,6 +583,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_few_kernel(const 
   }
 }
 
+// The joins, and the check of cu_q that the items leave over.
+template <typename H, int kBatch, bool kCheck>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    prefix_join_kernel(const __grid_constant__ PrefixArgs a, int per_row) {
+  join_rows<H, kBatch>(a, per_row);
+  if (kCheck) check_cu_q(a, kJoinWarps, &g_prefix_flags);
+}
+template <typename H, int kRanges, bool kCheck>
+__global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_few_kernel(const __grid_constant__ PrefixArgs a) {
+  join_rows_few<H, kRanges>(a);
+  if (kCheck) check_cu_q(a, kJoinWarps, &g_prefix_flags);
+}
+
 // A call without a single key.
 template <typename H>
 __global__ void __launch_bounds__(128) prefix_empty_kernel(const __grid_constant__ PrefixArgs a) {
@@ -612,6 +624,22 @@ template <typename H, int DP>
 cudaError_t launch_rows(const PrefixArgs& p, int rows, unsigned items, cudaStream_t stream) {
   if (rows == 64) return launch_mma<H, DP, 64, 4>(p, items, stream);
   return items <= kFewItems ? launch_mma<H, DP, 16, 4>(p, items, stream) : launch_mma<H, DP, 16, 2>(p, items, stream);
+}
+
+template <typename H, bool kCheck>
+cudaError_t launch_join(const PrefixArgs& p, cudaStream_t stream) {
+  const int64_t rows = int64_t(p.tokens) * p.q_heads;
+  const int64_t few = int64_t(kJoinWarps) * kFewRows;
+  if (p.splits <= 4 && rows >= few * kSms)
+    return launch_k(p.splits <= 2 ? prefix_join_few_kernel<H, 2, kCheck> : prefix_join_few_kernel<H, 4, kCheck>,
+                    dim3(unsigned((rows + few - 1) / few)), dim3(32 * kJoinWarps), 0, stream, p);
+  int per_row = 1;
+  while (per_row < kJoinWarps && per_row * 8 < p.splits) per_row *= 2;
+  const int64_t blocks = (rows * per_row + kJoinWarps - 1) / kJoinWarps;
+  return launch_k(p.splits <= 4    ? prefix_join_kernel<H, 4, kCheck>
+                  : p.splits <= 64 ? prefix_join_kernel<H, 8, kCheck>
+                                   : prefix_join_kernel<H, 16, kCheck>,
+                  dim3(unsigned(blocks)), dim3(32 * kJoinWarps), 0, stream, p, per_row);
 }
 
 template <typename H>
@@ -643,17 +671,8 @@ cudaError_t launch_typed(const PrefixArgs& p, cudaStream_t stream) {
     first += items;
   }
   if (e != cudaSuccess || p.direct || p.fused) return e;
-  const int64_t few = int64_t(kJoinWarps) * kFewRows;
-  if (p.splits <= 4 && rows >= few * kSms)
-    return launch_k(p.splits <= 2 ? prefix_join_few_kernel<H, 2> : prefix_join_few_kernel<H, 4>,
-                    dim3(unsigned((rows + few - 1) / few)), dim3(32 * kJoinWarps), 0, stream, p);
-  int per_row = 1;
-  while (per_row < kJoinWarps && per_row * 8 < p.splits) per_row *= 2;
-  const int64_t blocks = (rows * per_row + kJoinWarps - 1) / kJoinWarps;
-  return launch_k(p.splits <= 4    ? prefix_join_kernel<H, 4>
-                  : p.splits <= 64 ? prefix_join_kernel<H, 8>
-                                   : prefix_join_kernel<H, 16>,
-                  dim3(unsigned(blocks)), dim3(32 * kJoinWarps), 0, stream, p, per_row);
+  const bool check = p.cu_q && p.suffix_splits > 0 && p.batch > 32;  // (its mere presence costs 0.3 us)
+  return check ? launch_join<H, true>(p, stream) : launch_join<H, false>(p, stream);
 }
 
 }  // namespace
@@ -763,9 +782,10 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
   p->prefix_rows = rows > 16 || p->prefix_len > 1024 ? 256 : 16;
   p->suffix_rows = rows > 64 * a.batch ? 256 : rows > 32 * a.batch ? 64 : 16;
   p->prefix_tiles = int((rows + p->prefix_rows - 1) / p->prefix_rows);
-  // sum over sequences of ceil(rows / suffix_rows) is below both bounds
+  // the two ways of first_tile()
   const int64_t whole = rows / p->suffix_rows + a.batch;
-  p->suffix_tiles = int(whole < rows ? whole : rows);
+  p->tile_per_row = rows <= whole;
+  p->suffix_tiles = int(p->tile_per_row ? rows : whole);
   // as many as there are when the tokens are spread evenly (the ranges are made for these)
   const int64_t likely = a.batch > 0 ? a.batch * ((rows / a.batch + p->suffix_rows - 1) / p->suffix_rows) : 0;
   // units of both, of which the tcgen05 kernel's ranges have an even number: whole tiles

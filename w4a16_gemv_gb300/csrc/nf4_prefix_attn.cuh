@@ -32,7 +32,8 @@ struct PrefixArgs {
   float scale_log2;                                // scale * log2(e)
   // plan
   int prefix_rows, suffix_rows;                    // rows per tile: 16, 64 or 256
-  int prefix_tiles, suffix_tiles;                  // tiles of a key/value head (suffix: an upper bound)
+  int prefix_tiles, suffix_tiles;                  // tiles of a key/value head (suffix: the numbers they take)
+  int tile_per_row;                                // 1: tiles of own rows are numbered by their first row
   int prefix_splits, suffix_splits;                // ranges of keys, of this many each:
   int prefix_chunk, suffix_chunk;
   int splits;                                      // prefix_splits + suffix_splits
@@ -83,12 +84,20 @@ __device__ __forceinline__ int visible_keys(const PrefixItem& it, int i) {
   return it.own ? min(max(it.len - it.n + i + 1, 0), it.len) : it.len;
 }
 
-constexpr int kMostTiles = 1 << 30;
+// Tiles of own rows are numbered so that the sequence of a tile is found without
+// counting the tiles of those before it: sequence b, with the rows [x, y) of a
+// key/value head, has the numbers from x / suffix_rows + b on (rounded down; y / suffix_rows
+// + b + 1 is the next one's first, which leaves room for its ceil((y - x) / suffix_rows)
+// tiles), or from x on where that makes fewer numbers in all. Numbers past a
+// sequence's rows are empty items. (8192 sequences x 2 heads over 200 own keys of 64:
+// 120 us; with a scan of the batch for every tile 620.)
+__device__ __forceinline__ int first_tile(const PrefixArgs& a, int t0, int b) {
+  return a.tile_per_row ? t0 * a.group : ((t0 * a.group) >> (31 - __clz(a.suffix_rows))) + b;
+}
 
 // Item `index` of a launch that covers prefix items first (a key/value head's
 // tiles of one key range side by side, so that they meet in L2), then suffix
-// items. Tiles of the suffix are numbered along the batch; every warp finds
-// its own by a scan of cu_q, 32 sequences at a time. Called by whole warps.
+// items. Called by whole warps.
 __device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, unsigned index, unsigned int* flags) {
   PrefixItem it;
   const unsigned prefix_items = unsigned(a.prefix_tiles) * unsigned(a.k_heads) * unsigned(a.prefix_splits);
@@ -119,48 +128,51 @@ __device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, unsigned 
   it.r0 = it.t0 = it.n = it.len = it.k0 = it.k1 = 0;
   it.pages = a.suffix_pages;
   const int lane = threadIdx.x & 31;
-  int before = 0;  // tiles of the sequences before this group of 32
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const int b = b0 + lane;
-    int lo = 0, hi = 0, length = 0;
-    if (b < a.batch) {
-      length = a.suffix_lens[b];  // with cu_q, not after it: one latency
-      lo = a.cu_q ? a.cu_q[b] : b;
-      hi = a.cu_q ? a.cu_q[b + 1] : b + 1;
-      const int l2 = min(max(lo, 0), a.tokens), h2 = min(max(hi, l2), a.tokens);
-      if (l2 != lo || h2 != hi) atomicOr(flags, kFlagBadIndex);
-      lo = l2;
-      hi = h2;
+  // The tile's sequence is the last whose first tile is at or before it. One
+  // token each: b group / suffix_rows + b < tile + 1, solved for b (the product is at
+  // most rows + batch * suffix_rows, below 2^31). Else a search of cu_q, 32 looks at a
+  // time; whatever stands there, it ends at a sequence of the batch.
+  int b0 = 0, span = a.batch;
+  if (!a.cu_q) {
+    const unsigned last =
+        a.tile_per_row ? unsigned(tile) / unsigned(a.group)
+                       : (unsigned(tile + 1) * unsigned(a.suffix_rows) - 1u) / unsigned(a.group + a.suffix_rows);
+    b0 = min(int(last), a.batch - 1);
+    span = 1;
+  } else {
+    while (span > 32) {
+      const int step = (span + 31) >> 5, at = lane * step;
+      const bool before = at < span && first_tile(a, min(max(a.cu_q[b0 + at], 0), a.tokens), b0 + at) <= tile;
+      const int src = 31 - __clz(int(__ballot_sync(0xffffffffu, before) | 1u));
+      b0 += src * step;
+      span = min(step, span - src * step);
     }
-    const int mine = ((hi - lo) * a.group + a.suffix_rows - 1) / a.suffix_rows;
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto = min(upto + o, kMostTiles);  // a falling cu_q must not overflow the sums
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, before + upto > tile);
-    if (past) {
-      const int src = __ffs(int(past)) - 1;
-      const int first = before + __shfl_sync(0xffffffffu, upto - mine, src);
-      const int seq = b0 + src;
-      it.t0 = __shfl_sync(0xffffffffu, lo, src);
-      it.n = __shfl_sync(0xffffffffu, hi, src) - it.t0;
-      const int64_t r0 = int64_t(tile - first) * a.suffix_rows;
-      if (r0 < 0 || r0 >= int64_t(it.n) * a.group) return it;  // (nor make a row where there is none)
-      it.r0 = int(r0);
-      it.rows = min(a.suffix_rows, it.n * a.group - it.r0);
-      const int len = __shfl_sync(0xffffffffu, length, src);
-      it.len = min(max(len, 0), a.suffix_max);
-      if (it.len != len && lane == 0) atomicOr(flags, kFlagBadIndex);
-      it.pages = a.suffix_pages + int64_t(seq) * a.suffix_pages_stride;
-      const int sees = visible_keys(it, (it.r0 + it.rows - 1) / a.group);  // the tile's last row sees most
-      it.k0 = int(min(int64_t(split) * a.suffix_chunk, int64_t(sees)));
-      it.k1 = int(min(int64_t(it.k0) + a.suffix_chunk, int64_t(sees)));
-      return it;
-    }
-    before = min(before + __shfl_sync(0xffffffffu, upto, 31), kMostTiles);
   }
+  int lo = 0, hi = 0, length = 0;
+  if (lane < span) {
+    length = a.suffix_lens[b0 + lane];  // with cu_q, not after it: one latency
+    lo = a.cu_q ? a.cu_q[b0 + lane] : b0;
+    hi = a.cu_q ? a.cu_q[b0 + lane + 1] : b0 + 1;
+    const int l2 = min(max(lo, 0), a.tokens), h2 = min(max(hi, l2), a.tokens);
+    if (l2 != lo || h2 != hi) atomicOr(flags, kFlagBadIndex);
+    lo = l2;
+    hi = h2;
+  }
+  const int mine = first_tile(a, lo, b0 + lane);
+  const int src = 31 - __clz(int(__ballot_sync(0xffffffffu, lane < span && mine <= tile) | 1u));
+  const int first = __shfl_sync(0xffffffffu, mine, src);
+  it.t0 = __shfl_sync(0xffffffffu, lo, src);
+  it.n = __shfl_sync(0xffffffffu, hi, src) - it.t0;
+  const int len = __shfl_sync(0xffffffffu, length, src);
+  if (tile < first || tile - first >= (it.n * a.group + a.suffix_rows - 1) >> (31 - __clz(a.suffix_rows))) return it;
+  it.r0 = (tile - first) * a.suffix_rows;
+  it.rows = min(a.suffix_rows, it.n * a.group - it.r0);
+  it.len = min(max(len, 0), a.suffix_max);
+  if (it.len != len && lane == 0) atomicOr(flags, kFlagBadIndex);
+  it.pages = a.suffix_pages + int64_t(b0 + src) * a.suffix_pages_stride;
+  const int sees = visible_keys(it, (it.r0 + it.rows - 1) / a.group);  // the tile's last row sees most
+  it.k0 = int(min(int64_t(split) * a.suffix_chunk, int64_t(sees)));
+  it.k1 = int(min(int64_t(it.k0) + a.suffix_chunk, int64_t(sees)));
   return it;
 }
 
@@ -260,15 +272,27 @@ __device__ __forceinline__ void shared_row(const PrefixArgs& a, int64_t row) {
   write_row<H>(out, a.lse ? a.lse + row : nullptr, col, x.x, x.y, v);
 }
 
+// Reports entries of cu_q out of range, where an item's search does not look at
+// all of them (more than 32 sequences). By the first `warps` warps of every CTA of
+// a call's last launch, at its end.
+__device__ __forceinline__ void check_cu_q(const PrefixArgs& a, int warps, unsigned int* flags) {
+  if (!a.cu_q || a.suffix_splits == 0 || a.batch <= 32) return;
+  for (int64_t b = int64_t(blockIdx.x) * warps * 32 + threadIdx.x; b < a.batch; b += int64_t(gridDim.x) * warps * 32) {
+    const int lo = a.cu_q[b], hi = a.cu_q[b + 1];
+    if (lo < 0 || hi < lo || hi > a.tokens) atomicOr(flags, kFlagBadIndex);
+  }
+}
+
 // The rows of tokens that no sequence holds, dealt out to the first `warps`
-// warps of every CTA of a launch of own items.
+// warps of every CTA of a launch of own items; and the check above.
 template <typename H>
-__device__ __forceinline__ void unheld_rows(const PrefixArgs& a, int warps) {
+__device__ __forceinline__ void unheld_rows(const PrefixArgs& a, int warps, unsigned int* flags) {
   if (!a.cu_q) return;
   const int lo = min(max(a.cu_q[0], 0), a.tokens), hi = min(max(a.cu_q[a.batch], lo), a.tokens);
   const int64_t rows = int64_t(lo + a.tokens - hi) * a.q_heads;
   for (int64_t r = int64_t(blockIdx.x) * warps + (threadIdx.x >> 5); r < rows; r += int64_t(gridDim.x) * warps)
     shared_row<H>(a, r < int64_t(lo) * a.q_heads ? r : r + int64_t(hi - lo) * a.q_heads);
+  check_cu_q(a, warps, flags);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (a.fused) {
       if (a.beside) pdl_wait_prior_grid();
       for (int r = warp; r < it.rows; r += kTcThreads / 32) shared_row<H>(a, row_out(a, it, it.r0 + r).row);
-      if (warp < 8) unheld_rows<H>(a, 8);
+      if (warp < 8) unheld_rows<H>(a, 8, &g_prefix_tc_flags);
       return;
     }
     begin();
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (a.fused) {
       if (a.beside) pdl_wait_prior_grid();
-      unheld_rows<H>(a, 8);
+      unheld_rows<H>(a, 8, &g_prefix_tc_flags);
     }
   } else if (kTma && warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
