@@ -698,15 +698,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 12) {
       begin();
-      // What follows within a call (other items, the join) uses no tensor memory
-      // and may start now; after a call's only launch anything may follow, and
-      // starts when this CTA has its allocation.
-      if (!a.direct) pdl_allow_dependents();
       asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_taddr)),
                    "r"(kTmemCols)
                    : "memory");
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-      if (a.direct) pdl_allow_dependents();
+      // Only now may what follows start: it lets its own followers start in turn, and
+      // one of these that allocates ahead of its wait (the tensor-core GEMV) must not
+      // hold what a CTA of this grid still waits for.
+      pdl_allow_dependents();
       tmem_address();
     }
     if (warp == 12 && lane == 0) {
