@@ -34,3 +34,36 @@ def test_beside_kernels_that_take_tensor_memory(dim):
     for n, out, lse, z in got:
         assert torch.equal(out, want[n][0]) and torch.equal(lse, want[n][1]) and torch.equal(z, y)
     assert nf4.nf4_device_error_flags() == 0
+
+
+@pytest.mark.parametrize("dim,rot", [(128, 128), (80, 40), (36, 18)], ids=["16 bytes", "8 bytes", "elements"])
+def test_what_the_launch_before_has_just_written(dim, rot):
+    """The table, the rows and the norm's weights of a call are the outputs of the ones right before it, in the same
+    buffers every time."""
+    nf4 = lib()
+    tokens, heads = 300, 6
+    pos = torch.randint(0, 500, (tokens,), device="cuda")
+    x = torch.randn(tokens, heads, dim, device="cuda").bfloat16()
+    one = torch.zeros(1, dtype=torch.int64, device="cuda")
+    table, q, k, kk, w = (torch.empty(s, dtype=t, device="cuda") for s, t in (
+        ((500, rot // 2, 2), torch.float32), (x.shape, x.dtype), (x.shape, x.dtype), (x.shape, x.dtype),
+        ((1, 1, dim), x.dtype)))
+
+    def step(i, wait):
+        nf4.nf4_rope_table(500, rot, base=100.0 + 50 * i, out=table)
+        wait()
+        # rotated weights, and rows rotated by the new table
+        nf4.nf4_qk_norm_rope(x[i:i + 1, :1], x[i:i + 1, 1:2], one + i, table, q_out=w, k_out=kk[:1, :1])
+        wait()
+        nf4.nf4_qk_norm_rope(x, x, pos, table, q_weight=w[0, 0], q_out=q, k_out=k)
+        wait()
+        nf4.nf4_qk_norm_rope(q, k, pos, table, k_weight=w[0, 0], q_out=q, k_out=kk)
+        wait()
+        return q.clone(), kk.clone()
+
+    want = [step(i, torch.cuda.synchronize) for i in range(20)]
+    got = [step(i, lambda: None) for _ in range(5) for i in range(20)]
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(got):
+        assert torch.equal(a, want[i % 20][0]) and torch.equal(b, want[i % 20][1])
+    assert nf4.nf4_device_error_flags() == 0

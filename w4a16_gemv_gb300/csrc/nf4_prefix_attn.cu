@@ -189,7 +189,7 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int d = s * 16 + h * 8 + (lane & 3) * 2;
-          if (there[x] && d < a.dim) qf[s][x + 2 * h] = __ldg(reinterpret_cast<const uint32_t*>(qp[x] + d * 2));
+          if (there[x] && d < a.dim) qf[s][x + 2 * h] = *reinterpret_cast<const uint32_t*>(qp[x] + d * 2);
         }
     }
   }

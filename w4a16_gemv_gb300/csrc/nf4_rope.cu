@@ -343,8 +343,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<E>) rope_rows_kernel
     if (kind < 2) {
       float wa[P], wb[P];
       if (wt) {
-        E::template up<kInterleaved>(__ldg(reinterpret_cast<const Chunk*>(wt + c0)),
-                                     __ldg(reinterpret_cast<const Chunk*>(wt + c0 + c1)), wa, wb);
+        E::template up<kInterleaved>(*reinterpret_cast<const Chunk*>(wt + c0),
+                                     *reinterpret_cast<const Chunk*>(wt + c0 + c1), wa, wb);
       } else {
 #pragma unroll
         for (int i = 0; i < P; ++i) wa[i] = wb[i] = 1.0f;
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<E>) rope_rows_kernel
 #pragma unroll
       for (int i = 0; i < P / 2; ++i) {
         float4 f = make_float4(none, 0.0f, none, 0.0f);
-        if (turned && good) f = __ldg(src + (i < P / 4 ? i : i + far));
+        if (turned && good) f = src[i < P / 4 ? i : i + far];
         const uint64_t c = pack2(f.x, f.z);
         ac[i] = mul2(pack2(wa[2 * i], wa[2 * i + 1]), c);
         bc[i] = mul2(pack2(wb[2 * i], wb[2 * i + 1]), c);
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_any_kernel(const __gri
   for (int i = lane; i < a.rot / 2; i += 32) {
     const int i0 = a.interleaved ? 2 * i : i, i1 = a.interleaved ? 2 * i + 1 : i + a.rot / 2;
     const float p = value(i0), b = value(i1);
-    const float2 f = good ? __ldg(cs + i) : make_float2(nan, nan);
+    const float2 f = good ? cs[i] : make_float2(nan, nan);
     E::store(out + i0 * E::kSize, p * f.x - b * f.y);
     E::store(out + i1 * E::kSize, b * f.x + p * f.y);
   }
