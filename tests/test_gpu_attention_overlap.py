@@ -67,3 +67,28 @@ def test_what_the_launch_before_has_just_written(dim, rot):
     for i, (a, b) in enumerate(got):
         assert torch.equal(a, want[i % 20][0]) and torch.equal(b, want[i % 20][1])
     assert nf4.nf4_device_error_flags() == 0
+
+
+@pytest.mark.parametrize("dim", [128, 24])
+def test_tokens_that_go_nowhere_beside_others(dim):
+    """Appends of nothing but padding leave the cache as it is, and disturb no call that takes their place on the SMs."""
+    nf4 = lib()
+    tokens, heads = 2000, 8
+    pos = torch.randint(0, 500, (tokens,), device="cuda")
+    table = nf4.nf4_rope_table(500, dim)
+    x = torch.randn(tokens, heads, dim, device="cuda").bfloat16()
+    cache = torch.randn(3, 16, heads, dim, device="cuda").bfloat16()
+    kept = cache.clone()
+    none = torch.full((tokens,), -1, device="cuda")
+    want = nf4.nf4_qk_norm_rope(x, x, pos, table)[0].clone()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(50):
+        for s in streams:
+            with torch.cuda.stream(s):
+                nf4.nf4_kv_append(cache, cache, none, x, x, pos, table)
+                got.append(nf4.nf4_qk_norm_rope(x, x, pos, table)[0])
+    torch.cuda.synchronize()
+    assert torch.equal(cache, kept) and all(torch.equal(g, want) for g in got)
+    assert nf4.nf4_device_error_flags() == 0

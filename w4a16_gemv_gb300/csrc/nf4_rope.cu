@@ -422,6 +422,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<E>) rope_rows_kernel
     }
     copy_wait<0>();
   }
+  copy_wait<0>();  // rows that go nowhere were asked for too: the block's shared memory is not given back under them
 }
 
 // Any head size, alignment and rotated part: one warp per row, a lane per
