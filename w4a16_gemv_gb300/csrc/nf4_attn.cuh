@@ -8,12 +8,13 @@
 namespace nf4 {
 
 // Device error flags of the attention side, one word per translation unit and
-// device, read and cleared together with the tensor-core GEMV's.
+// device (their addresses on the current one), read and cleared together with the
+// tensor-core GEMV's.
 constexpr unsigned kFlagWaitRanOut = 1u;  // a bounded wait ran out
 constexpr unsigned kFlagBadIndex = 2u;    // a position, slot, page, length or cu_q entry out of range
-cudaError_t read_and_clear_rope_flags(unsigned int* flags);
-cudaError_t read_and_clear_prefix_flags(unsigned int* flags);
-cudaError_t read_and_clear_prefix_tc_flags(unsigned int* flags);
+cudaError_t rope_flags(unsigned int** word);
+cudaError_t prefix_flags(unsigned int** word);
+cudaError_t prefix_tc_flags(unsigned int** word);
 
 nf4_status status_of(cudaError_t e);
 

@@ -675,11 +675,8 @@ cudaError_t try_gemm_tc(const QuantTensor& t, int64_t N, int64_t K, const uint16
   }
 }
 
-cudaError_t read_and_clear_tc_flags(unsigned int* flags) {
-  unsigned int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(flags, g_tc_flags, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_tc_flags, &zero, sizeof(unsigned int));
+cudaError_t tc_flags(unsigned int** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_tc_flags);
 }
 
 }  // namespace nf4

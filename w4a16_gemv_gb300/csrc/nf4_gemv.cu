@@ -23,6 +23,8 @@
 //     registers; each x chunk is reused for R rows.
 //   * For thin layers several warps split K (ks > 1) and combine through
 //     shared memory, so that small N still spreads over all SMs.
+#include <mutex>
+
 #include "nf4_attn.cuh"
 #include "nf4_internal.cuh"
 
@@ -373,18 +375,33 @@ cudaError_t dispatch_batch(const QuantTensor& t, int64_t N, int64_t K, const uin
   }
 }
 
+// The words of the device error flags, taken and cleared in one launch (read and
+// cleared one by one, four words take eight synchronous copies, 52 us).
+struct FlagWords {
+  unsigned int* word[4];
+};
+__device__ unsigned int g_collected;
+__global__ void collect_flags_kernel(FlagWords w) {
+  unsigned int all = 0;
+  for (int i = 0; i < 4; ++i) all |= atomicExch(w.word[i], 0u);
+  g_collected = all;
+}
+
 }  // namespace
 
 cudaError_t read_and_clear_device_flags(unsigned int* flags) {
   // one word per translation unit that reports something: the tensor-core
-  // GEMV (waits) and the attention side (indices read on the device)
-  unsigned int part[4] = {0u, 0u, 0u, 0u};
-  cudaError_t e = read_and_clear_tc_flags(&part[0]);
-  if (e == cudaSuccess) e = read_and_clear_rope_flags(&part[1]);
-  if (e == cudaSuccess) e = read_and_clear_prefix_flags(&part[2]);
-  if (e == cudaSuccess) e = read_and_clear_prefix_tc_flags(&part[3]);
-  if (e == cudaSuccess) *flags = part[0] | part[1] | part[2] | part[3];
-  return e;
+  // GEMV (waits) and the attention side (waits, indices read on the device)
+  FlagWords w;
+  cudaError_t e = tc_flags(&w.word[0]);
+  if (e == cudaSuccess) e = rope_flags(&w.word[1]);
+  if (e == cudaSuccess) e = prefix_flags(&w.word[2]);
+  if (e == cudaSuccess) e = prefix_tc_flags(&w.word[3]);
+  if (e != cudaSuccess) return e;
+  static std::mutex one_at_a_time;
+  const std::lock_guard<std::mutex> lock(one_at_a_time);
+  e = launch_k_pdl(false, collect_flags_kernel, dim3(1), dim3(1), 0, cudaStream_t(nullptr), w);
+  return e == cudaSuccess ? cudaMemcpyFromSymbol(flags, g_collected, sizeof(unsigned int)) : e;
 }
 
 cudaError_t launch_gemv(const QuantTensor& t, int64_t N, int64_t K, const uint16_t* x, int batch,

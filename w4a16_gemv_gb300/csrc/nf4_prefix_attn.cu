@@ -892,11 +892,8 @@ cudaError_t launch_prefix_attention(const nf4_prefix_attention_args& a, void* wo
   return a.dtype == NF4_BF16 ? launch_typed<Bf16>(p, stream) : launch_typed<Fp16>(p, stream);
 }
 
-cudaError_t read_and_clear_prefix_flags(unsigned int* flags) {
-  const unsigned int zero = 0;
-  const cudaError_t e = cudaMemcpyFromSymbol(flags, g_prefix_flags, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_prefix_flags, &zero, sizeof(unsigned int));
+cudaError_t prefix_flags(unsigned int** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_prefix_flags);
 }
 
 }  // namespace nf4

@@ -859,11 +859,8 @@ cudaError_t launch_prefix_tc(const PrefixArgs& p, nf4_dtype dtype, unsigned item
   return launch_typed<false>(p, maps, dtype, items, stream);
 }
 
-cudaError_t read_and_clear_prefix_tc_flags(unsigned int* flags) {
-  const unsigned int zero = 0;
-  const cudaError_t e = cudaMemcpyFromSymbol(flags, g_prefix_tc_flags, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_prefix_tc_flags, &zero, sizeof(unsigned int));
+cudaError_t prefix_tc_flags(unsigned int** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_prefix_tc_flags);
 }
 
 }  // namespace nf4

@@ -565,11 +565,8 @@ cudaError_t launch_float(RopeArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t read_and_clear_rope_flags(unsigned int* flags) {
-  const unsigned int zero = 0;
-  const cudaError_t e = cudaMemcpyFromSymbol(flags, g_rope_flags, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_rope_flags, &zero, sizeof(unsigned int));
+cudaError_t rope_flags(unsigned int** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_rope_flags);
 }
 
 cudaError_t launch_rope_table(const nf4_rope_table_args& a, cudaStream_t stream) {
