@@ -92,3 +92,51 @@ def test_tokens_that_go_nowhere_beside_others(dim):
     torch.cuda.synchronize()
     assert torch.equal(cache, kept) and all(torch.equal(g, want) for g in got)
     assert nf4.nf4_device_error_flags() == 0
+
+
+def test_calls_that_follow_one_another_through_one_workspace():
+    """Steps of an append and an attention over it, of three plans (own keys joined on the way out, two launches and a join,
+    one launch) and two values of every input, never synchronised: first through one workspace in one stream, then in two
+    streams with one each. A part read before it is written, or overwritten before it is read, is another call's."""
+    nf4 = lib()
+    cases = []
+    for prefix, counts, lens in ((700, [300, 150], [300, 200]), (6000, [1] * 40, [90 + b for b in range(40)]),
+                                 (500, [60], [0])):
+        for seed in (1, 2):
+            width = None if lens[0] else 0
+            c = Call(8, 2, 128, prefix, lens, counts, seed=seed, junk=0.25, width=width)
+            tokens = sum(counts)
+            new = torch.randn(tokens, 12, 128, device="cuda").bfloat16()
+            table = nf4.nf4_rope_table(100, 128, base=50.0 * seed)
+            pos = torch.randint(0, 100, (tokens,), device="cuda")
+            # every token's key and value go to its sequence's last slots, or nowhere
+            slots = []
+            for b, (n, m) in enumerate(zip(counts, lens)):
+                at = [m - n + i for i in range(n)]
+                slots += [int(c.suffix_pages[b, j // c.page]) * c.page + j % c.page if m else -1 for j in at]
+            cases.append((c, new, table, pos, torch.tensor(slots, device="cuda")))
+    need = max(nf4.nf4_prefix_attention_workspace_size(*c.args(), cu_q=c.cu_q) for c, *_ in cases)
+
+    def step(n, ws):
+        c, new, table, pos, slots = cases[n]
+        q = nf4.nf4_kv_append(c.k, c.v, slots, new[:, 8:10], new[:, 10:], pos, table, q=new[:, :8])
+        return nf4.nf4_prefix_attention(q, *c.args()[1:], cu_q=c.cu_q, return_lse=True, workspace=ws)
+
+    spaces = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    want = []
+    for n in range(len(cases)):
+        want.append(step(n, spaces[0]))
+        torch.cuda.synchronize()
+    # (in two streams, each keeps to cases of its own: an append writes the cache that its call reads)
+    for parts in ([list(range(6))], [[0, 2, 4], [1, 3, 5]]):
+        streams = [torch.cuda.Stream() for _ in parts]
+        got = []
+        for i in range(60):
+            for k, (mine, s) in enumerate(zip(parts, streams)):
+                with torch.cuda.stream(s):
+                    n = mine[i * 5 % len(mine)]
+                    got.append((n, *step(n, spaces[k])))
+        torch.cuda.synchronize()
+        for n, out, lse in got:
+            assert torch.equal(out, want[n][0]) and torch.equal(lse, want[n][1]), n
+    assert nf4.nf4_device_error_flags() == 0
