@@ -88,13 +88,15 @@ NF4_API int nf4_last_cuda_error(void);
 /*
  * nf4_device_error_flags -- read and clear the library's device-side error
  * flags. Bit 0 is set when a bounded wait of the tensor-core GEMV (batches
- * 9..64) on its own copy or MMA pipeline ran out (about one second); that
- * launch then writes undefined values to its outputs and finishes instead
- * of hanging. Bit 1 is set when a kernel of nf4_attention.h read an index
- * (position, slot, page, length) on the device that is out of range; the call
- * says what then becomes of its outputs. The flags are one word per device, shared by every stream and
- * caller of the library. Synchronises with the device (cudaMemcpyFromSymbol).
- * `flags` is a host pointer.
+ * 9..64) or of nf4_prefix_attention on its own copy or MMA pipeline ran out
+ * (about one second); that launch then writes undefined values to its outputs
+ * and finishes instead of hanging. Bit 1 is set when a kernel of
+ * nf4_attention.h read an index (position, slot, page, length) on the device
+ * that is out of range; the call says what then becomes of its outputs. The
+ * flags are one word per device, shared by every stream and caller of the
+ * library; each is reported once. Synchronises with the device
+ * (cudaMemcpyFromSymbol, after a launch on the default stream). `flags` is a
+ * host pointer.
  * Errors: NF4_ERR_NULL, NF4_ERR_CUDA.
  */
 NF4_API nf4_status nf4_device_error_flags(unsigned int* flags);

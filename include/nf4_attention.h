@@ -192,7 +192,9 @@ NF4_API size_t nf4_prefix_attention_workspace_size(const nf4_prefix_attention_ar
  * A NaN or infinity in k or v reaches every row that sees it; one in v of an
  * own key may also reach rows of the same sequence that stand before it.
  * cu_q, lengths and pages are read on the device, so a recorded graph can be
- * replayed as sequences grow within suffix_pages_width. Lengths out of range
+ * replayed as sequences grow within suffix_pages_width. (The work is shared out
+ * for sequences about that long: a table many times wider than the sequences
+ * are long costs time, not exactness.) Lengths out of range
  * are clamped into it; rows that would read a page outside 0 .. num_pages - 1
  * are undefined; both set bit 1 of the device error flags. Tokens that no
  * sequence holds attend to the prefix alone.

@@ -16,10 +16,16 @@
 // handful of rows only: the bytes of the cache bound them, and the 16 x 8 x 16
 // tensor instruction does the arithmetic, since the 128 rows of the
 // 5th-generation ones would be empty. Own keys alone, 32 heads of 128: 128
-// sequences of 187 keys take 64-66 us (6.1 TB/s, 90% of measured copy
-// bandwidth), 64 of 750 keys 129 us (93%). Short sequences are bound by a
+// sequences of 187 keys take 66 us (6.0 TB/s, 89% of measured copy
+// bandwidth), 64 of 750 keys 128 us (93%). Short sequences are bound by a
 // warp's instructions (start, addresses, epilogue: 2200 of them for 75 keys before
-// the addresses were made cheaper): 128 x 75 keys 35 us (67%).
+// the addresses were made cheaper): 128 x 75 keys 37 us (64%).
+//
+// The weights e^(s - m) are rounded to the caches' 16-bit type for the product
+// with v: a tensor instruction takes both operands in one type, and a second
+// product with the remainders would double that work. One rounding per key
+// (2^-8 of its weight in bf16, 2^-11 in fp16), independent from key to key, adds
+// about what the output's own rounding does.
 #include "nf4_prefix_attn.cuh"
 
 namespace nf4 {
@@ -680,7 +686,7 @@ cudaError_t launch_typed(const PrefixArgs& p, cudaStream_t stream) {
 namespace {
 
 constexpr int64_t kStreamBytes = 32 << 20;  // a quarter of L2
-constexpr int kMaxRanges = 152;  // per row, of the shared and of the own keys each
+constexpr int kMaxRanges = 152;  // per row, of the shared and of the own keys each (more where ranges reach kMostKeys)
 
 // Keys per range of the mma kernel, in units of 64: about eight items per SM
 // where there is that much, else one for each CTA that fits on the SMs (128

@@ -12,12 +12,13 @@
 //
 // One CTA of 16 warps per SM:
 //   * warps 0-3 and 4-7: softmax of tile 0 and 1, one row per thread. Scores
-//     come from tensor memory into registers, the weights exp2(s - m) go back as
-//     16-bit pairs over the same columns, where the second product reads them
-//     as its A operand. m is the maximum at the time of the last rescale: O and l are
-//     rescaled only when a row's maximum has grown past 2^8 (exact all the same,
-//     since O and l share m; binary32 and the 16-bit weights hold 2^8 times 1
-//     with the same relative error), so that O is rarely touched;
+//     come from tensor memory into registers, the weights exp2(s - m) (in binary16
+//     lifted, see kLift) go back as 16-bit pairs, V's type, over the same columns,
+//     where the second product reads them as its A operand. m is the maximum at the
+//     time of the last rescale: O and l are rescaled only when a row's maximum has
+//     grown past 2^8 (exact all the same, since O and l share m; binary32 and the
+//     16-bit weights hold 2^8 times 1 with the same relative error), so that O is
+//     rarely touched;
 //   * warp 8: keys and values from their pages into a ring of 128-row tiles, by
 //     tensor copies (TMA) of as many rows as are sure to lie in one page, one
 //     lane per box; boxes past the range, or on a page that does not exist,
@@ -36,8 +37,8 @@
 // Tensor memory: S (and P) of the tiles in columns 0 and 128, O in 256 and 384.
 // Measured: 4864 tokens x 8 query heads over 16384 keys of 2 heads x 128 in
 // bf16 take 195 us (1670 TFLOP/s, 88% of measured bf16 peak; head_dim 64: 170 us,
-// 960); 12 heads of sixteen tokens stream 2^20 keys at 6.7 TB/s; a call over 8192
-// keys takes 8.5 us of start, two key tiles and partial results.
+// 960); 12 heads of sixteen tokens stream 2^20 keys in 159 us (6.75 TB/s); a call over
+// 8192 keys takes 8.5 us of start, two key tiles and partial results.
 // Waits are bounded; one that runs out sets bit 0 of the device error flags.
 #include <cuda.h>
 #include <cudaTypedefs.h>
