@@ -169,6 +169,16 @@ class Launch {
   bool other_ = false;
 };
 
+// A C call, without the interpreter's lock: a launch waits while its stream's queue
+// is full, and what it waits for may need another Python thread.
+template <typename F>
+nf4_status unlocked(F&& call) {
+  PyThreadState* const thread = PyEval_SaveThread();
+  const nf4_status st = call();
+  PyEval_RestoreThread(thread);
+  return st;
+}
+
 void raise_status(nf4_status status, const char* where) {
   PyObject* e = PyObject_CallFunction(g_error, "is", int(status), where);
   if (e) {
@@ -280,7 +290,7 @@ PyObject* py_qk_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t nargs, Py
     nf4_qk_norm_rope_args a;
     at::Tensor q_out, k_out;
     fill_qk(QkInputs{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], v[8], v[9]}, on, false, &a, &q_out, &k_out);
-    const nf4_status st = nf4_qk_norm_rope(&a, on.stream());
+    const nf4_status st = unlocked([&] { return nf4_qk_norm_rope(&a, on.stream()); });
     if (st != NF4_OK) raise_status(st, "nf4_qk_norm_rope");
     PyObject* q = given(v[8]) ? Py_NewRef(v[8]) : THPVariable_Wrap(q_out);
     PyObject* k = given(v[9]) ? Py_NewRef(v[9]) : THPVariable_Wrap(k_out);
@@ -326,7 +336,7 @@ PyObject* py_kv_append(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObj
     a.v_cache_head_stride = vc.stride(2);
     a.num_pages = shape[0];
     a.page_size = shape[1];
-    const nf4_status st = nf4_kv_append(&a, on.stream());
+    const nf4_status st = unlocked([&] { return nf4_kv_append(&a, on.stream()); });
     if (st != NF4_OK) raise_status(st, "nf4_kv_append");
     if (!given(v[7])) Py_RETURN_NONE;
     return given(v[12]) ? Py_NewRef(v[12]) : THPVariable_Wrap(q_out);
@@ -427,7 +437,7 @@ PyObject* py_prefix_attention(PyObject*, PyObject* const* args, Py_ssize_t nargs
       ws = on.empty({int64_t(bytes)}, at::kByte);
       scratch = ws.data_ptr();
     }
-    const nf4_status st = nf4_prefix_attention(&a, scratch, bytes, on.stream());
+    const nf4_status st = unlocked([&] { return nf4_prefix_attention(&a, scratch, bytes, on.stream()); });
     if (st != NF4_OK) raise_status(st, "nf4_prefix_attention");
     PyObject* o = given(v[9]) ? Py_NewRef(v[9]) : THPVariable_Wrap(out);
     if (!want_lse) return o;
