@@ -92,8 +92,9 @@ NF4_API int nf4_last_cuda_error(void);
  * (about one second); that launch then writes undefined values to its outputs
  * and finishes instead of hanging. Bit 1 is set when a kernel of
  * nf4_attention.h read an index (position, slot, page, length) on the device
- * that is out of range; the call says what then becomes of its outputs. The
- * flags are one word per device, shared by every stream and caller of the
+ * that is out of range; the call says what then becomes of its outputs (those
+ * of nf4_decoding.h likewise). Bit 2 is set when nf4_kv_pages had fewer free
+ * pages than a request asked for. The flags are one word per device, shared by every stream and caller of the
  * library; each is reported once. Synchronises with the device
  * (cudaMemcpyFromSymbol, after a launch on the default stream). `flags` is a
  * host pointer.

@@ -18,7 +18,8 @@ import torch
 __all__ = ["NF4Error", "NF4Weight", "nf4_dequant", "nf4_gemv", "nf4_gemv_ex", "DecodeStep", "nf4_quantize",
            "nf4_quantize_workspace_size", "nf4_quantize_noalloc", "nf4_version", "nf4_status_string",
            "nf4_device_error_flags", "LIB_PATH", "nf4_rope_table", "nf4_qk_norm_rope", "nf4_kv_append",
-           "nf4_prefix_attention", "nf4_prefix_attention_workspace_size"]
+           "nf4_prefix_attention", "nf4_prefix_attention_workspace_size", "nf4_kv_pages", "nf4_tree_attention",
+           "nf4_tree_attention_workspace_size", "nf4_adjust_logits", "nf4_tree_commit"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnf4.so")
 
@@ -94,7 +95,8 @@ def nf4_status_string(status: int) -> str:
 
 def nf4_device_error_flags() -> int:
     """Read and clear the device-side error flags (bit 0: a bounded wait ran out; bit 1: an index
-    that the attention side read on the device was out of range)."""
+    that the attention side, or a call around a decode step, read on the device was out of range;
+    bit 2: nf4_kv_pages had fewer free pages than it was asked for)."""
     f = ctypes.c_uint(0)
     _check(_lib.nf4_device_error_flags(ctypes.byref(f)), "nf4_device_error_flags")
     return int(f.value)
@@ -349,6 +351,8 @@ def gemv(wt: NF4Weight, x: torch.Tensor, y=None, stream=None, bias=None, out_dty
 try:
     from .attention import (nf4_kv_append, nf4_prefix_attention,  # noqa: E402
                             nf4_prefix_attention_workspace_size, nf4_qk_norm_rope, nf4_rope_table)
+    from .decoding import (nf4_adjust_logits, nf4_kv_pages, nf4_tree_attention,  # noqa: E402
+                           nf4_tree_attention_workspace_size, nf4_tree_commit)
 except ImportError as _error:
     def _without(name, error=_error):
         def call(*args, **kwargs):
@@ -357,5 +361,6 @@ except ImportError as _error:
         return call
 
     for _name in ("nf4_rope_table", "nf4_qk_norm_rope", "nf4_kv_append", "nf4_prefix_attention",
-                  "nf4_prefix_attention_workspace_size"):
+                  "nf4_prefix_attention_workspace_size", "nf4_kv_pages", "nf4_tree_attention",
+                  "nf4_tree_attention_workspace_size", "nf4_adjust_logits", "nf4_tree_commit"):
         globals()[_name] = _without(_name)

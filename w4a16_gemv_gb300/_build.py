@@ -17,7 +17,9 @@ BINDING = os.path.join(PKG, "_attention.so")
 BINDING_KEY = os.path.join(OBJDIR, "binding.txt")
 SOURCES = ("nf4_api.cu", "nf4_dequant.cu", "nf4_gemv.cu", "nf4_gemv_b1.cu", "nf4_gemv_stream.cu",
            "nf4_quantize.cu", "nf4_step.cu", "nf4_gemm_tc.cu", "nf4_attn_api.cu", "nf4_rope.cu",
-           "nf4_prefix_attn.cu", "nf4_prefix_attn_tc.cu")
+           "nf4_prefix_attn.cu", "nf4_prefix_attn_tc.cu", "nf4_decoding_api.cu", "nf4_kv_pages.cu", "nf4_adjust_logits.cu",
+           "nf4_tree_commit.cu")
+BINDINGS = ("attention_binding.cpp", "decoding_binding.cpp")
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 
@@ -62,8 +64,9 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _binding_command(out: str) -> list[str]:
-    """Compile and link the Python entry points against the running interpreter, torch and libnf4.so."""
+def _binding_commands(out: str) -> tuple[list[list[str]], list[str]]:
+    """Compile the Python entry points against the running interpreter, torch and the headers, one command per source;
+    link them with libnf4.so."""
     import sysconfig
 
     import torch
@@ -72,49 +75,50 @@ def _binding_command(out: str) -> list[str]:
             sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include"),
             INCLUDE]
     libs = os.path.join(root, "lib")
-    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[a for d in dirs for a in ("-isystem", d)],
-            os.path.join(CSRC, "attention_binding.cpp"), "-o", out, "-L", PKG, "-l:libnf4.so", "-L", libs, "-ltorch_python",
-            "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    cxx = os.environ.get("CXX", "g++")
+    objs = [os.path.join(OBJDIR, f.replace(".cpp", ".o")) for f in BINDINGS]
+    flags = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[a for d in dirs for a in ("-isystem", d)]]
+    return ([[cxx, *flags, "-c", os.path.join(CSRC, f), "-o", o] for f, o in zip(BINDINGS, objs)],
+            [cxx, "-shared", *objs, "-o", out, "-L", PKG, "-l:libnf4.so", "-L", libs, "-ltorch_python", "-ltorch", "-ltorch_cpu",
+             "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"])
 
 
 def build(force: bool = False, verbose: bool = False, extra: tuple[str, ...] = ()) -> str:
-    """Compile every source to an object in parallel, link libnf4.so, then the Python entry points."""
+    """Compile every source to an object in parallel, link libnf4.so and the Python entry points."""
     if not force and not _stale():
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)
     nvcc = nvcc_path()
+    objs = [os.path.join(OBJDIR, src.replace(".cu", ".o")) for src in SOURCES]
+    tmp_binding = BINDING + f".tmp{os.getpid()}"
+    compile_binding, link_binding = _binding_commands(tmp_binding)
     procs = []
-    for src in SOURCES:
-        obj = os.path.join(OBJDIR, src.replace(".cu", ".o"))
-        cmd = [nvcc, *nvcc_flags(extra), "-c", os.path.join(CSRC, src), "-o", obj]
+    for src, cmd in [*((src, [nvcc, *nvcc_flags(extra), "-c", os.path.join(CSRC, src), "-o", obj])
+                       for src, obj in zip(SOURCES, objs)), *zip(BINDINGS, compile_binding)]:
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
-        procs.append((src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    objs = []
+        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
-    for src, obj, p in procs:
+    for src, p in procs:
         out, _ = p.communicate()
         if p.returncode != 0:
             failed.append((src, out.decode(errors="replace")))
         elif verbose and out:
             print(out.decode(errors="replace"), file=sys.stderr)
-        objs.append(obj)
     if failed:
         msg = "\n".join(f"--- {s}\n{o}" for s, o in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
+        raise RuntimeError(f"the compiler failed:\n{msg}")
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, "-gencode", GENCODE, "-shared", "-o", tmp, *objs]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
-    tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = _binding_command(tmp)
     if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    p = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        print(" ".join(link_binding), file=sys.stderr)
+    p = subprocess.run(link_binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if p.returncode != 0:
         raise RuntimeError(f"g++ failed:\n{p.stdout.decode(errors='replace')}")
-    os.replace(tmp, BINDING)
+    os.replace(tmp_binding, BINDING)
     with open(BINDING_KEY, "w") as f:
         f.write(_binding_key())
     return LIB

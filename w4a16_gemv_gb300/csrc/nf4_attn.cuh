@@ -2,7 +2,7 @@
 // (the entry points of include/nf4_attention.h).
 #pragma once
 
-#include "nf4_attention.h"
+#include "nf4_decoding.h"
 #include "nf4_internal.cuh"
 
 namespace nf4 {
@@ -25,8 +25,12 @@ cudaError_t launch_qk_rope(const nf4_qk_norm_rope_args& a, const nf4_kv_append_a
                            cudaStream_t stream);
 size_t prefix_attention_workspace_bytes(const nf4_prefix_attention_args& a);
 // *enough is false, and nothing was launched, where the workspace does not do.
-cudaError_t launch_prefix_attention(const nf4_prefix_attention_args& a, void* workspace, size_t workspace_bytes,
-                                    bool* enough, cudaStream_t stream);
+// `tree`: null, or the call whose attention member `a` is.
+cudaError_t launch_prefix_attention(const nf4_prefix_attention_args& a, const nf4_tree_attention_args* tree,
+                                    void* workspace, size_t workspace_bytes, bool* enough, cudaStream_t stream);
+// Host-side checks of the attention calls: the sizes, and (tokens > 0) the rest.
+nf4_status check_attention_sizes(const nf4_prefix_attention_args& a);
+nf4_status check_attention(const nf4_prefix_attention_args& a);
 
 // 16-bit element types: conversions to and from binary32.
 struct Bf16 {

@@ -45,6 +45,10 @@ nf4_status check_qk(const nf4_qk_norm_rope_args& a, bool append) {
   return NF4_OK;
 }
 
+}  // namespace
+
+namespace nf4 {
+
 nf4_status check_attention_sizes(const nf4_prefix_attention_args& a) {
   if (!in(a.batch, 0, int64_t(1) << 20) || !in(a.tokens, 0, int64_t(1) << 24) || !in(a.k_heads, 1, 65535) ||
       !in(a.q_heads, 1, 65535) || a.q_heads % a.k_heads != 0)
@@ -66,7 +70,30 @@ nf4_status check_attention_sizes(const nf4_prefix_attention_args& a) {
   return NF4_OK;
 }
 
-}  // namespace
+nf4_status check_attention(const nf4_prefix_attention_args& a) {
+  if (!a.cu_q && a.tokens != a.batch) return NF4_ERR_INVALID_SIZE;
+  if (a.tokens == 0) return NF4_OK;
+  const bool own = a.batch > 0 && a.suffix_pages_width > 0;
+  if (!a.q || !a.out || (a.prefix_len > 0 && !a.prefix_pages) || (own && (!a.suffix_pages || !a.suffix_lens)) ||
+      (a.num_pages > 0 && (a.prefix_len > 0 || own) && (!a.k_cache || !a.v_cache)))
+    return NF4_ERR_NULL;
+  // the stride of a dimension of one is never used
+  const int64_t sizes[] = {a.tokens, a.q_heads, a.num_pages, a.page_size, a.k_heads};
+  const int64_t strides[][5] = {{a.q_token_stride, a.q_head_stride, 0, 0, 0},
+                                {a.out_token_stride, a.out_head_stride, 0, 0, 0},
+                                {0, 0, a.k_page_stride, a.k_slot_stride, a.k_head_stride},
+                                {0, 0, a.v_page_stride, a.v_slot_stride, a.v_head_stride}};
+  for (const auto& of : strides)
+    for (int i = 0; i < 5; ++i)
+      if (sizes[i] > 1 && of[i] % 8 != 0) return NF4_ERR_MISALIGNED;
+  if (!aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) ||
+      !aligned(a.lse, 4) || !aligned(a.prefix_pages, 4) || !aligned(a.suffix_pages, 4) ||
+      !aligned(a.suffix_lens, 4) || !aligned(a.cu_q, 4))
+    return NF4_ERR_MISALIGNED;
+  return NF4_OK;
+}
+
+}  // namespace nf4
 
 extern "C" {
 
@@ -114,7 +141,7 @@ nf4_status nf4_kv_append(const nf4_kv_append_args* args, nf4_stream_t stream) {
 }
 
 size_t nf4_prefix_attention_workspace_size(const nf4_prefix_attention_args* args) {
-  if (!args || check_attention_sizes(*args) != NF4_OK || args->tokens == 0) return 0;
+  if (!args || nf4::check_attention_sizes(*args) != NF4_OK || args->tokens == 0) return 0;
   return nf4::prefix_attention_workspace_bytes(*args);
 }
 
@@ -122,29 +149,12 @@ nf4_status nf4_prefix_attention(const nf4_prefix_attention_args* args, void* wor
                                 nf4_stream_t stream) {
   if (!args) return NF4_ERR_NULL;
   const nf4_prefix_attention_args& a = *args;
-  const nf4_status st = check_attention_sizes(a);
+  const nf4_status st = nf4::check_attention_sizes(a);
   if (st != NF4_OK) return st;
-  if (!a.cu_q && a.tokens != a.batch) return NF4_ERR_INVALID_SIZE;
-  if (a.tokens == 0) return NF4_OK;
-  const bool own = a.batch > 0 && a.suffix_pages_width > 0;
-  if (!a.q || !a.out || (a.prefix_len > 0 && !a.prefix_pages) || (own && (!a.suffix_pages || !a.suffix_lens)) ||
-      (a.num_pages > 0 && (a.prefix_len > 0 || own) && (!a.k_cache || !a.v_cache)))
-    return NF4_ERR_NULL;
-  // the stride of a dimension of one is never used
-  const int64_t sizes[] = {a.tokens, a.q_heads, a.num_pages, a.page_size, a.k_heads};
-  const int64_t strides[][5] = {{a.q_token_stride, a.q_head_stride, 0, 0, 0},
-                                {a.out_token_stride, a.out_head_stride, 0, 0, 0},
-                                {0, 0, a.k_page_stride, a.k_slot_stride, a.k_head_stride},
-                                {0, 0, a.v_page_stride, a.v_slot_stride, a.v_head_stride}};
-  for (const auto& of : strides)
-    for (int i = 0; i < 5; ++i)
-      if (sizes[i] > 1 && of[i] % 8 != 0) return NF4_ERR_MISALIGNED;
-  if (!aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.k_cache, 16) || !aligned(a.v_cache, 16) ||
-      !aligned(a.lse, 4) || !aligned(a.prefix_pages, 4) || !aligned(a.suffix_pages, 4) ||
-      !aligned(a.suffix_lens, 4) || !aligned(a.cu_q, 4))
-    return NF4_ERR_MISALIGNED;
+  const nf4_status rest = nf4::check_attention(a);
+  if (rest != NF4_OK || a.tokens == 0) return rest;
   bool enough = false;
-  const cudaError_t e = nf4::launch_prefix_attention(a, workspace, workspace_bytes, &enough,
+  const cudaError_t e = nf4::launch_prefix_attention(a, nullptr, workspace, workspace_bytes, &enough,
                                                      reinterpret_cast<cudaStream_t>(stream));
   return enough ? nf4::status_of(e) : NF4_ERR_WORKSPACE;
 }

@@ -25,7 +25,7 @@
 //     shared memory, so that small N still spreads over all SMs.
 #include <mutex>
 
-#include "nf4_attn.cuh"
+#include "nf4_decoding.cuh"
 #include "nf4_internal.cuh"
 
 namespace nf4 {
@@ -377,13 +377,14 @@ cudaError_t dispatch_batch(const QuantTensor& t, int64_t N, int64_t K, const uin
 
 // The words of the device error flags, taken and cleared in one launch (read and
 // cleared one by one, four words take eight synchronous copies, 52 us).
+constexpr int kFlagWords = 7;
 struct FlagWords {
-  unsigned int* word[4];
+  unsigned int* word[kFlagWords];
 };
 __device__ unsigned int g_collected;
 __global__ void collect_flags_kernel(FlagWords w) {
   unsigned int all = 0;
-  for (int i = 0; i < 4; ++i) all |= atomicExch(w.word[i], 0u);
+  for (int i = 0; i < kFlagWords; ++i) all |= atomicExch(w.word[i], 0u);
   g_collected = all;
 }
 
@@ -391,12 +392,16 @@ __global__ void collect_flags_kernel(FlagWords w) {
 
 cudaError_t read_and_clear_device_flags(unsigned int* flags) {
   // one word per translation unit that reports something: the tensor-core
-  // GEMV (waits) and the attention side (waits, indices read on the device)
+  // GEMV (waits), the attention side and the calls around a step (waits, indices
+  // read on the device, pages that ran out)
   FlagWords w;
   cudaError_t e = tc_flags(&w.word[0]);
   if (e == cudaSuccess) e = rope_flags(&w.word[1]);
   if (e == cudaSuccess) e = prefix_flags(&w.word[2]);
   if (e == cudaSuccess) e = prefix_tc_flags(&w.word[3]);
+  if (e == cudaSuccess) e = pages_flags(&w.word[4]);
+  if (e == cudaSuccess) e = logits_flags(&w.word[5]);
+  if (e == cudaSuccess) e = commit_flags(&w.word[6]);
   if (e != cudaSuccess) return e;
   static std::mutex one_at_a_time;
   const std::lock_guard<std::mutex> lock(one_at_a_time);

@@ -82,7 +82,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 // One item with tiles of R rows. The warps' key shares of R = 16 are joined
 // through shared memory at the end.
-template <typename H, int DP, int R, int W>
+template <typename H, int DP, int R, int W, bool T>
 __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it, unsigned char* smem) {
   constexpr int kWarps = W, kThreads = Shape<R, W>::kThreads, kKeys = Shape<R, W>::kKeys;
   constexpr int KW = R == 64 ? kKeys : kKeys / kWarps;  // keys of a stage per warp
@@ -200,10 +200,10 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
     }
   }
   // keys (within the segment) that the two rows see
-  const int lima = ra < it.rows ? min(visible_keys(it, (it.r0 + ra) / a.group), it.k1) : 0;
-  const int limb = rb < it.rows ? min(visible_keys(it, (it.r0 + rb) / a.group), it.k1) : 0;
+  const int lima = ra < it.rows ? min(visible_keys<T>(it, (it.r0 + ra) / a.group), it.k1) : 0;
+  const int limb = rb < it.rows ? min(visible_keys<T>(it, (it.r0 + rb) / a.group), it.k1) : 0;
   // up to here no row of the tile is masked
-  const int free_to = min(visible_keys(it, it.r0 / a.group), it.k1);
+  const int free_to = min(unmasked_keys<T>(it, it.r0 / a.group), it.k1);
 
   float o[DP / 8][4];
 #pragma unroll
@@ -255,6 +255,18 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             if (j0 + n * 8 + (x & 1) >= (x < 2 ? lima : limb)) s[n][x] = -INFINITY;
+        if constexpr (T) {
+          if (it.own) {  // at most 64 keys of a warp: one window per row
+            const int first_key = it.k0 + i * kKeys + kw;
+            const uint64_t wa = lima > 0 ? tree_window(a, it, it.t0 + (it.r0 + ra) / a.group, first_key) : 0ull;
+            const uint64_t wb = limb > 0 ? tree_window(a, it, it.t0 + (it.r0 + rb) / a.group, first_key) : 0ull;
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (!((x < 2 ? wa : wb) >> (n * 8 + (lane & 3) * 2 + (x & 1)) & 1ull)) s[n][x] = -INFINITY;
+          }
+        }
       }
       float xa = -INFINITY, xb = -INFINITY;
 #pragma unroll
@@ -419,14 +431,14 @@ __device__ __forceinline__ void attend(const PrefixArgs& a, const PrefixItem& it
 // ahead of letting this one start, so there is nothing to wait for here; but
 // what follows (the join) only waits for this launch, so its last CTA ends
 // after the other launch did.
-template <typename H, int DP, int R, int W>
+template <typename H, int DP, int R, int W, bool T>
 __global__ void __launch_bounds__(Shape<R, W>::kThreads, R == 64 ? 2 : (DP == 64 ? 20 : 12) / W)
     prefix_mma_kernel(const __grid_constant__ PrefixArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   if (!a.beside) pdl_wait_prior_grid();
   pdl_allow_dependents();
-  const PrefixItem it = prefix_item(a, unsigned(a.first) + blockIdx.x, &g_prefix_flags);
-  if (it.rows > 0) attend<H, DP, R, W>(a, it, smem);
+  const PrefixItem it = prefix_item<T>(a, unsigned(a.first) + blockIdx.x, &g_prefix_flags);
+  if (it.rows > 0) attend<H, DP, R, W, T>(a, it, smem);
   if (a.fused) unheld_rows<H>(a, W, &g_prefix_flags);
   if (a.beside && blockIdx.x + 1 == gridDim.x) pdl_wait_prior_grid();
 }
@@ -616,9 +628,9 @@ __global__ void __launch_bounds__(128) prefix_empty_kernel(const __grid_constant
   if (lane == 0 && a.lse) a.lse[row] = -INFINITY;
 }
 
-template <typename H, int DP, int R, int W>
+template <typename H, int DP, int R, int W, bool T>
 cudaError_t launch_mma(const PrefixArgs& p, unsigned items, cudaStream_t stream) {
-  auto kern = prefix_mma_kernel<H, DP, R, W>;
+  auto kern = prefix_mma_kernel<H, DP, R, W, T>;
   constexpr int smem = kStages * 2 * Shape<R, W>::kKeys * int(kPitch<DP>);
   static PerDeviceCache attr_set;
   const cudaError_t e = set_max_dynamic_smem_once(kern, smem, attr_set);
@@ -626,10 +638,15 @@ cudaError_t launch_mma(const PrefixArgs& p, unsigned items, cudaStream_t stream)
   return launch_k(kern, dim3(items), dim3(Shape<R, W>::kThreads), smem, stream, p);
 }
 
-template <typename H, int DP>
+template <typename H, int DP, bool T>
 cudaError_t launch_rows(const PrefixArgs& p, int rows, unsigned items, cudaStream_t stream) {
-  if (rows == 64) return launch_mma<H, DP, 64, 4>(p, items, stream);
-  return items <= kFewItems ? launch_mma<H, DP, 16, 4>(p, items, stream) : launch_mma<H, DP, 16, 2>(p, items, stream);
+  if (rows == 64) return launch_mma<H, DP, 64, 4, T>(p, items, stream);
+  return items <= kFewItems ? launch_mma<H, DP, 16, 4, T>(p, items, stream)
+                            : launch_mma<H, DP, 16, 2, T>(p, items, stream);
+}
+template <typename H, bool T>
+cudaError_t launch_rows(const PrefixArgs& p, int rows, unsigned items, cudaStream_t stream) {
+  return p.dim <= 64 ? launch_rows<H, 64, T>(p, rows, items, stream) : launch_rows<H, 128, T>(p, rows, items, stream);
 }
 
 template <typename H, bool kCheck>
@@ -671,9 +688,10 @@ cudaError_t launch_typed(const PrefixArgs& p, cudaStream_t stream) {
     q.beside = first > 0;
     q.fused = p.fused && i == 1;
     q.direct = p.direct || q.fused;
-    e = tile == 256 ? launch_prefix_tc(q, H::kDtype, unsigned(items), stream)
-        : p.dim <= 64 ? launch_rows<H, 64>(q, tile, unsigned(items), stream)
-                      : launch_rows<H, 128>(q, tile, unsigned(items), stream);
+    const bool tree = p.tree && first + items > prefix_items;  // own keys are among them
+    e = tile == 256 ? launch_prefix_tc(q, H::kDtype, tree, unsigned(items), stream)
+        : tree      ? launch_rows<H, true>(q, tile, unsigned(items), stream)
+                    : launch_rows<H, false>(q, tile, unsigned(items), stream);
     first += items;
   }
   if (e != cudaSuccess || p.direct || p.fused) return e;
@@ -857,8 +875,8 @@ size_t prefix_attention_workspace_bytes(const nf4_prefix_attention_args& a) {
   return bytes;
 }
 
-cudaError_t launch_prefix_attention(const nf4_prefix_attention_args& a, void* workspace, size_t workspace_bytes,
-                                    bool* enough, cudaStream_t stream) {
+cudaError_t launch_prefix_attention(const nf4_prefix_attention_args& a, const nf4_tree_attention_args* tree,
+                                    void* workspace, size_t workspace_bytes, bool* enough, cudaStream_t stream) {
   PrefixArgs p = {};
   size_t bytes = 0;
   plan_prefix_attention(a, &p, &bytes);
@@ -884,6 +902,11 @@ cudaError_t launch_prefix_attention(const nf4_prefix_attention_args& a, void* wo
   p.suffix_pages = a.suffix_pages;
   p.suffix_lens = a.suffix_lens;
   p.cu_q = a.cu_q;
+  if (tree) {
+    p.tree = tree->tree_mask;
+    p.tree_stride = tree->tree_mask_stride;
+    p.tree_words = int(tree->tree_words);
+  }
   p.suffix_pages_stride = a.suffix_pages_stride;
   p.page_size = int(a.page_size);
   p.page_shift = -1;

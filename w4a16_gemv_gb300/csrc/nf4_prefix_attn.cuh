@@ -24,6 +24,9 @@ struct PrefixArgs {
   const int32_t* suffix_pages;
   const int32_t* suffix_lens;
   const int32_t* cu_q;
+  const uint64_t* tree;                            // a tree's tokens: which nodes of its sequence each one sees (or null)
+  int64_t tree_stride;
+  int tree_words;
   int64_t suffix_pages_stride;
   int suffix_max;                                  // keys that the page table of a sequence can hold
   int prefix_len;
@@ -62,8 +65,8 @@ inline int prefix_tile_keys(int64_t page_size) {
 void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, size_t* bytes);
 
 // Items [p.first, p.first + items), tiles of 256 rows, on the tensor cores
-// (nf4_prefix_attn_tc.cu).
-cudaError_t launch_prefix_tc(const PrefixArgs& p, nf4_dtype dtype, unsigned items, cudaStream_t stream);
+// (nf4_prefix_attn_tc.cu); `tree`: some of them are own keys of trees.
+cudaError_t launch_prefix_tc(const PrefixArgs& p, nf4_dtype dtype, bool tree, unsigned items, cudaStream_t stream);
 
 // One work item, the same in every thread.
 struct PrefixItem {
@@ -79,9 +82,30 @@ struct PrefixItem {
   bool own;        // the sequence's own keys: token i sees the first len - n + i + 1
 };
 
-// Keys of the segment that token i (of n) sees.
+// Keys of the segment up to the last one that token i (of n) sees. Where the
+// tokens form a tree (T), that may be any; which ones, tree_window() says.
+template <bool T>
 __device__ __forceinline__ int visible_keys(const PrefixItem& it, int i) {
-  return it.own ? min(max(it.len - it.n + i + 1, 0), it.len) : it.len;
+  return it.own && !T ? min(max(it.len - it.n + i + 1, 0), it.len) : it.len;
+}
+// Keys that every row of the tile with the first token i sees.
+template <bool T>
+__device__ __forceinline__ int unmasked_keys(const PrefixItem& it, int i) {
+  return it.own && T ? max(it.len - it.n, 0) : visible_keys<T>(it, i);
+}
+
+// The nodes of a tree that token t sees, 64 keys at a time: bit j says whether it
+// sees key j0 + j of its sequence's own ones. Keys before the nodes are seen. (A
+// key past the last node is past the sequence's keys, and cut off with these.)
+__device__ __forceinline__ uint64_t tree_window(const PrefixArgs& a, const PrefixItem& it, int t, int j0) {
+  const int x = j0 - (it.len - it.n);  // node of key j0
+  if (x <= -64) return ~0ull;
+  const uint64_t* const row = a.tree + int64_t(t) * a.tree_stride;
+  if (x < 0) return row[0] << -x | ((1ull << -x) - 1);
+  const int word = x >> 6, shift = x & 63;
+  uint64_t w = word < a.tree_words ? row[word] >> shift : 0ull;
+  if (shift != 0 && word + 1 < a.tree_words) w |= row[word + 1] << (64 - shift);
+  return w;
 }
 
 // Tiles of own rows are numbered so that the sequence of a tile is found without
@@ -98,6 +122,7 @@ __device__ __forceinline__ int first_tile(const PrefixArgs& a, int t0, int b) {
 // Item `index` of a launch that covers prefix items first (a key/value head's
 // tiles of one key range side by side, so that they meet in L2), then suffix
 // items. Called by whole warps.
+template <bool T>
 __device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, unsigned index, unsigned int* flags) {
   PrefixItem it;
   const unsigned prefix_items = unsigned(a.prefix_tiles) * unsigned(a.k_heads) * unsigned(a.prefix_splits);
@@ -170,7 +195,7 @@ __device__ __forceinline__ PrefixItem prefix_item(const PrefixArgs& a, unsigned 
   it.len = min(max(len, 0), a.suffix_max);
   if (it.len != len && lane == 0) atomicOr(flags, kFlagBadIndex);
   it.pages = a.suffix_pages + int64_t(b0 + src) * a.suffix_pages_stride;
-  const int sees = visible_keys(it, (it.r0 + it.rows - 1) / a.group);  // the tile's last row sees most
+  const int sees = visible_keys<T>(it, (it.r0 + it.rows - 1) / a.group);  // the tile's last row sees most
   it.k0 = int(min(int64_t(split) * a.suffix_chunk, int64_t(sees)));
   it.k1 = int(min(int64_t(it.k0) + a.suffix_chunk, int64_t(sees)));
   return it;

@@ -226,7 +226,7 @@ struct Layout {
   static constexpr uint32_t kBytes = kBars + 256 + 1024;        // + slack to align the base
 };
 
-template <typename H, int DP, bool kTma>
+template <typename H, int DP, bool kTma, bool T>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefix_tc_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CacheMaps maps) {
   using L = Layout<DP>;
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   };
   if (unsigned(a.first) + blockIdx.x >= unsigned(a.prefix_tiles) * unsigned(a.k_heads) * unsigned(a.prefix_splits))
     begin();
-  const PrefixItem it = prefix_item(a, unsigned(a.first) + blockIdx.x, &g_prefix_tc_flags);
+  const PrefixItem it = prefix_item<T>(a, unsigned(a.first) + blockIdx.x, &g_prefix_tc_flags);
   const int n = (it.k1 - it.k0 + step - 1) / step;  // key tiles
   const bool works = it.rows > 0 && n > 0;          // the same in the whole CTA
   const int tiles = it.rows > kTileRows ? 2 : 1;
@@ -354,9 +354,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t s_col = tbase + lanes + uint32_t(tile) * 128u;
       const uint32_t o_col = tbase + lanes + 256u + uint32_t(tile) * 128u;
       const int r = tile * kTileRows + (warp & 3) * 32 + lane;
-      const int limit = r < it.rows ? min(visible_keys(it, (it.r0 + r) / a.group), it.k1) - it.k0 : 0;
+      const int limit = r < it.rows ? min(visible_keys<T>(it, (it.r0 + r) / a.group), it.k1) - it.k0 : 0;
       // key tiles below this one need no mask in this warp
-      int free_tiles = limit / step;
+      int free_tiles = T ? max(min(unmasked_keys<T>(it, 0), it.k1) - it.k0, 0) / step : limit / step;
       if (r >= it.rows) free_tiles = n;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) free_tiles = min(free_tiles, __shfl_xor_sync(0xffffffffu, free_tiles, d));
@@ -376,6 +376,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int j = 0; j < 128; ++j)
             if (i * step + j >= limit) s[j] = -INFINITY;
+          if constexpr (T) {
+            if (it.own && r < it.rows) {
+              const int t = it.t0 + (it.r0 + r) / a.group;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint64_t seen = tree_window(a, it, t, it.k0 + i * step + 64 * h);
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                  if (!(seen >> j & 1ull)) s[64 * h + j] = -INFINITY;
+              }
+            }
+          }
         }
         if (kTma && step < kTileKeys) {
 #pragma unroll
@@ -773,9 +785,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-template <typename H, int DP, bool kTma>
+template <typename H, int DP, bool kTma, bool T>
 cudaError_t launch_one(const PrefixArgs& p, const CacheMaps& maps, unsigned items, cudaStream_t stream) {
-  auto kern = prefix_tc_kernel<H, DP, kTma>;
+  auto kern = prefix_tc_kernel<H, DP, kTma, T>;
   static PerDeviceCache attr_set, regs;
   cudaError_t e = set_max_dynamic_smem_once(kern, int(Layout<DP>::kBytes), attr_set);
   if (e != cudaSuccess) return e;
@@ -830,19 +842,17 @@ bool encode_cache(const PrefixArgs& p, nf4_dtype dtype, const char* base, int64_
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kTma>
+template <bool kTma, bool T>
 cudaError_t launch_typed(const PrefixArgs& p, const CacheMaps& maps, nf4_dtype dtype, unsigned items,
                          cudaStream_t stream) {
   if (dtype == NF4_BF16)
-    return p.dim <= 64 ? launch_one<Bf16, 64, kTma>(p, maps, items, stream)
-                       : launch_one<Bf16, 128, kTma>(p, maps, items, stream);
-  return p.dim <= 64 ? launch_one<Fp16, 64, kTma>(p, maps, items, stream)
-                     : launch_one<Fp16, 128, kTma>(p, maps, items, stream);
+    return p.dim <= 64 ? launch_one<Bf16, 64, kTma, T>(p, maps, items, stream)
+                       : launch_one<Bf16, 128, kTma, T>(p, maps, items, stream);
+  return p.dim <= 64 ? launch_one<Fp16, 64, kTma, T>(p, maps, items, stream)
+                     : launch_one<Fp16, 128, kTma, T>(p, maps, items, stream);
 }
-
-}  // namespace
-
-cudaError_t launch_prefix_tc(const PrefixArgs& p, nf4_dtype dtype, unsigned items, cudaStream_t stream) {
+template <bool T>
+cudaError_t launch_maps(const PrefixArgs& p, nf4_dtype dtype, unsigned items, cudaStream_t stream) {
   CacheMaps maps = {};
   // Rows of a box: the largest power of two that divides the page (a box that
   // starts at a multiple of it stays in one page), 8 to 128.
@@ -856,8 +866,14 @@ cudaError_t launch_prefix_tc(const PrefixArgs& p, nf4_dtype dtype, unsigned item
                    &maps.k_head) &&
       encode_cache(p, dtype, p.v, p.v_ps, p.v_ss, p.v_hs, maps.box_rows, &maps.v, &maps.v_slot,
                    &maps.v_head))
-    return launch_typed<true>(p, maps, dtype, items, stream);
-  return launch_typed<false>(p, maps, dtype, items, stream);
+    return launch_typed<true, T>(p, maps, dtype, items, stream);
+  return launch_typed<false, T>(p, maps, dtype, items, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_tc(const PrefixArgs& p, nf4_dtype dtype, bool tree, unsigned items, cudaStream_t stream) {
+  return tree ? launch_maps<true>(p, dtype, items, stream) : launch_maps<false>(p, dtype, items, stream);
 }
 
 cudaError_t prefix_tc_flags(unsigned int** word) {
