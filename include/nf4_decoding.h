@@ -122,7 +122,7 @@ typedef struct nf4_adjust_logits_args {
                                   cu_rows[b] .. cu_rows[b + 1] - 1; NULL: one row each (rows == requests) */
   const int32_t* history;      /* NULL, or [requests][history_width]: tokens of each request, prompt first */
   int64_t history_stride;
-  int64_t history_width;       /* 0 .. 2^29 */
+  int64_t history_width;       /* 0 .. 2^28 */
   const int32_t* history_lens; /* [requests]: tokens that count, 0 .. history_width */
   const int32_t* prompt_lens;  /* NULL (0), or [requests]: how many of these are the prompt */
   const float* repetition;     /* NULL (1), or [requests] */

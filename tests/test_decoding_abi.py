@@ -140,7 +140,7 @@ def test_null_argument_structures(lib):
     ("nf4_adjust_logits", ERR_SIZE,
      [dict(rows=-1), dict(rows=(1 << 20) + 1), dict(vocab=0), dict(vocab=(1 << 24) + 1, out_stride=1 << 30),
       dict(requests=-1), dict(requests=(1 << 20) + 1), dict(logits_stride=-1), dict(out_stride=999), dict(out_stride=-1),
-      dict(history_width=-1), dict(history_width=(1 << 29) + 1), dict(history_stride=-1), dict(bias_width=1025),
+      dict(history_width=-1), dict(history_width=(1 << 28) + 1), dict(history_stride=-1), dict(bias_width=1025),
       dict(bias_width=-1), dict(bias_stride=-1), dict(mask_count=-1), dict(mask_stride=-1), dict(mask_rows=0, mask_count=4),
       dict(tree_words=0), dict(tree_words=1025), dict(tree_mask_stride=-1), dict(cu_rows=0)]),
     ("nf4_adjust_logits", ERR_DTYPE, [dict(dtype=3), dict(dtype=-1)]),

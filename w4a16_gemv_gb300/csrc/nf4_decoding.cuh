@@ -29,24 +29,24 @@ __device__ __forceinline__ unsigned cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-// All threads of the cluster; what they wrote to shared and device memory before
-// is there for all of them after. (Its wait is the hardware's: the CTAs of a
-// cluster are on their SMs together, and none of them leaves before.)
-__device__ __forceinline__ void cluster_barrier() {
+// A barrier of all threads of the cluster in two halves; with the release, what they
+// wrote to shared and device memory before is there for those that waited. (The wait
+// is the hardware's: the CTAs of a cluster are on their SMs together, and one that
+// has ended counts as arrived.)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_release() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_barrier() {
+  cluster_arrive_release();
+  cluster_wait();
 }
 // Address of `saddr` (this CTA's shared memory) in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_address(uint32_t saddr, unsigned rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
-}
-__device__ __forceinline__ void cluster_add(uint32_t addr, uint32_t v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void cluster_or(uint32_t addr, uint32_t v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void cluster_store64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
@@ -90,6 +90,21 @@ __device__ __forceinline__ void token_range(const int32_t* cu, int b, int total,
   *lo = min(max(x, 0), total);
   *hi = min(max(y, *lo), total);
   *bad = *bad || *lo != x || *hi != y;
+}
+
+// The last of n entries whose first token is at most t (the first, where none is), by a whole warp, 32 looks at a time.
+__device__ __forceinline__ int entry_of(const int32_t* cu, int n, int total, int t) {
+  if (!cu) return min(t, n - 1);
+  const int lane = threadIdx.x & 31;
+  int b = 0, span = n;
+  while (span > 1) {
+    const int step = (span + 31) >> 5, at = lane * step;
+    const bool before = at < span && offset_at(cu, b + at, total) <= t;
+    const int src = 31 - __clz(int(__ballot_sync(0xffffffffu, before) | 1u));
+    b += src * step;
+    span = min(step, span - src * step);
+  }
+  return b;
 }
 
 }  // namespace nf4

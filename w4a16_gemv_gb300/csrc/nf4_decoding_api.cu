@@ -79,7 +79,7 @@ nf4_status nf4_adjust_logits(const nf4_adjust_logits_args* args, nf4_stream_t st
       !in(a.logits_stride, 0, kMaxStride) || !in(a.out_stride, 0, kMaxStride) || !apart(a.rows, a.out_stride, a.vocab))
     return NF4_ERR_INVALID_SIZE;
   if (a.dtype != NF4_BF16 && a.dtype != NF4_FP16 && a.dtype != NF4_F32) return NF4_ERR_UNSUPPORTED_DTYPE;
-  if (a.history && (!in(a.history_width, 0, int64_t(1) << 29) || !in(a.history_stride, 0, kMaxStride)))
+  if (a.history && (!in(a.history_width, 0, int64_t(1) << 28) || !in(a.history_stride, 0, kMaxStride)))
     return NF4_ERR_INVALID_SIZE;
   if (a.bias_tokens && (!in(a.bias_width, 0, 1024) || !in(a.bias_stride, 0, kMaxStride))) return NF4_ERR_INVALID_SIZE;
   if (a.mask && (!in(a.mask_count, 0, kMaxBatch) || !in(a.mask_stride, 0, kMaxStride) ||

@@ -8,11 +8,13 @@
 // batch, so every request knows its places without waiting for the others.
 //
 // One cluster: every CTA forms the sums of the whole batch by itself (a few
-// bytes per request), then the CTAs share the pages and the tokens, with a barrier
-// of the cluster where one reads what another wrote (pages that come back before
-// any are taken, tables before tokens, and all inputs before the outputs that may
-// be the same arrays). Latency bounds it: a call of 16 bytes per token and a few
-// per request is a chain of four to six dependent loads.
+// bytes per request), then the CTAs share the pages and the tokens. A token's page
+// is looked up where it comes from (its row of the table, or the stack), not in
+// the table after it has been written, so that both go on at once; a barrier of the
+// cluster stands only where pages come back before any are taken, and in front of
+// the results that may be the same arrays as inputs. (Batches of more requests than
+// a CTA has threads go by chunks, and their tokens wait for the tables.) Latency
+// bounds it: a chain of loads, sums, loads and stores.
 #include "nf4_decoding.cuh"
 
 namespace nf4 {
@@ -21,6 +23,7 @@ namespace {
 __device__ unsigned int g_pages_flags = 0;
 
 constexpr int kMostThreads = 1024;
+constexpr int kNone = 0x7fffffff;
 
 struct PagesArgs {
   nf4_kv_pages_args a;
@@ -89,11 +92,15 @@ __device__ __forceinline__ int last_at_most(const V* list, int n, V v) {
   return at;
 }
 
+constexpr int kRun = 4;  // tokens of a thread, one after another, where there are more tokens than threads
+
 __global__ void __launch_bounds__(kMostThreads, 1) kv_pages_kernel(const __grid_constant__ PagesArgs p) {
   const nf4_kv_pages_args& a = p.a;
-  __shared__ uint64_t start[kMostThreads];  // of a chunk of requests: its pages' first place in the chunk,
-  __shared__ unsigned first[kMostThreads];  // and the first of these pages' place in its row
-  __shared__ int s_cu[kMostThreads + 1];    // a batch of one chunk: first tokens, lengths (or ~0: not served)
+  // of a chunk of requests: its missing (or surplus) pages' first place in the chunk, and the first one's place in
+  // its row; of a batch of one chunk also first tokens and lengths
+  __shared__ uint64_t start[kMostThreads];
+  __shared__ unsigned first[kMostThreads];
+  __shared__ int s_cu[kMostThreads + 1];
   __shared__ unsigned s_len[kMostThreads];
   __shared__ uint64_t sums[32];
   __shared__ uint64_t s_limit;
@@ -103,7 +110,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) kv_pages_kernel(const __grid_
   const int tid = threadIdx.x, threads = blockDim.x;
   const unsigned rank = cluster_rank(), ctas = cluster_size();
   const int share = int(rank) * threads + tid, shares = int(ctas) * threads;
-  const int batch = int(a.batch);
+  const int batch = int(a.batch), tokens = int(a.tokens);
   const bool one_chunk = batch <= threads;
   bool bad = false;
 
@@ -117,6 +124,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) kv_pages_kernel(const __grid_
     r = request_of(p, b0 + tid, &bad);
     back += r.back;
   }
+  if (tid == 0) s_failed = kNone;
   int top = free0;
   if (__syncthreads_or(back != 0)) {
     uint64_t done = 0;
@@ -143,8 +151,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) kv_pages_kernel(const __grid_
   // Pages that are taken. A request is served where the pages that it and those before it ask for are there;
   // `failed` is the first that is not.
   uint64_t taken = 0;
-  if (tid == 0) s_failed = 0x7fffffff;
-  int failed = 0x7fffffff;
+  int failed = kNone;
   for (int b0 = 0; b0 < batch; b0 += threads) {
     if (!one_chunk) r = request_of(p, b0 + tid, &bad);
     uint64_t total;
@@ -152,12 +159,20 @@ __global__ void __launch_bounds__(kMostThreads, 1) kv_pages_kernel(const __grid_
     start[tid] = mine;
     first[tid] = r.held;
     if (tid == 0) s_limit = total;
-    __syncthreads();
-    const bool fits = taken + mine + r.grow <= uint64_t(top);
-    if (r.grow > 0 && !fits) atomicMin(&s_failed, b0 + tid);
-    __syncthreads();
-    failed = s_failed;
-    if (failed == b0 + tid) s_limit = mine;
+    if (one_chunk && b0 + tid < batch) {
+      int lo, hi;
+      token_range(a.cu_q, tid, tokens, &lo, &hi, &bad);
+      s_cu[tid] = lo;
+      if (tid + 1 == batch) s_cu[batch] = hi;
+      s_len[tid] = r.len;
+    }
+    if (taken + total > uint64_t(top)) {  // the same in every thread
+      __syncthreads();
+      if (r.grow > 0 && taken + mine + r.grow > uint64_t(top)) atomicMin(&s_failed, b0 + tid);
+      __syncthreads();
+      failed = s_failed;
+      if (failed == b0 + tid) s_limit = mine;
+    }
     __syncthreads();
     const uint64_t limit = s_limit;
     for (uint64_t e = share; e < limit; e += shares) {
@@ -166,79 +181,91 @@ __global__ void __launch_bounds__(kMostThreads, 1) kv_pages_kernel(const __grid_
           __ldcg(a.free_pages + (uint64_t(top) - 1 - taken - e));
     }
     taken += limit;
-    if (failed != 0x7fffffff) break;
+    if (failed != kNone) break;
   }
   auto served = [&](const Request& q, int b) { return !q.wide && (q.need <= q.held || b < failed); };
-  if (one_chunk && tid < batch) {
-    int lo, hi;
-    token_range(a.cu_q, tid, int(a.tokens), &lo, &hi, &bad);
-    s_cu[tid] = lo;
-    if (tid + 1 == batch) s_cu[batch] = hi;
-    s_len[tid] = served(r, tid) ? r.len : ~0u;
-  }
-  cluster_barrier();  // tables are whole, and nobody needs held and free_count as they were
+  if (!one_chunk) cluster_barrier();  // tables are whole
 
-  // The requests' results. (Whether a request is served reads the same from held before and after.)
+  // The tokens, kRun at a time.
+  const bool vectors = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
+  const int run = tokens > shares ? kRun : 1;
+  for (int t0 = share * run; t0 < tokens; t0 += shares * run) {
+    int64_t slot[kRun], position[kRun];
+    int b = 0, lo = 0, hi = 0;   // the last token's request
+    unsigned len = 0, limit = 0; // its length, and the pages that its row has now (0: not served)
+    int at_page = -1, page = -1;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      const int t = t0 + i;
+      slot[i] = -1;
+      position[i] = 0;
+      if (i >= run || t >= tokens || batch == 0) continue;
+      if (t >= hi) {
+        if (one_chunk) {
+          b = a.cu_q ? last_at_most(s_cu, batch, t) : t;
+          lo = s_cu[b];
+          hi = a.cu_q ? s_cu[b + 1] : t + 1;
+          len = s_len[b];
+          const unsigned need = pages_of(p, len + unsigned(max(hi - lo, 0)));
+          limit = need <= unsigned(a.width) && (need <= first[b] || b < failed) ? need : 0u;
+        } else {
+          b = t;
+          if (a.cu_q) {
+            b = 0;
+            for (int step = 1 << (31 - __clz(batch)); step > 0; step >>= 1)
+              if (b + step < batch && offset_at(a.cu_q, b + step, tokens) <= t) b += step;
+          }
+          const Request q = request_of(p, b, &bad);
+          token_range(a.cu_q, b, tokens, &lo, &hi, &bad);
+          len = q.len;
+          limit = served(q, b) ? q.need : 0u;
+        }
+        at_page = -1;
+        if (t < lo || t >= hi) {  // no request holds it
+          hi = t;
+          continue;
+        }
+      }
+      position[i] = a.first_position + len + (a.depths ? a.depths[t] : t - lo);
+      if (limit == 0) continue;
+      const unsigned key = len + unsigned(t - lo);
+      const int at = int(p.page_shift >= 0 ? key >> p.page_shift : key / unsigned(a.page_size));
+      if (at != at_page) {
+        page = one_chunk && unsigned(at) >= first[b]
+                   ? __ldcg(a.free_pages + (uint64_t(top) - 1 - start[b] - (unsigned(at) - first[b])))
+                   : __ldcg(a.page_table + int64_t(b) * a.page_table_stride + at);
+        at_page = at;
+        bad = bad || page < 0;
+      }
+      if (page >= 0) slot[i] = int64_t(page) * a.page_size + (key - unsigned(at) * unsigned(a.page_size));
+    }
+    if (vectors && run == kRun && t0 + kRun <= tokens) {
+#pragma unroll
+      for (int i = 0; i < kRun; i += 2) {
+        *reinterpret_cast<longlong2*>(a.slots + t0 + i) = make_longlong2(slot[i], slot[i + 1]);
+        if (a.positions)
+          *reinterpret_cast<longlong2*>(a.positions + t0 + i) = make_longlong2(position[i], position[i + 1]);
+      }
+    } else {
+      for (int i = 0; i < kRun; ++i)
+        if (i < run && t0 + i < tokens) {
+          a.slots[t0 + i] = slot[i];
+          if (a.positions) a.positions[t0 + i] = position[i];
+        }
+    }
+  }
+
+  // The requests' results, when nobody needs held and free_count as they were.
+  cluster_barrier();
   for (int b = share; b < batch; b += shares) {
-    if (!one_chunk || ctas > 1) r = request_of(p, b, &bad);
+    if (!one_chunk) r = request_of(p, b, &bad);  // else this thread's own
     const bool yes = served(r, b);
     a.new_held[b] = int(yes ? r.need : r.held);
     a.new_lens[b] = int(yes ? r.len + r.n : r.len);
   }
   if (share == 0) {
     a.new_free_count[0] = top - int(taken);
-    if (failed != 0x7fffffff) atomicOr(&g_pages_flags, kFlagNoPages);
-  }
-
-  // The tokens.
-  const int tokens = int(a.tokens);
-  for (int t = share; t < tokens; t += shares) {
-    int b, lo, hi = tokens;
-    unsigned len;
-    bool yes = batch > 0;
-    if (one_chunk && yes) {
-      b = a.cu_q ? last_at_most(s_cu, batch, t) : t;
-      lo = s_cu[b];
-      hi = b + 1 < batch ? s_cu[b + 1] : s_cu[batch];
-      len = s_len[b];
-      yes = t >= lo && t < hi;
-      if (yes && len == ~0u) {
-        yes = false;
-        len = unsigned(max(a.lens[b], 0));
-        if (a.positions) a.positions[t] = a.first_position + len + (a.depths ? a.depths[t] : t - lo);
-        a.slots[t] = -1;
-        continue;
-      }
-    } else if (yes) {
-      b = t;
-      if (a.cu_q) {
-        b = 0;
-        for (int step = 1 << (31 - __clz(batch)); step > 0; step >>= 1)
-          if (b + step < batch && offset_at(a.cu_q, b + step, tokens) <= t) b += step;
-      }
-      const Request q = request_of(p, b, &bad);
-      token_range(a.cu_q, b, tokens, &lo, &hi, &bad);
-      len = q.len;
-      yes = t >= lo && t < hi;
-      if (yes && !served(q, b)) {
-        if (a.positions) a.positions[t] = a.first_position + len + (a.depths ? a.depths[t] : t - lo);
-        a.slots[t] = -1;
-        continue;
-      }
-    }
-    int64_t slot = -1, position = 0;
-    if (yes) {
-      const unsigned key = len + unsigned(t - lo);
-      const unsigned at = p.page_shift >= 0 ? key >> p.page_shift : key / unsigned(a.page_size);
-      const int page = at < unsigned(a.width) ? __ldcg(a.page_table + int64_t(b) * a.page_table_stride + at) : -1;
-      if (page >= 0)
-        slot = int64_t(page) * a.page_size + (key - at * unsigned(a.page_size));
-      else
-        bad = true;
-      position = a.first_position + len + (a.depths ? a.depths[t] : t - lo);
-    }
-    a.slots[t] = slot;
-    if (a.positions) a.positions[t] = position;
+    if (failed != kNone) atomicOr(&g_pages_flags, kFlagNoPages);
   }
   if (bad) atomicOr(&g_pages_flags, kFlagBadIndex);
 }
@@ -253,7 +280,7 @@ cudaError_t launch_kv_pages(const nf4_kv_pages_args& a, cudaStream_t stream) {
     if (a.page_size == int64_t(1) << s) p.page_shift = s;
   const unsigned threads = a.batch > 256 || a.tokens > 256 ? kMostThreads : 256;
   unsigned ctas = 1;
-  while (ctas < 8 && a.tokens > int64_t(ctas) * 2 * threads) ctas *= 2;
+  while (ctas < 8 && a.tokens > int64_t(ctas) * kRun * threads) ctas *= 2;
   return launch_cluster(kv_pages_kernel, ctas, dim3(ctas), dim3(threads), 0, stream, p);
 }
 
