@@ -171,14 +171,16 @@ def test_calls_without_work(lib):
     assert call(lib, "nf4_tree_commit", batch=0, tokens=0, parents=0) == OK
 
 
-def test_workspace_of_a_tree_is_that_of_its_attention(lib):
-    lib.nf4_prefix_attention_workspace_size.argtypes = [ctypes.c_void_p]
-    lib.nf4_prefix_attention_workspace_size.restype = ctypes.c_size_t
-    args = STRUCTS["nf4_tree_attention_args"](**GOOD["nf4_tree_attention_args"])
-    size = lib.nf4_tree_attention_workspace_size(ctypes.byref(args))
-    assert size > 0 and size == lib.nf4_prefix_attention_workspace_size(ctypes.byref(args))
-    args.tree_words = 0
-    assert lib.nf4_tree_attention_workspace_size(ctypes.byref(args)) == 0
+def test_workspace_of_a_tree(lib):
+    """Two numbers and a row in binary32 for each row and range of keys; nothing where one range writes the output."""
+    size = lambda **kw: lib.nf4_tree_attention_workspace_size(ctypes.byref(  # noqa: E731
+        STRUCTS["nf4_tree_attention_args"](**{**GOOD["nf4_tree_attention_args"], **kw})))
+    for kw in (dict(), dict(prefix_len=0, suffix_pages_width=4000, suffix_pages_stride=4000), dict(batch=1, tokens=200)):
+        t = {**GOOD["nf4_tree_attention_args"], **kw}
+        row = t["tokens"] * t["q_heads"] * (t["head_dim"] * 4 + 8)
+        assert size(**kw) > 0 and size(**kw) % row == 0 and size(**kw) // row <= 304, kw
+    assert size(tree_words=0) == size(tokens=0) == size(head_dim=4) == 0
+    assert size(prefix_len=0, suffix_pages_width=0) == 0
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="these calls would launch")

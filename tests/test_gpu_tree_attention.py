@@ -218,13 +218,15 @@ def test_rows_without_a_bit_see_nothing():
     (0, [5, 0, 1, 3], [5, 7, 1, 0]), (257, [130, 1, 0, 64], [130, 9, 4, 70]), (0, [200], [100]),
     (1000, [40] * 6, [40, 41, 60, 100, 39, 20]), (4000, [33, 300, 2], [33, 900, 1000])])
 def test_a_chain_is_causal(hq, hk, dim, prefix, counts, lens):
-    """Ones up to the own bit: the results of nf4_prefix_attention, also where there are fewer keys than tokens."""
+    """Ones up to the own bit: what nf4_prefix_attention gives, within its tolerance, also where there are fewer keys
+    than tokens."""
     c = Call(hq, hk, dim, prefix, lens, counts, seen=[set(range(i + 1)) for n in counts for i in range(n)], seed=prefix)
-    out, lse = c.run()
-    want, want_lse = lib().nf4_prefix_attention(c.q, c.k, c.v, c.prefix_pages, prefix, c.suffix_pages, c.suffix_lens,
-                                                cu_q=c.cu_q, scale=c.scale, return_lse=True)
-    assert torch.equal(out, want) and torch.equal(lse, want_lse)
-    c.check((out, lse))
+    got = c.run()
+    c.check(got, "tree")
+    want = lib().nf4_prefix_attention(c.q, c.k, c.v, c.prefix_pages, prefix, c.suffix_pages, c.suffix_lens, cu_q=c.cu_q,
+                                      scale=c.scale, return_lse=True)
+    c.check(want, "causal")
+    assert torch.equal(got[1] == float("-inf"), want[1] == float("-inf"))
 
 
 def test_one_token_each_without_offsets():

@@ -23,7 +23,7 @@ cudaError_t launch_rope_table(const nf4_rope_table_args& a, cudaStream_t stream)
 // its slots.
 cudaError_t launch_qk_rope(const nf4_qk_norm_rope_args& a, const nf4_kv_append_args* cache,
                            cudaStream_t stream);
-size_t prefix_attention_workspace_bytes(const nf4_prefix_attention_args& a);
+size_t prefix_attention_workspace_bytes(const nf4_prefix_attention_args& a, bool tree);
 // *enough is false, and nothing was launched, where the workspace does not do.
 // `tree`: null, or the call whose attention member `a` is.
 cudaError_t launch_prefix_attention(const nf4_prefix_attention_args& a, const nf4_tree_attention_args* tree,

@@ -142,7 +142,7 @@ nf4_status nf4_kv_append(const nf4_kv_append_args* args, nf4_stream_t stream) {
 
 size_t nf4_prefix_attention_workspace_size(const nf4_prefix_attention_args* args) {
   if (!args || nf4::check_attention_sizes(*args) != NF4_OK || args->tokens == 0) return 0;
-  return nf4::prefix_attention_workspace_bytes(*args);
+  return nf4::prefix_attention_workspace_bytes(*args, false);
 }
 
 nf4_status nf4_prefix_attention(const nf4_prefix_attention_args* args, void* workspace, size_t workspace_bytes,

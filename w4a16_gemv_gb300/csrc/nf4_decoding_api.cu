@@ -54,7 +54,7 @@ nf4_status nf4_kv_pages(const nf4_kv_pages_args* args, nf4_stream_t stream) {
 
 size_t nf4_tree_attention_workspace_size(const nf4_tree_attention_args* args) {
   if (!args || check_tree(*args) != NF4_OK || args->attention.tokens == 0) return 0;
-  return nf4::prefix_attention_workspace_bytes(args->attention);
+  return nf4::prefix_attention_workspace_bytes(args->attention, true);
 }
 
 nf4_status nf4_tree_attention(const nf4_tree_attention_args* args, void* workspace, size_t workspace_bytes,

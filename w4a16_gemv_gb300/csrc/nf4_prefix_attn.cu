@@ -785,11 +785,89 @@ int sms_for_own(const PrefixArgs& p, int64_t own_items, int64_t tiles, int64_t p
   return keep < kSms / 8 && ctas > kSms - int64_t(keep) ? int(keep) : 0;
 }
 
+// Trees (many short runs of rows, each over keys of its own): which kernel, and how
+// long the ranges. A model of three plans, in microseconds, of which the least is
+// taken; "units" are 64 keys of a tile of 64 rows, "tiles" whole key tiles of 256.
+//   * everything on 64-row tiles in one launch: 7 + 2.4 per unit and SM's two CTAs.
+//     2 trees of 8 over 300 + 60 keys (12 heads over 2): 10.4 us, 16 on two kernels;
+//   * everything on the tcgen05 kernel in one launch: 6.5 + 1.5 per tile (2 with more
+//     than 128 rows) and SM, and 3.5 tiles of start and end per item. One tree of 25
+//     over 50000 keys of 32 heads: 137 us, 213 on 16-row tiles; 37 trees of up to 13
+//     over 777 + 500 keys in pages of 24: 19.6, 22 on 64-row tiles;
+//   * up to 16 rows of a sequence: own keys on 16-row tiles, at about 5.5 TB/s (up to
+//     32, at 4.2), and shared ones on the tcgen05 kernel beside them: 8 sequences x 32
+//     heads x 16 nodes over 500 + 300 keys 18.4 us, 22.7 on 64-row tiles.
+// Over 64 shapes drawn at random the plan's time is 1.5% above the best of all plans
+// and ranges tried for each.
+// Sequences hold some 80% of the longest one's keys on average.
+struct TreePlan {
+  int prefix_rows, suffix_rows;
+  int64_t per;  // keys of a range, in half key tiles (tcgen05) or units (64 rows); 0: as for other calls
+};
+TreePlan plan_tree(const nf4_prefix_attention_args& a, int64_t suffix_max, int64_t tile_keys) {
+  const double kFull = 0.8, kStart = 3.5;
+  const double heads = double(a.k_heads);
+  const int64_t group = a.q_heads / a.k_heads, rows = a.tokens * group;
+  const int64_t each = a.batch > 0 ? (rows + a.batch - 1) / a.batch : 0;  // of a sequence
+  auto tiles = [](int64_t n, int64_t of) { return (n + of - 1) / of; };
+  // 64 rows
+  const double own_units = double(a.batch * tiles(each, 64) * tiles(suffix_max, kUnit)) * heads;
+  const double shared_units = double(tiles(rows, 64) * tiles(a.prefix_len, kUnit)) * heads;
+  const double est64 = 7.0 + 2.4 * (own_units * kFull + shared_units) / double(2 * kSms);
+  // 256 rows
+  const double own_items = double(a.batch * tiles(each, 256)) * heads, shared_items = double(tiles(rows, 256)) * heads;
+  const int64_t own_tiles = tiles(suffix_max, tile_keys), shared_tiles = tiles(a.prefix_len, tile_keys);
+  const double own_time = each > 128 ? 2.0 : 1.5, shared_time = rows > 128 ? 2.0 : 1.5;
+  const double own_work = own_items * double(own_tiles) * kFull, shared_work = shared_items * double(shared_tiles);
+  const double least = (own_tiles > 0 ? own_items : 0.0) + (shared_tiles > 0 ? shared_items : 0.0);
+  const double est256 = 6.5 + (own_work * own_time + shared_work * shared_time +
+                               1.5 * kStart * (least > kSms ? least : double(kSms))) / kSms;
+  TreePlan plan = {256, 256, 0};
+  if (each <= 32) {
+    const double bytes = double(a.batch * suffix_max) * heads * double(a.head_dim) * 4.0 * kFull;
+    const double est16 = (a.prefix_len > 0 ? 10.0 : 8.0) + bytes / (each <= 16 ? 5.5e6 : 4.2e6) +
+                         (a.prefix_len > 0 ? (shared_work * shared_time + 1.5 * kStart * shared_items) / kSms : 0.0);
+    if (est16 < est64 && est16 < est256) {
+      plan.prefix_rows = rows > 16 || a.prefix_len > 1024 ? 256 : 16;
+      plan.suffix_rows = 16;
+      return plan;
+    }
+  }
+  if (est64 < est256) {
+    // as many items as there are places, of one unit or more; longer ones in about four rounds
+    const int64_t units = int64_t(own_units + shared_units), whole = tiles(units, 2 * kSms), four = units / (4 * kSms);
+    plan.prefix_rows = plan.suffix_rows = 64;
+    plan.per = whole <= 6 ? whole : four < 6 ? 6 : four;
+    return plan;
+  }
+  // The ranges that end soonest: shared items, all alike, in rounds, and own ones, which are not, where these leave
+  // SMs free and behind them.
+  double best = 0.0;
+  const int64_t longest = own_tiles > shared_tiles ? own_tiles : shared_tiles;
+  for (int64_t parts = 1; parts <= kMaxRanges && parts <= longest; parts += parts / 8 + 1) {
+    const int64_t per = tiles(longest, parts);
+    const int64_t s = tiles(shared_tiles, per), o = tiles(own_tiles, per);
+    const double shared_all = shared_items * double(s), own_all = own_items * double(o);
+    const double item = double(per) + kStart, own_total = own_work + kStart * own_all;
+    const double whole = double(int64_t(shared_all) / kSms), rest = shared_all - whole * kSms;
+    const double room = rest > 0.0 ? (kSms - rest) * item : 0.0;
+    double time = (whole + (rest > 0.0 ? 1.0 : 0.0)) * item;
+    if (own_total > room)
+      time += own_all + rest <= kSms ? (rest > 0.0 ? 0.0 : item) : (own_total - room) / kSms + 0.5 * item;
+    const double cost = time + double(s + o) * double(rows) * heads * 1e-4;
+    if (parts == 1 || cost < best) {
+      best = cost;
+      plan.per = 2 * per;
+    }
+  }
+  return plan;
+}
+
 }  // namespace
 
 // Rows per tile, and the ranges of keys. Everything follows from the sizes
 // that the host knows (never from lengths on the device).
-void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, size_t* bytes) {
+void plan_prefix_attention(const nf4_prefix_attention_args& a, bool tree, PrefixArgs* p, size_t* bytes) {
   p->batch = int(a.batch);
   p->tokens = int(a.tokens);
   p->q_heads = int(a.q_heads);
@@ -805,6 +883,12 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
   // rows, the call is one launch fewer with everything on the other kernel.
   p->prefix_rows = rows > 16 || p->prefix_len > 1024 ? 256 : 16;
   p->suffix_rows = rows > 64 * a.batch ? 256 : rows > 32 * a.batch ? 64 : 16;
+  TreePlan plan = {};
+  if (tree) {
+    plan = plan_tree(a, p->suffix_max, prefix_tile_keys(a.page_size));
+    p->prefix_rows = plan.prefix_rows;
+    p->suffix_rows = plan.suffix_rows;
+  }
   p->prefix_tiles = int((rows + p->prefix_rows - 1) / p->prefix_rows);
   // the two ways of first_tile()
   const int64_t whole = rows / p->suffix_rows + a.batch;
@@ -821,8 +905,15 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
     const int64_t most = kMostKeys / (2 * unit) * 2;
     return per < most ? per : most;
   };
+  // a tree's ranges, whole ones of these units
+  auto planned = [&](int64_t units, int64_t unit, int tile_rows) {
+    const int64_t least = (units + kMaxRanges - 1) / kMaxRanges, even = tile_rows == 256 ? 2 : 1;
+    const int64_t per = plan.per > least ? plan.per : least;
+    return bounded((per + even - 1) / even * even, unit);
+  };
   if (sk > 0) {
     const int64_t per =
+        plan.per > 0 ? planned(sk, su, p->suffix_rows) :
         bounded(p->suffix_rows == 256 ? tc_range(likely * p->k_heads, (sk + 1) / 2, rows * p->k_heads, kSms)
                                       : mma_range(likely * p->k_heads, sk, p->dim),
                 su);
@@ -832,7 +923,9 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
   if (pk > 0) {
     const int64_t tiles = int64_t(p->prefix_tiles) * p->k_heads;
     int64_t per;
-    if (p->prefix_rows != 256) {
+    if (plan.per > 0) {
+      per = planned(pk, pu, p->prefix_rows);  // (no fused items: trees bring few rows)
+    } else if (p->prefix_rows != 256) {
       per = mma_range(tiles, pk, p->dim);  // (at most 1024 keys)
     } else {
       const int64_t longest = (pk + 1) / 2;
@@ -844,7 +937,7 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
       // few-row kernel, whose items would hold their SMs waiting for the shared part:
       // 64 sequences x 32 heads over 2048 + 190 took 56 us instead of 49; nor with two
       // ranges and more to read back: 16 prompts of 100 35 instead of 29.
-      p->fused = p->suffix_splits == 1 && p->suffix_rows == 256 && pk <= per;
+      p->fused = !tree && p->suffix_splits == 1 && p->suffix_rows == 256 && pk <= per;
       if (!p->fused && p->suffix_rows != 256 && sk > 0) {
         per = beside_range(a, *p, tiles, longest, rows, per);
         const int keep = sms_for_own(*p, likely * p->k_heads * p->suffix_splits, tiles, per, pk);
@@ -868,10 +961,10 @@ void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, si
   *bytes = p->splits > 0 && !p->direct ? size_t(all) * size_t(p->splits) * (size_t(a.head_dim) * 4 + 8) : 0;
 }
 
-size_t prefix_attention_workspace_bytes(const nf4_prefix_attention_args& a) {
+size_t prefix_attention_workspace_bytes(const nf4_prefix_attention_args& a, bool tree) {
   PrefixArgs p = {};
   size_t bytes = 0;
-  plan_prefix_attention(a, &p, &bytes);
+  plan_prefix_attention(a, tree, &p, &bytes);
   return bytes;
 }
 
@@ -879,7 +972,7 @@ cudaError_t launch_prefix_attention(const nf4_prefix_attention_args& a, const nf
                                     void* workspace, size_t workspace_bytes, bool* enough, cudaStream_t stream) {
   PrefixArgs p = {};
   size_t bytes = 0;
-  plan_prefix_attention(a, &p, &bytes);
+  plan_prefix_attention(a, tree != nullptr, &p, &bytes);
   *enough =
       bytes == 0 || (workspace && workspace_bytes >= bytes && (reinterpret_cast<uintptr_t>(workspace) & 15u) == 0);
   if (!*enough) return cudaSuccess;

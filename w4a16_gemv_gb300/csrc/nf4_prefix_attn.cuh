@@ -61,8 +61,8 @@ inline int prefix_tile_keys(int64_t page_size) {
   return page_size > 8 && keys >= 112 ? keys : 128;
 }
 
-// The sizes and the plan of a call, and the bytes of its workspace.
-void plan_prefix_attention(const nf4_prefix_attention_args& a, PrefixArgs* p, size_t* bytes);
+// The sizes and the plan of a call (`tree`: of a tree's), and the bytes of its workspace.
+void plan_prefix_attention(const nf4_prefix_attention_args& a, bool tree, PrefixArgs* p, size_t* bytes);
 
 // Items [p.first, p.first + items), tiles of 256 rows, on the tensor cores
 // (nf4_prefix_attn_tc.cu); `tree`: some of them are own keys of trees.
