@@ -792,8 +792,8 @@ int sms_for_own(const PrefixArgs& p, int64_t own_items, int64_t tiles, int64_t p
 //     2 trees of 8 over 300 + 60 keys (12 heads over 2): 10.4 us, 16 on two kernels;
 //   * everything on the tcgen05 kernel in one launch: 6.5 + 1.5 per tile (2 with more
 //     than 128 rows) and SM, and 3.5 tiles of start and end per item. One tree of 25
-//     over 50000 keys of 32 heads: 137 us, 213 on 16-row tiles; 37 trees of up to 13
-//     over 777 + 500 keys in pages of 24: 19.6, 22 on 64-row tiles;
+//     over 50000 keys of 32 heads: 133 us, 213 on 16-row tiles; 37 trees of up to 13
+//     over 777 + 500 keys in pages of 24: 17.3, 22 on 64-row tiles;
 //   * up to 16 rows of a sequence: own keys on 16-row tiles, at about 5.5 TB/s (up to
 //     32, at 4.2), and shared ones on the tcgen05 kernel beside them: 8 sequences x 32
 //     heads x 16 nodes over 500 + 300 keys 18.4 us, 22.7 on 64-row tiles.
@@ -840,20 +840,26 @@ TreePlan plan_tree(const nf4_prefix_attention_args& a, int64_t suffix_max, int64
     plan.per = whole <= 6 ? whole : four < 6 ? 6 : four;
     return plan;
   }
-  // The ranges that end soonest: shared items, all alike, in rounds, and own ones, which are not, where these leave
-  // SMs free and behind them.
+  // The ranges that end soonest: shared items, all alike, in rounds (an item's start and end are 5.5 tiles of an SM's
+  // time there: 16 sequences and heads over 47458 keys take 77 us in 9 ranges, one round, 111 in 10), and own ones
+  // where these leave SMs free and behind them, half as if they were alike and half as if uneven ones filled the SMs.
+  const double kItem = 5.5;
   double best = 0.0;
   const int64_t longest = own_tiles > shared_tiles ? own_tiles : shared_tiles;
-  for (int64_t parts = 1; parts <= kMaxRanges && parts <= longest; parts += parts / 8 + 1) {
+  for (int64_t parts = 1; parts <= kMaxRanges && parts <= longest; parts += parts / 16 + 1) {
     const int64_t per = tiles(longest, parts);
     const int64_t s = tiles(shared_tiles, per), o = tiles(own_tiles, per);
     const double shared_all = shared_items * double(s), own_all = own_items * double(o);
-    const double item = double(per) + kStart, own_total = own_work + kStart * own_all;
+    const double item = double(per) + kItem, own_item = double(per < own_tiles ? per : own_tiles) + kItem;
+    const double own_total = own_work + kItem * own_all;
     const double whole = double(int64_t(shared_all) / kSms), rest = shared_all - whole * kSms;
-    const double room = rest > 0.0 ? (kSms - rest) * item : 0.0;
     double time = (whole + (rest > 0.0 ? 1.0 : 0.0)) * item;
-    if (own_total > room)
-      time += own_all + rest <= kSms ? (rest > 0.0 ? 0.0 : item) : (own_total - room) / kSms + 0.5 * item;
+    const double more = own_total - (rest > 0.0 ? (kSms - rest) * item : 0.0);
+    if (rest > 0.0 && more > 0.0)
+      time += more / kSms + 0.75 * own_item;
+    else if (rest == 0.0 && own_all > 0.0)
+      time += own_all <= kSms ? own_item
+                              : 0.5 * (double((int64_t(own_all) + kSms - 1) / kSms) * own_item + more / kSms + 0.5 * own_item);
     const double cost = time + double(s + o) * double(rows) * heads * 1e-4;
     if (parts == 1 || cost < best) {
       best = cost;
