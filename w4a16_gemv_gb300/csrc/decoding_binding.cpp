@@ -13,13 +13,48 @@ const at::Tensor& shaped(PyObject* o, const char* name, int64_t dims, const char
   return t;
 }
 
-// An output: the given tensor, or a new one.
-at::Tensor output(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape, const Launch& on) {
-  if (!given(o)) return on.empty(shape, type);
-  const at::Tensor& t = tensor(o, name);
-  check(t, name, type, shape, on.device(), true);
-  return t;
-}
+// Outputs: the given tensors, or new ones; those of one type share an allocation (one takes 0.8 us, a call of four
+// or five small outputs 7 to 8). Two passes: add() for each, then get() in the same order.
+class Outputs {
+ public:
+  explicit Outputs(const Launch& on) : on_(on) {}
+  void add(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape) {
+    Part& p = parts_[n_++];
+    p.type = type;
+    for (const int64_t s : shape) p.shape[p.dims++] = s;
+    if (given(o)) {
+      p.given = tensor(o, name);
+      check(p.given, name, type, shape, on_.device(), true);
+    } else {
+      p.at = total_[type == at::kLong];
+      total_[type == at::kLong] += p.numel();
+    }
+  }
+  at::Tensor get() {
+    Part& p = parts_[next_++];
+    if (p.given.defined()) return p.given;
+    at::Tensor& whole = whole_[p.type == at::kLong];
+    if (!whole.defined()) whole = on_.empty({total_[p.type == at::kLong]}, p.type);
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(at::IntArrayRef(p.shape, size_t(p.dims)));
+    t.unsafeGetTensorImpl()->set_storage_offset(p.at);
+    return t;
+  }
+
+ private:
+  struct Part {
+    at::ScalarType type = at::kInt;
+    int64_t shape[2] = {0, 0}, at = 0;
+    int dims = 0;
+    at::Tensor given;
+    int64_t numel() const { return shape[0] * (dims > 1 ? shape[1] : 1); }
+  };
+  const Launch& on_;
+  Part parts_[5];
+  int n_ = 0, next_ = 0;
+  int64_t total_[2] = {0, 0};
+  at::Tensor whole_[2];
+};
 PyObject* result(PyObject* given_one, const at::Tensor& made) {
   return given(given_one) ? Py_NewRef(given_one) : THPVariable_Wrap(made);
 }
@@ -86,11 +121,14 @@ PyObject* py_kv_pages(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObje
     a.free_count = static_cast<const int32_t*>(flat(v[4], "free_count", at::kInt, {1}, dev));
     if (given(v[6])) a.cu_q = static_cast<const int32_t*>(flat(v[6], "cu_q", at::kInt, {a.batch + 1}, dev));
     if (given(v[8])) a.depths = static_cast<const int32_t*>(flat(v[8], "depths", at::kInt, {a.tokens}, dev));
-    const at::Tensor slots = output(v[10], "slots", at::kLong, {a.tokens}, on);
-    const at::Tensor positions = output(v[11], "positions", at::kLong, {a.tokens}, on);
-    const at::Tensor new_lens = output(v[12], "new_lens", at::kInt, {a.batch}, on);
-    const at::Tensor new_held = output(v[13], "new_held", at::kInt, {a.batch}, on);
-    const at::Tensor left = output(v[14], "new_free_count", at::kInt, {1}, on);
+    Outputs outputs(on);
+    outputs.add(v[10], "slots", at::kLong, {a.tokens});
+    outputs.add(v[11], "positions", at::kLong, {a.tokens});
+    outputs.add(v[12], "new_lens", at::kInt, {a.batch});
+    outputs.add(v[13], "new_held", at::kInt, {a.batch});
+    outputs.add(v[14], "new_free_count", at::kInt, {1});
+    const at::Tensor slots = outputs.get(), positions = outputs.get(), new_lens = outputs.get(), new_held = outputs.get(),
+                     left = outputs.get();
     a.slots = static_cast<int64_t*>(slots.data_ptr());
     a.positions = static_cast<int64_t*>(positions.data_ptr());
     a.new_lens = static_cast<int32_t*>(new_lens.data_ptr());
@@ -221,7 +259,9 @@ PyObject* py_adjust_logits(PyObject*, PyObject* const* args, Py_ssize_t nargs, P
     a.out_stride = out.stride(0);
     const bool want = truth(v[15]);
     if (want || given(v[16])) {
-      best = output(v[16], "best", at::kInt, {a.rows}, on);
+      Outputs outputs(on);
+      outputs.add(v[16], "best", at::kInt, {a.rows});
+      best = outputs.get();
       a.best = static_cast<int32_t*>(best.data_ptr());
     }
     const nf4_status st = unlocked([&] { return nf4_adjust_logits(&a, on.stream()); });
@@ -283,10 +323,12 @@ PyObject* py_tree_commit(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyO
       a.page_table_stride = table.stride(0);
       a.width = table.size(1);
     }
-    const at::Tensor accepted = output(v[9], "accepted", at::kInt, {a.batch}, on);
-    const at::Tensor path = output(v[10], "path", at::kInt, {a.batch, a.max_path}, on);
-    const at::Tensor chosen = output(v[11], "chosen", at::kInt, {a.batch, a.max_path}, on);
-    const at::Tensor new_lens = output(v[12], "new_lens", at::kInt, {a.batch}, on);
+    Outputs outputs(on);
+    outputs.add(v[9], "accepted", at::kInt, {a.batch});
+    outputs.add(v[10], "path", at::kInt, {a.batch, a.max_path});
+    outputs.add(v[11], "chosen", at::kInt, {a.batch, a.max_path});
+    outputs.add(v[12], "new_lens", at::kInt, {a.batch});
+    const at::Tensor accepted = outputs.get(), path = outputs.get(), chosen = outputs.get(), new_lens = outputs.get();
     a.accepted = static_cast<int32_t*>(accepted.data_ptr());
     a.path = static_cast<int32_t*>(path.data_ptr());
     a.chosen = static_cast<int32_t*>(chosen.data_ptr());

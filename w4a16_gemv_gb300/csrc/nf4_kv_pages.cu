@@ -12,9 +12,11 @@
 // is looked up where it comes from (its row of the table, or the stack), not in
 // the table after it has been written, so that both go on at once; a barrier of the
 // cluster stands only where pages come back before any are taken, and in front of
-// the results that may be the same arrays as inputs. (Batches of more requests than
-// a CTA has threads go by chunks, and their tokens wait for the tables.) Latency
-// bounds it: a chain of loads, sums, loads and stores.
+// the results that may be the same arrays as inputs. Where there are many tokens,
+// or more requests than a CTA has threads, a second launch lays them out on all SMs,
+// from the tables as they are then (256 prompts, 115000 tokens: 8.0 us; by one
+// cluster of eight CTAs 19).
+// Latency bounds both: a chain of loads, sums, loads and stores.
 #include "nf4_decoding.cuh"
 
 namespace nf4 {
@@ -24,10 +26,12 @@ __device__ unsigned int g_pages_flags = 0;
 
 constexpr int kMostThreads = 1024;
 constexpr int kNone = 0x7fffffff;
+constexpr int kApart = 4096;  // more tokens than this have a launch of their own
 
 struct PagesArgs {
   nf4_kv_pages_args a;
   int page_shift;  // log2 of page_size, or -1
+  int apart;       // 1: the tokens have a launch of their own
 };
 
 // One request: L cached keys, n new tokens, h pages held, `need` needed.
@@ -92,7 +96,17 @@ __device__ __forceinline__ int last_at_most(const V* list, int n, V v) {
   return at;
 }
 
-constexpr int kRun = 4;  // tokens of a thread, one after another, where there are more tokens than threads
+// Where token t, the i-th of a request with len keys, goes.
+__device__ __forceinline__ int64_t position_of(const PagesArgs& p, int t, unsigned len, int i) {
+  return p.a.first_position + len + (p.a.depths ? p.a.depths[t] : i);
+}
+__device__ __forceinline__ unsigned page_number(const PagesArgs& p, unsigned key) {
+  return p.page_shift >= 0 ? key >> p.page_shift : key / unsigned(p.a.page_size);
+}
+__device__ __forceinline__ int64_t slot_of(const PagesArgs& p, int page, unsigned key, unsigned at, bool* bad) {
+  *bad = *bad || page < 0;
+  return page < 0 ? -1 : int64_t(page) * p.a.page_size + (key - at * unsigned(p.a.page_size));
+}
 
 __global__ void __launch_bounds__(kMostThreads, 1) kv_pages_kernel(const __grid_constant__ PagesArgs p) {
   const nf4_kv_pages_args& a = p.a;
@@ -184,74 +198,25 @@ __global__ void __launch_bounds__(kMostThreads, 1) kv_pages_kernel(const __grid_
     if (failed != kNone) break;
   }
   auto served = [&](const Request& q, int b) { return !q.wide && (q.need <= q.held || b < failed); };
-  if (!one_chunk) cluster_barrier();  // tables are whole
 
-  // The tokens, kRun at a time.
-  const bool vectors = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
-  const int run = tokens > shares ? kRun : 1;
-  for (int t0 = share * run; t0 < tokens; t0 += shares * run) {
-    int64_t slot[kRun], position[kRun];
-    int b = 0, lo = 0, hi = 0;   // the last token's request
-    unsigned len = 0, limit = 0; // its length, and the pages that its row has now (0: not served)
-    int at_page = -1, page = -1;
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      const int t = t0 + i;
-      slot[i] = -1;
-      position[i] = 0;
-      if (i >= run || t >= tokens || batch == 0) continue;
-      if (t >= hi) {
-        if (one_chunk) {
-          b = a.cu_q ? last_at_most(s_cu, batch, t) : t;
-          lo = s_cu[b];
-          hi = a.cu_q ? s_cu[b + 1] : t + 1;
-          len = s_len[b];
-          const unsigned need = pages_of(p, len + unsigned(max(hi - lo, 0)));
-          limit = need <= unsigned(a.width) && (need <= first[b] || b < failed) ? need : 0u;
-        } else {
-          b = t;
-          if (a.cu_q) {
-            b = 0;
-            for (int step = 1 << (31 - __clz(batch)); step > 0; step >>= 1)
-              if (b + step < batch && offset_at(a.cu_q, b + step, tokens) <= t) b += step;
-          }
-          const Request q = request_of(p, b, &bad);
-          token_range(a.cu_q, b, tokens, &lo, &hi, &bad);
-          len = q.len;
-          limit = served(q, b) ? q.need : 0u;
-        }
-        at_page = -1;
-        if (t < lo || t >= hi) {  // no request holds it
-          hi = t;
-          continue;
-        }
+  // The tokens, of a batch of one chunk.
+  if (!p.apart) {
+#pragma unroll 1
+    for (int t = share; t < tokens; t += shares) {
+      int64_t slot = -1, position = 0;
+      const int b = batch == 0 ? -1 : a.cu_q ? last_at_most(s_cu, batch, t) : t;
+      const int lo = b < 0 ? 0 : s_cu[b], hi = b < 0 ? 0 : a.cu_q ? s_cu[b + 1] : t + 1;
+      if (t >= lo && t < hi) {
+        const unsigned len = s_len[b], held = first[b], need = pages_of(p, len + unsigned(hi - lo));
+        const unsigned key = len + unsigned(t - lo), at = page_number(p, key);
+        position = position_of(p, t, len, t - lo);
+        if (need <= unsigned(a.width) && (need <= held || b < failed))
+          slot = slot_of(p, __ldcg(at < held ? a.page_table + int64_t(b) * a.page_table_stride + at
+                                             : a.free_pages + (uint64_t(top) - 1 - start[b] - (at - held))),
+                         key, at, &bad);
       }
-      position[i] = a.first_position + len + (a.depths ? a.depths[t] : t - lo);
-      if (limit == 0) continue;
-      const unsigned key = len + unsigned(t - lo);
-      const int at = int(p.page_shift >= 0 ? key >> p.page_shift : key / unsigned(a.page_size));
-      if (at != at_page) {
-        page = one_chunk && unsigned(at) >= first[b]
-                   ? __ldcg(a.free_pages + (uint64_t(top) - 1 - start[b] - (unsigned(at) - first[b])))
-                   : __ldcg(a.page_table + int64_t(b) * a.page_table_stride + at);
-        at_page = at;
-        bad = bad || page < 0;
-      }
-      if (page >= 0) slot[i] = int64_t(page) * a.page_size + (key - unsigned(at) * unsigned(a.page_size));
-    }
-    if (vectors && run == kRun && t0 + kRun <= tokens) {
-#pragma unroll
-      for (int i = 0; i < kRun; i += 2) {
-        *reinterpret_cast<longlong2*>(a.slots + t0 + i) = make_longlong2(slot[i], slot[i + 1]);
-        if (a.positions)
-          *reinterpret_cast<longlong2*>(a.positions + t0 + i) = make_longlong2(position[i], position[i + 1]);
-      }
-    } else {
-      for (int i = 0; i < kRun; ++i)
-        if (i < run && t0 + i < tokens) {
-          a.slots[t0 + i] = slot[i];
-          if (a.positions) a.positions[t0 + i] = position[i];
-        }
+      a.slots[t] = slot;
+      if (a.positions) a.positions[t] = position;
     }
   }
 
@@ -270,6 +235,45 @@ __global__ void __launch_bounds__(kMostThreads, 1) kv_pages_kernel(const __grid_
   if (bad) atomicOr(&g_pages_flags, kFlagBadIndex);
 }
 
+// The tokens, from the tables, held pages and lengths that the launch before has written: a request whose pages
+// are all there was served. Whole warps find the request of their first token, the lanes go on from there.
+__global__ void __launch_bounds__(256) kv_slots_kernel(const __grid_constant__ PagesArgs p) {
+  const nf4_kv_pages_args& a = p.a;
+  pdl_wait_prior_grid();
+  pdl_allow_dependents();
+  const int tokens = int(a.tokens), batch = int(a.batch), t = int(blockIdx.x) * 256 + int(threadIdx.x);
+  bool bad = false;
+  int b = batch > 0 ? entry_of(a.cu_q, batch, tokens, t & ~31) : -1;
+  if (t >= tokens) return;
+  int64_t slot = -1, position = 0;
+  if (b >= 0) {
+    if (!a.cu_q) {
+      b = t;
+    } else {
+      int steps = 0;
+      while (b + 1 < batch && steps < 32 && offset_at(a.cu_q, b + 1, tokens) <= t) {
+        ++b;
+        ++steps;
+      }
+      for (int step = steps < 32 ? 0 : 1 << (31 - __clz(batch)); step > 0; step >>= 1)  // many empty requests
+        if (b + step < batch && offset_at(a.cu_q, b + step, tokens) <= t) b += step;
+    }
+    int lo, hi;
+    bool ignored = false;  // (reported by the launch before)
+    token_range(a.cu_q, b, tokens, &lo, &hi, &ignored);
+    if (t >= lo && t < hi) {
+      const unsigned len = unsigned(max(a.lens[b], 0)), need = pages_of(p, len + unsigned(hi - lo));
+      const unsigned key = len + unsigned(t - lo), at = page_number(p, key);
+      position = position_of(p, t, len, t - lo);
+      if (need <= unsigned(a.width) && need <= unsigned(max(a.new_held[b], 0)))
+        slot = slot_of(p, a.page_table[int64_t(b) * a.page_table_stride + at], key, at, &bad);
+    }
+  }
+  a.slots[t] = slot;
+  if (a.positions) a.positions[t] = position;
+  if (bad) atomicOr(&g_pages_flags, kFlagBadIndex);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_pages(const nf4_kv_pages_args& a, cudaStream_t stream) {
@@ -279,9 +283,12 @@ cudaError_t launch_kv_pages(const nf4_kv_pages_args& a, cudaStream_t stream) {
   for (int s = 0; s <= 16; ++s)
     if (a.page_size == int64_t(1) << s) p.page_shift = s;
   const unsigned threads = a.batch > 256 || a.tokens > 256 ? kMostThreads : 256;
+  p.apart = a.tokens > kApart || (a.batch > kMostThreads && a.tokens > 0);
   unsigned ctas = 1;
-  while (ctas < 8 && a.tokens > int64_t(ctas) * kRun * threads) ctas *= 2;
-  return launch_cluster(kv_pages_kernel, ctas, dim3(ctas), dim3(threads), 0, stream, p);
+  while (ctas < 4 && (p.apart || a.tokens > int64_t(ctas) * threads)) ctas *= 2;
+  const cudaError_t e = launch_cluster(kv_pages_kernel, ctas, dim3(ctas), dim3(threads), 0, stream, p);
+  if (e != cudaSuccess || !p.apart) return e;
+  return launch_k(kv_slots_kernel, dim3(unsigned((a.tokens + 255) / 256)), dim3(256), 0, stream, p);
 }
 
 cudaError_t pages_flags(unsigned int** word) {
