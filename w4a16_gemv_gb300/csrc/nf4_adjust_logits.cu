@@ -3,12 +3,12 @@
 //
 // A cluster of CTAs takes a run of rows, each CTA every eighth (fourth, second) block
 // of 256 tokens: frequent tokens often have low numbers, and in one piece the first
-// eighth of a vocabulary would be most of the work. What a request's history, its
+// part of a vocabulary would be most of the work. What a request's history, its
 // bias list and a row's branch of the tree say about a token is one word in the
 // shared memory of the token's CTA (how often it stands in the answer, whether it is
 // known at all, whether it has a bias) and one bit that says that there is a word.
 // These are made once per request and run of rows, by every CTA from the whole history
-// (a warp picks what is in its CTA, about one in eight, and counts that 32 at a time.
+// (a warp picks what is in its CTA, about one in four, and counts that 32 at a time.
 // Sharing the history among the CTAs and adding to one another's shared memory took
 // longer: an SM does a remote addition every seven cycles).
 // From one row to the next only the branch changes. Then each CTA streams its tokens, 16 bytes at a time, with the
@@ -16,7 +16,10 @@
 // each: a few in a hundred, and done where they lie every warp would go through the
 // division and the bias list for each of its chunks.
 // The logits are read and written once: memory bounds many rows, a chain of loads
-// (offsets, lengths, history) a few.
+// (offsets, lengths, history) a few. Without a context 64 rows of 128000 in bf16 take
+// 5.7 us and 384 in binary32 65 (5.9 and 6.0 TB/s); with masks, best tokens and 8000 (3000)
+// words of history each 24 and 109, bound by instructions (a quarter of them picks
+// words) and by the latencies between a row's stream and its listed tokens.
 #include "nf4_decoding.cuh"
 #include "nf4_prefix_attn.cuh"  // 16-byte asynchronous copies
 
@@ -25,11 +28,11 @@ namespace {
 
 __device__ unsigned int g_logits_flags = 0;
 
-constexpr int kThreads = 256;
-constexpr int kResident = 4;  // CTAs on an SM: 64 registers a thread
+constexpr int kThreads = 512;
+constexpr int kResident = 2;  // CTAs on an SM: 64 registers a thread
 constexpr int kMostRows = 64; // of a cluster
 constexpr int kBlock = 256;   // tokens that lie in one CTA
-constexpr int kList = 4096;   // listed tokens of a slice; where there are more, every word is looked at
+constexpr int kList = 8192;   // listed tokens of a slice; where there are more, every word is looked at
 
 constexpr int kSteps = 2;     // pieces of the history, of 128 words, that a warp has under way,
 constexpr int kQueue = 256;   // and words that it has picked: together where the list will be
@@ -366,8 +369,10 @@ __global__ void __launch_bounds__(kThreads, kResident) adjust_logits_kernel(cons
       if (build) {
         __syncthreads();
         // The list: counted first, so that a warp takes its part at once.
+        // (By bytes, so that the bits of frequent tokens, which lie side by side, are many lanes' work.)
+        const uint8_t* const eight = reinterpret_cast<const uint8_t*>(bits);
         int mine = 0;
-        for (int i = tid; i < p.slice / 32; i += kThreads) mine += __popc(bits[i]);
+        for (int i = tid; i < p.slice / 8; i += kThreads) mine += __popc(eight[i]);
         int to = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -377,9 +382,9 @@ __global__ void __launch_bounds__(kThreads, kResident) adjust_logits_kernel(cons
         int start = 0;
         if ((tid & 31) == 31) start = atomicAdd(&s_listed, to);
         to += __shfl_sync(0xffffffffu, start, 31) - mine;
-        for (int i = tid; i < p.slice / 32; i += kThreads)
-          for (uint32_t m = bits[i]; m; m &= m - 1, ++to)
-            if (to < kList) s_list[to] = uint32_t(i * 32 + __ffs(int(m)) - 1);
+        for (int i = tid; i < p.slice / 8; i += kThreads)
+          for (unsigned m = eight[i]; m; m &= m - 1, ++to)
+            if (to < kList) s_list[to] = uint32_t(i * 8 + __ffs(int(m)) - 1);
         built = b;
         built_at = skew;
       } else if (use) {
@@ -443,56 +448,40 @@ __global__ void __launch_bounds__(kThreads, kResident) adjust_logits_kernel(cons
       const int edges = kVector ? 2 * V : 0;
       const int start = kVector ? (V - skew) % V : 0, stop = kVector ? vocab - (vocab + skew) % V : vocab;
       const int count = edges + (listed > kList ? p.slice : listed);
-      constexpr int kTwo = 1;
-      for (int e0 = tid; e0 < count; e0 += kThreads * kTwo) {
-        int v[kTwo];
-        uint32_t w[kTwo], allowed[kTwo];
-        S y[kTwo];
-#pragma unroll
-        for (int k = 0; k < kTwo; ++k) {
-          const int e = e0 + k * kThreads;
-          v[k] = -1;
-          if (e >= count) continue;
-          int t, at;
-          if (e < edges) {
-            t = e < V ? e : max(stop, start) + e - V;
-            at = t < (e < V ? min(start, vocab) : vocab) ? place.here(t) : -1;
-          } else {
-            at = listed > kList ? e - edges : int(s_list[e - edges]);
-            t = place.token(at);
-            if (t < start || t >= stop || (listed > kList && (bits[at / 32] >> (at & 31) & 1u) == 0)) at = -1;
-          }
-          if (at < 0) continue;
-          w[k] = use ? words[at / W::kPerWord] >> shift_of<W>(at) : 0u;
-          if (W::kPerWord == 2) w[k] &= 0xffffu;
-          y[k] = in[t];
-          allowed[k] = mask ? mask[t >> 5] : ~0u;
-          v[k] = t;
+      for (int e = tid; e < count; e += kThreads) {
+        int v, at;
+        if (e < edges) {
+          v = e < V ? e : max(stop, start) + e - V;
+          at = v < (e < V ? min(start, vocab) : vocab) ? place.here(v) : -1;
+        } else {
+          at = listed > kList ? e - edges : int(s_list[e - edges]);
+          v = place.token(at);
+          if (v < start || v >= stop || (listed > kList && (bits[at / 32] >> (at & 31) & 1u) == 0)) at = -1;
         }
-#pragma unroll
-        for (int k = 0; k < kTwo; ++k) {
-          if (v[k] < 0) continue;
-          if (!(allowed[k] >> (v[k] & 31) & 1u)) {
-            y[k] = E::down1(-INFINITY);
-          } else if (w[k] != 0) {
-            float z = E::up1(y[k]);
-            if (w[k] & (W::kKnown | W::kCount)) z = z > 0.0f ? __fdiv_rn(z, repetition) : __fmul_rn(z, repetition);
-            const uint32_t c = w[k] & W::kCount;
-            if (c) z = __fsub_rn(__fsub_rn(z, __fmul_rn(frequency, float(c))), presence);
-            if (w[k] & W::kBiased) {
-              float sum = 0.0f;
+        if (at < 0) continue;
+        uint32_t w = use ? words[at / W::kPerWord] >> shift_of<W>(at) : 0u;
+        if (W::kPerWord == 2) w &= 0xffffu;
+        S y = in[v];
+        if (mask && !(mask[v >> 5] >> (v & 31) & 1u)) {
+          y = E::down1(-INFINITY);
+        } else if (w != 0) {
+          float z = E::up1(y);
+          if (w & (W::kKnown | W::kCount)) z = z > 0.0f ? __fdiv_rn(z, repetition) : __fmul_rn(z, repetition);
+          const uint32_t c = w & W::kCount;
+          if (c) z = __fsub_rn(__fsub_rn(z, __fmul_rn(frequency, float(c))), presence);
+          if (w & W::kBiased) {
+            float sum = 0.0f;
 #pragma unroll 4
-              for (int j = 0; j < int(a.bias_width); ++j)
-                if (s_bias[j] == v[k]) sum = __fadd_rn(sum, s_value[j]);
-              z = __fadd_rn(z, sum);
-            }
-            y[k] = E::down1(z);
+            for (int j = 0; j < int(a.bias_width); ++j)
+              if (s_bias[j] == v) sum = __fadd_rn(sum, s_value[j]);
+            z = __fadd_rn(z, sum);
           }
-          out[v[k]] = y[k];
-          if (a.best) {
-            const uint64_t key = best_key(E::up1(y[k]), v[k]);
-            other = key > other ? key : other;
-          }
+          y = E::down1(z);
+        }
+        out[v] = y;
+        if (a.best) {
+          const uint64_t key = best_key(E::up1(y), v);
+          other = key > other ? key : other;
         }
       }
     }
@@ -532,7 +521,7 @@ cudaError_t launch(const LogitsArgs& p, unsigned ctas, cudaStream_t stream) {
   auto kern = adjust_logits_kernel<E, kVector, kContext, W>;
   const int64_t smem = kContext ? p.slice * 4 / W::kPerWord + p.slice / 8 + p.a.bias_width * 8 + kList * 4 : 0;
   static PerDeviceCache attr_set;
-  const cudaError_t e = set_max_dynamic_smem_once(kern, kContext ? 192 * 1024 : 0, attr_set);
+  const cudaError_t e = set_max_dynamic_smem_once(kern, kContext ? 216 * 1024 : 0, attr_set);
   if (e != cudaSuccess) return e;
   const int64_t clusters = (p.a.rows + p.per - 1) / p.per;
   return launch_cluster(kern, ctas, dim3(unsigned(clusters) * ctas), dim3(kThreads), size_t(smem), stream, p);
@@ -567,7 +556,9 @@ cudaError_t launch_adjust_logits(const nf4_adjust_logits_args& a, cudaStream_t s
   const int64_t most = context ? (wide ? 40 : 80) * 1024 : int64_t(1) << 24;  // tokens of a slice: 160 KB of words
   const int64_t all = a.vocab + 8;                                            // with the skew of any row
   unsigned ctas = 1;
-  while (ctas < 8 && all > int64_t(ctas) * 4096) ctas *= 2;
+  // Four CTAs a row, and eight where that is few CTAs or four would leave one an SM: every CTA reads the whole history.
+  const unsigned cap = !context || a.rows * 8 <= 152 * kResident || all * (wide ? 4 : 2) > 4 * 64 * 1024 + 64 ? 8 : 4;
+  while (ctas < cap && all > int64_t(ctas) * 4096) ctas *= 2;
   const int64_t per_pass = int64_t(ctas) * most;
   p.passes = int((all + per_pass - 1) / per_pass);
   const int64_t parts = int64_t(p.passes) * ctas;
