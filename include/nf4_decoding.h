@@ -147,7 +147,8 @@ typedef struct nf4_adjust_logits_args {
  * token. For a row of request b, c counts the times that token v stands in
  * the part of the request's history after its prompt, and, with draft_tokens,
  * among the nodes x of the request whose bit x is set in the row's tree_mask;
- * v is known where it stands there or in the prompt. Then, in binary32 and in
+ * v is known where it stands there or in the prompt. (A row's own node and node 0
+ * count where their bits are set: a history then ends before node 0.) Then, in binary32 and in
  * this order,
  *   known:  x = x > 0 ? x / repetition : x * repetition
  *   c > 0:  x = (x - fl(frequency * c)) - presence
@@ -199,6 +200,8 @@ typedef struct nf4_tree_commit_args {
  * is lens - n + accepted. With caches, the keys and values of the path's node j
  * (own key lens - n + path[j]) move to own key lens - n + j, in every layer; the
  * rejected nodes' slots then hold anything.
+ * The two caches, and their layers, must not overlap (nor may two sequences share a
+ * page that is moved).
  * A sequence without nodes: accepted 0, path and chosen -1, new_lens = lens.
  * A node whose parent is not a node before it is on no path, nor is one past
  * the first 4096 of its sequence; a row whose slot

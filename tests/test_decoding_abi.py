@@ -56,7 +56,7 @@ GOOD = {
              mask_count=5, mask_rows=A, draft_tokens=A, tree_mask=A, tree_mask_stride=1, tree_words=1),
     "nf4_tree_commit_args":
         dict(parents=A, draft_tokens=A, targets=A, cu_q=A, lens=A, batch=3, tokens=5, max_path=8, accepted=A, path=A,
-             chosen=A, new_lens=B, k_cache=A, k_layer_stride=65536, k_page_stride=4096, k_slot_stride=256,
+             chosen=A, new_lens=B, k_cache=A + 4096, k_layer_stride=65536, k_page_stride=4096, k_slot_stride=256,
              k_head_stride=128, v_cache=A, v_layer_stride=65536, v_page_stride=4096, v_slot_stride=256, v_head_stride=128,
              layers=2, num_pages=50, page_size=16, k_heads=2, head_dim=128, page_table=A, page_table_stride=4, width=4),
 }
@@ -152,7 +152,7 @@ def test_null_argument_structures(lib):
      [dict(batch=-1), dict(batch=(1 << 20) + 1), dict(tokens=-1), dict(max_path=0), dict(max_path=1025), dict(cu_q=0),
       dict(layers=-1), dict(layers=65536), dict(num_pages=-1), dict(page_size=0), dict(k_heads=0), dict(head_dim=0),
       dict(head_dim=513), dict(width=-1), dict(page_table_stride=-1), dict(k_slot_stride=-1), dict(v_layer_stride=-1),
-      dict(new_lens=A)]),
+      dict(k_layer_stride=0), dict(v_layer_stride=0), dict(k_cache=A), dict(new_lens=A)]),
     ("nf4_tree_commit", ERR_NULL,
      [dict(parents=0), dict(draft_tokens=0), dict(targets=0), dict(lens=0), dict(accepted=0), dict(path=0), dict(chosen=0),
       dict(new_lens=0), dict(k_cache=0), dict(v_cache=0), dict(page_table=0)]),

@@ -113,6 +113,8 @@ nf4_status nf4_tree_commit(const nf4_tree_commit_args* args, nf4_stream_t stream
     for (const int64_t s : {a.k_layer_stride, a.k_page_stride, a.k_slot_stride, a.k_head_stride, a.v_layer_stride,
                             a.v_page_stride, a.v_slot_stride, a.v_head_stride})
       if (!in(s, 0, kMaxStride)) return NF4_ERR_INVALID_SIZE;
+    if (a.layers > 1 && (a.k_layer_stride == 0 || a.v_layer_stride == 0)) return NF4_ERR_INVALID_SIZE;  // moved twice
+    if (a.k_cache && a.k_cache == a.v_cache) return NF4_ERR_INVALID_SIZE;  // both would be moved, beside one another
   }
   if (a.batch == 0) return NF4_OK;
   if ((a.tokens > 0 && (!a.parents || !a.draft_tokens || !a.targets)) || !a.lens || !a.accepted || !a.path || !a.chosen ||

@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_cons
   const bool reports = block == 0 && blockIdx.y == 0;
   bool bad = false;
   int lo, hi;
-  const int len = a.lens[b], most = int(a.max_path);
+  const int given_len = a.lens[b], len = max(given_len, 0), most = int(a.max_path);
   token_range(a.cu_q, b, int(a.tokens), &lo, &hi, &bad);
   const int nodes = min(hi - lo, kMostNodes);
   bad = bad || nodes != hi - lo;
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_cons
     if (tid == 0) {
       a.accepted[b] = n;
       a.new_lens[b] = max(base + n, 0);
-      bad = bad || len < 0;
+      bad = bad || given_len < 0;
     }
   }
   if (a.layers > 0 && n > 0) {
