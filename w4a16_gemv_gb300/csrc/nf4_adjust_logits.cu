@@ -557,15 +557,20 @@ cudaError_t launch_adjust_logits(const nf4_adjust_logits_args& a, cudaStream_t s
   const int64_t all = a.vocab + 8;                                            // with the skew of any row
   unsigned ctas = 1;
   // Four CTAs a row, and eight where that is few CTAs or four would leave one an SM: every CTA reads the whole history.
-  const unsigned cap = !context || a.rows * 8 <= 152 * kResident || all * (wide ? 4 : 2) > 4 * 64 * 1024 + 64 ? 8 : 4;
+  const unsigned cap = !context || a.rows * 8 <= 144 * kResident || all * (wide ? 4 : 2) > 4 * 64 * 1024 + 64 ? 8 : 4;
   while (ctas < cap && all > int64_t(ctas) * 4096) ctas *= 2;
   const int64_t per_pass = int64_t(ctas) * most;
   p.passes = int((all + per_pass - 1) / per_pass);
   const int64_t parts = int64_t(p.passes) * ctas;
   p.slice = int(((all + parts - 1) / parts + kBlock - 1) / kBlock * kBlock);
   p.ctas_log2 = ctas == 8 ? 3 : ctas == 4 ? 2 : ctas == 2 ? 1 : 0;
-  const int64_t resident = 152 * kResident / ctas;  // clusters
-  const int64_t per = (a.rows + resident - 1) / resident;
+  // Rows of a cluster: so many that all clusters are there at once. (An SM takes two CTAs of up to 110 KB; the CTAs of a
+  // cluster lie within a GPU processing cluster, whose last SMs may be left over: the numbers are the occupancy
+  // calculator's. With 76 clusters of four where 74 are there, the last two ran alone: 384 rows 162 us, not 110.)
+  const int64_t bytes = context ? int64_t(p.slice) * (wide ? 4 : 2) + p.slice / 8 + p.a.bias_width * 8 + kList * 4 : 0;
+  const int per_sm = bytes <= 105 * 1024 ? kResident : 1;
+  const int sms = ctas <= 2 ? 152 : ctas == 4 ? (per_sm > 1 ? 148 : 144) : per_sm > 1 ? 144 : 120;
+  const int64_t resident = sms * per_sm / int(ctas), per = (a.rows + resident - 1) / resident;
   p.per = int(per < kMostRows ? per : kMostRows);
   switch (a.dtype) {
     case NF4_BF16: return launch_vector<B16>(p, context, wide, ctas, stream);
