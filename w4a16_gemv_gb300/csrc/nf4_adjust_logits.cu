@@ -18,7 +18,7 @@
 // The logits are read and written once: memory bounds many rows, a chain of loads
 // (offsets, lengths, history) a few. Without a context 64 rows of 128000 in bf16 take
 // 5.7 us and 384 in binary32 65 (5.9 and 6.0 TB/s); with masks, best tokens and 8000 (3000)
-// words of history each 24 and 109, bound by instructions (a quarter of them picks
+// words of history each 24 and 108, bound by instructions (a quarter of them picks
 // words) and by the latencies between a row's stream and its listed tokens.
 #include "nf4_decoding.cuh"
 #include "nf4_prefix_attn.cuh"  // 16-byte asynchronous copies
@@ -349,10 +349,13 @@ __global__ void __launch_bounds__(kThreads, kResident) adjust_logits_kernel(cons
       constexpr int kBatch = kContext ? 2 : 4;  // chunks of a thread under way (with four, registers spill)
       uint4 x[kBatch];
       uint32_t low[kBatch], high[kBatch];  // bits of the mask for these, from v0 & 31 on
-      auto load = [&](int at0) {
+      constexpr int kStep = kThreads * V;  // to the thread's next chunk: whole blocks,
+      static_assert(!kVector || kStep % kBlock == 0, "");
+      const int stride = kVector ? kStep << p.ctas_log2 : 0;  // so many tokens on
+      auto next_token = [&](int v0, int at) { return kVector ? v0 + stride : place.token(at + kStep); };
+      auto load = [&](int at, int v0) {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int at = at0 + k * kThreads * V, v0 = place.token(at);
+        for (int k = 0; k < kBatch; ++k, v0 = next_token(v0, at), at += kStep) {
           low[k] = high[k] = 0xffffffffu;
           if (at >= p.slice || v0 < 0 || v0 + V > vocab) continue;
           if (kVector)
@@ -365,7 +368,8 @@ __global__ void __launch_bounds__(kThreads, kResident) adjust_logits_kernel(cons
           }
         }
       };
-      load(tid * V);
+      const int token0 = place.token(tid * V);
+      load(tid * V, token0);
       if (build) {
         __syncthreads();
         // The list: counted first, so that a warp takes its part at once.
@@ -402,11 +406,10 @@ __global__ void __launch_bounds__(kThreads, kResident) adjust_logits_kernel(cons
       if (use) added = row;
 
       // The stream. Tokens with a word are left out of the choice of the best.
-      for (int at0 = tid * V; at0 < p.slice; at0 += kThreads * V * kBatch) {
-        if (at0 != tid * V) load(at0);
+      for (int at = tid * V, v0 = token0; at < p.slice;) {
+        if (at != tid * V) load(at, v0);
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int at = at0 + k * kThreads * V, v0 = place.token(at);
+        for (int k = 0; k < kBatch; ++k, v0 = next_token(v0, at), at += kStep) {
           if (at >= p.slice || v0 < 0 || v0 + V > vocab) continue;
           const uint32_t allowed = __funnelshift_r(low[k], high[k], v0 & 31);
           if constexpr (kVector) {
