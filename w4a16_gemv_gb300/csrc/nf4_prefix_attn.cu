@@ -788,17 +788,20 @@ int sms_for_own(const PrefixArgs& p, int64_t own_items, int64_t tiles, int64_t p
 // Trees (many short runs of rows, each over keys of its own): which kernel, and how
 // long the ranges. A model of three plans, in microseconds, of which the least is
 // taken; "units" are 64 keys of a tile of 64 rows, "tiles" whole key tiles of 256.
-//   * everything on 64-row tiles in one launch: 7 + 2.4 per unit and SM's two CTAs.
+//   * everything on 64-row tiles in one launch: 7 + 2.4 per unit and SM's two CTAs, or, with
+//     more items than those, 3.9 for each of them and SM's two CTAs.
 //     2 trees of 8 over 300 + 60 keys (12 heads over 2): 10.4 us, 16 on two kernels;
 //   * everything on the tcgen05 kernel in one launch: 6.5 + 1.5 per tile (2 with more
 //     than 128 rows) and SM, and 3.5 tiles of start and end per item. One tree of 25
 //     over 50000 keys of 32 heads: 133 us, 213 on 16-row tiles; 37 trees of up to 13
 //     over 777 + 500 keys in pages of 24: 17.3, 22 on 64-row tiles;
 //   * up to 16 rows of a sequence: own keys on 16-row tiles, at about 5.5 TB/s (up to
-//     32, at 4.2), and shared ones on the tcgen05 kernel beside them: 8 sequences x 32
+//     32, at 2.7), and shared ones on the tcgen05 kernel beside them: 8 sequences x 32
 //     heads x 16 nodes over 500 + 300 keys 18.4 us, 22.7 on 64-row tiles.
-// Over 64 shapes drawn at random the plan's time is 1.5% above the best of all plans
-// and ranges tried for each.
+// Over 192 shapes drawn at random the plan's time is 3% below the best of the kernels
+// with 1, 2, 4, 8, 16, 48 and 128 ranges tried for each (own keys; as many for shared
+// ones), and at worst 1.4 times it: 8 trees of equal lengths of 23162 keys, 88 us, 63 in
+// 4 ranges, where lengths are taken for uneven.
 // Sequences hold some 80% of the longest one's keys on average.
 struct TreePlan {
   int prefix_rows, suffix_rows;
@@ -813,7 +816,10 @@ TreePlan plan_tree(const nf4_prefix_attention_args& a, int64_t suffix_max, int64
   // 64 rows
   const double own_units = double(a.batch * tiles(each, 64) * tiles(suffix_max, kUnit)) * heads;
   const double shared_units = double(tiles(rows, 64) * tiles(a.prefix_len, kUnit)) * heads;
-  const double est64 = 7.0 + 2.4 * (own_units * kFull + shared_units) / double(2 * kSms);
+  const double places = 2.0 * kSms, work64 = (own_units * kFull + shared_units) / places;
+  const double items64 = double(a.batch * tiles(each, 64) + (a.prefix_len > 0 ? tiles(rows, 64) : 0)) * heads / places;
+  const double few64 = 7.0 + 2.4 * work64, many64 = 3.5 + 2.5 * work64 + 3.9 * items64;
+  const double est64 = items64 > 1.0 && many64 > few64 ? many64 : few64;
   // 256 rows
   const double own_items = double(a.batch * tiles(each, 256)) * heads, shared_items = double(tiles(rows, 256)) * heads;
   const int64_t own_tiles = tiles(suffix_max, tile_keys), shared_tiles = tiles(a.prefix_len, tile_keys);
@@ -825,7 +831,7 @@ TreePlan plan_tree(const nf4_prefix_attention_args& a, int64_t suffix_max, int64
   TreePlan plan = {256, 256, 0};
   if (each <= 32) {
     const double bytes = double(a.batch * suffix_max) * heads * double(a.head_dim) * 4.0 * kFull;
-    const double est16 = (a.prefix_len > 0 ? 10.0 : 8.0) + bytes / (each <= 16 ? 5.5e6 : 4.2e6) +
+    const double est16 = (a.prefix_len > 0 ? 10.0 : 8.0) + bytes / (each <= 16 ? 5.5e6 : 2.7e6) +
                          (a.prefix_len > 0 ? (shared_work * shared_time + 1.5 * kStart * shared_items) / kSms : 0.0);
     if (est16 < est64 && est16 < est256) {
       plan.prefix_rows = rows > 16 || a.prefix_len > 1024 ? 256 : 16;
@@ -838,28 +844,43 @@ TreePlan plan_tree(const nf4_prefix_attention_args& a, int64_t suffix_max, int64
     const int64_t units = int64_t(own_units + shared_units), whole = tiles(units, 2 * kSms), four = units / (4 * kSms);
     plan.prefix_rows = plan.suffix_rows = 64;
     plan.per = whole <= 6 ? whole : four < 6 ? 6 : four;
+    // one range where that is one unit more at most: it saves the join (12 trees of 47 over up to 128 keys, 16 heads
+    // over 4: 9.7 us in two ranges, 6.0 in one)
+    if (shared_tiles == 0 && whole <= 6 && tiles(suffix_max, kUnit) <= whole + 1) plan.per = whole + 1;
     return plan;
   }
   // The ranges that end soonest: shared items, all alike, in rounds (an item's start and end are 5.5 tiles of an SM's
-  // time there: 16 sequences and heads over 47458 keys take 77 us in 9 ranges, one round, 111 in 10), and own ones
-  // where these leave SMs free and behind them, half as if they were alike and half as if uneven ones filled the SMs.
+  // time there: 16 sequences and heads over 47458 keys take 77 us in 9 ranges, one round, 111 in 10), then own ones on
+  // the SMs that the last round leaves and behind it. Those are counted too, for a few items too many are a round more
+  // (6 sequences x 6 heads of 96 over 28842 keys: 4 ranges, 144 items, 95 us, 5 ranges 147): a third as if sequences
+  // were all as long as the longest, the rest with lengths spread evenly from 60% of it up, where a range behind a
+  // sequence's end costs nothing (37 sequences over 500 keys in ranges of 480: 17.3 us, in one range 20.4).
   const double kItem = 5.5;
   double best = 0.0;
   const int64_t longest = own_tiles > shared_tiles ? own_tiles : shared_tiles;
   for (int64_t parts = 1; parts <= kMaxRanges && parts <= longest; parts += parts / 16 + 1) {
     const int64_t per = tiles(longest, parts);
     const int64_t s = tiles(shared_tiles, per), o = tiles(own_tiles, per);
-    const double shared_all = shared_items * double(s), own_all = own_items * double(o);
-    const double item = double(per) + kItem, own_item = double(per < own_tiles ? per : own_tiles) + kItem;
-    const double own_total = own_work + kItem * own_all;
+    double uneven = 0.0;  // ranges of a sequence that hold keys, on average; one sequence is the longest
+    for (int64_t r = 0; r < o; ++r) {
+      const double part = double(own_tiles - r * per) / (2.0 * (1.0 - kFull) * double(own_tiles));
+      uneven += (1.0 + (part < 1.0 ? part : 1.0) * double(a.batch - 1)) / double(a.batch);
+    }
+    const double shared_all = shared_items * double(s);
+    const double item = double(per < shared_tiles ? per : shared_tiles) + kItem;
+    const double own_item = double(per < own_tiles ? per : own_tiles) + kItem;
     const double whole = double(int64_t(shared_all) / kSms), rest = shared_all - whole * kSms;
-    double time = (whole + (rest > 0.0 ? 1.0 : 0.0)) * item;
-    const double more = own_total - (rest > 0.0 ? (kSms - rest) * item : 0.0);
-    if (rest > 0.0 && more > 0.0)
-      time += more / kSms + 0.75 * own_item;
-    else if (rest == 0.0 && own_all > 0.0)
-      time += own_all <= kSms ? own_item
-                              : 0.5 * (double((int64_t(own_all) + kSms - 1) / kSms) * own_item + more / kSms + 0.5 * own_item);
+    const double spare = kSms - rest, last = rest > 0.0 ? item : 0.0;
+    auto end = [&](double ranges, double work) {  // behind the whole rounds
+      const double all = own_items * ranges;
+      if (all > 0.0 && all <= spare) return last > own_item ? last : own_item;  // all at once
+      if (all <= spare * double(int64_t(last / own_item))) return last;
+      const double beside = spare * double(int64_t(last / own_item)), more = work + kItem * all - spare * last;
+      const double rounds = double((int64_t(all - beside) + kSms - 1) / kSms) * own_item;
+      const double spread = (more > 0.0 ? more / kSms : 0.0) + 0.5 * own_item;
+      return last + (rounds < spread ? rounds : spread);
+    };
+    const double time = whole * item + end(double(o), own_work / kFull) / 3.0 + end(uneven, own_work) * 2.0 / 3.0;
     const double cost = time + double(s + o) * double(rows) * heads * 1e-4;
     if (parts == 1 || cost < best) {
       best = cost;
