@@ -73,7 +73,8 @@ typedef struct nf4_kv_pages_args {
  * Lengths, cu_q, held and free_count out of range are clamped into it, returned
  * pages past the capacity are dropped, a token on a negative page number gets
  * slot -1; all set bit 1 of the device error flags.
- * One launch of one thread-block cluster.
+ * One launch of one thread-block cluster; a second one of the tokens where these are more than 4096 or the requests
+ * more than 1024.
  * Errors: NF4_ERR_NULL, NF4_ERR_INVALID_SIZE, NF4_ERR_MISALIGNED, NF4_ERR_CUDA.
  */
 NF4_API nf4_status nf4_kv_pages(const nf4_kv_pages_args* args, nf4_stream_t stream);

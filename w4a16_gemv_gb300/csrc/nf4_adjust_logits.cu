@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, kResident) adjust_logits_kernel(cons
           copy(x + kSteps);
           auto pick = [&](int v, int nth) {
             if (real) worst = max(worst, unsigned(v));
-            const bool picked = (((v + skew) ^ first) & bits_of) == 0;
+            const bool picked = ((int(unsigned(v) + unsigned(skew)) ^ first) & bits_of) == 0;
             const unsigned all = __ballot_sync(0xffffffffu, picked);
             if (picked) s_queue[held + __popc(all & ((1u << lane) - 1u))] = uint32_t(v) | (j + nth < prompt ? kOnlyKnown : 0u);
             held += __popc(all);
