@@ -345,6 +345,40 @@ def test_long_caches(batch, nodes, length):
         c.check(c.run())
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("hq,hk,dim", [(32, 8, 128), (16, 8, 64), (24, 8, 80)])
+@pytest.mark.parametrize("page", [16, 24, 128])
+@pytest.mark.parametrize("prefix", [0, 700])
+def test_key_tiles_in_turns(dt, hq, hk, dim, page, prefix):
+    """Up to 128 rows of a sequence over two key tiles and more: each half of the tiles has a softmax of its own."""
+    lens = [129, 130, 200, 240, 241, 256, 257, 384, 385, 500, 640, 641, 900, 1024, 1025, 1150]
+    c = Call(hq, hk, dim, prefix, lens, [1 + (7 * b) % 32 for b in range(16)], page=page, dt=dt, seed=page + prefix)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("hk,dim", [(8, 64), (8, 128)])
+@pytest.mark.parametrize("page", [16, 24])
+def test_rows_that_see_one_half_of_the_keys(hk, dim, page):
+    rng = random.Random(3)
+    seen = [{rng.choice((0, 119, 120, 127, rng.randrange(128)))} if rng.random() < 0.8 else set() for _ in range(16 * 128)]
+    c = Call(hk, hk, dim, 0, [128] * 16, [128] * 16, page=page, seed=page, seen=seen)
+    c.check(c.run())
+
+
+def test_infinities_and_nan_in_one_half_of_the_keys():
+    c = Call(32, 8, 128, 0, [600] * 16, [30] * 16, seed=11)
+    keys = c.k[c.suffix_pages[3, 590 // 16].long(), 590 % 16]  # a node that few rows see
+    keys.fill_(float("nan"))
+    out, lse = c.run()
+    node, first = 590 - 570, 3 * 30
+    hit = torch.tensor([node in c.seen[first + i] for i in range(30)], device="cuda")
+    assert hit.any() and out[first:first + 30][hit].isnan().all() and not out[first:first + 30][~hit].isnan().any()
+    rest = torch.ones(len(out), dtype=torch.bool, device="cuda")
+    rest[first:first + 30] = False
+    assert not out[rest].isnan().any() and not lse[rest].isnan().any()
+    assert lib().nf4_device_error_flags() == 0
+
+
 def test_two_streams_and_workspaces():
     c = Call(12, 2, 128, 2000, [300, 200], [9, 12], seed=5)
     want = c.run()

@@ -788,106 +788,108 @@ int sms_for_own(const PrefixArgs& p, int64_t own_items, int64_t tiles, int64_t p
 // Trees (many short runs of rows, each over keys of its own): which kernel, and how
 // long the ranges. A model of three plans, in microseconds, of which the least is
 // taken; "units" are 64 keys of a tile of 64 rows, "tiles" whole key tiles of 256.
-//   * everything on 64-row tiles in one launch: 7 + 2.4 per unit and SM's two CTAs, or, with
-//     more items than those, 3.9 for each of them and SM's two CTAs.
+//   * everything on 64-row tiles in one launch: 7 + 2.4 per unit and SM's two CTAs (3.4 where some are shared), or, with
+//     more items than those, 2.5 and 3.9 for each of them; a fifth more for many ranges.
 //     2 trees of 8 over 300 + 60 keys (12 heads over 2): 10.4 us, 16 on two kernels;
-//   * everything on the tcgen05 kernel in one launch: 6.5 + 1.5 per tile (2 with more
-//     than 128 rows) and SM, and 3.5 tiles of start and end per item. One tree of 25
-//     over 50000 keys of 32 heads: 133 us, 213 on 16-row tiles; 37 trees of up to 13
-//     over 777 + 500 keys in pages of 24: 17.3, 22 on 64-row tiles;
+//   * everything on the tcgen05 kernel in one launch: 6.5 of start and end per item and 1 per
+//     tile (1.75 with more than 128 rows; 0.8 of that at 64 elements), in the ranges that end
+//     soonest, or the bytes at 6.3 TB/s. One tree of 25 over 50000 keys of 32 heads: 129 us,
+//     213 on 16-row tiles; 37 trees of up to 13 over 777 + 500 keys in pages of 24: 18, 22 on
+//     64-row tiles;
 //   * up to 16 rows of a sequence: own keys on 16-row tiles, at about 5.5 TB/s (up to
 //     32, at 2.7), and shared ones on the tcgen05 kernel beside them: 8 sequences x 32
 //     heads x 16 nodes over 500 + 300 keys 18.4 us, 22.7 on 64-row tiles.
-// Over 192 shapes drawn at random the plan's time is 3% below the best of the kernels
-// with 1, 2, 4, 8, 16, 48 and 128 ranges tried for each (own keys; as many for shared
-// ones), and at worst 1.4 times it: 8 trees of equal lengths of 23162 keys, 88 us, 63 in
-// 4 ranges, where lengths are taken for uneven.
+// Over 192 shapes drawn at random the choice of the kernel costs 1% against the best
+// of them; with its ranges the plan's time is 2% below the best of the kernels with 1, 2, 4,
+// 8, 16, 48 and 128 ranges tried for each, and at worst 1.45 times it: 8 trees of nearly
+// equal lengths of 23162 keys, 65 us, 45 in 4 ranges, where lengths are taken for uneven.
 // Sequences hold some 80% of the longest one's keys on average.
 struct TreePlan {
   int prefix_rows, suffix_rows;
   int64_t per;  // keys of a range, in half key tiles (tcgen05) or units (64 rows); 0: as for other calls
 };
 TreePlan plan_tree(const nf4_prefix_attention_args& a, int64_t suffix_max, int64_t tile_keys) {
-  const double kFull = 0.8, kStart = 3.5;
+  const double kFull = 0.8, kItem = 6.5, kBytes = 6.3e6;
   const double heads = double(a.k_heads);
   const int64_t group = a.q_heads / a.k_heads, rows = a.tokens * group;
   const int64_t each = a.batch > 0 ? (rows + a.batch - 1) / a.batch : 0;  // of a sequence
   auto tiles = [](int64_t n, int64_t of) { return (n + of - 1) / of; };
-  // 64 rows
-  const double own_units = double(a.batch * tiles(each, 64) * tiles(suffix_max, kUnit)) * heads;
-  const double shared_units = double(tiles(rows, 64) * tiles(a.prefix_len, kUnit)) * heads;
-  const double places = 2.0 * kSms, work64 = (own_units * kFull + shared_units) / places;
-  const double items64 = double(a.batch * tiles(each, 64) + (a.prefix_len > 0 ? tiles(rows, 64) : 0)) * heads / places;
-  const double few64 = 7.0 + 2.4 * work64, many64 = 3.5 + 2.5 * work64 + 3.9 * items64;
-  const double est64 = items64 > 1.0 && many64 > few64 ? many64 : few64;
-  // 256 rows
+  const double own_bytes = double(a.batch * suffix_max) * heads * double(a.head_dim) * 4.0 * kFull;
+  const double bytes = own_bytes + double(a.prefix_len) * heads * double(a.head_dim) * 4.0;
+
+  // 256 rows. The ranges that end soonest: shared items, all alike, in rounds (16 sequences and heads over 47458 keys
+  // took 77 us in 9 ranges, one round, 111 in 10), then own ones on the SMs that the last round leaves and behind it.
+  // Those are counted too, for a few items too many are a round more (6 sequences x 6 heads of 96 over 28842 keys: 4
+  // ranges, 144 items, 95 us, 5 ranges 147): a third as if sequences were all as long as the longest, the rest with
+  // lengths spread evenly from 60% of it up, where a range behind a sequence's end costs nothing (37 sequences over 500
+  // keys in ranges of 480: 17.3 us, in one range 20.4).
   const double own_items = double(a.batch * tiles(each, 256)) * heads, shared_items = double(tiles(rows, 256)) * heads;
   const int64_t own_tiles = tiles(suffix_max, tile_keys), shared_tiles = tiles(a.prefix_len, tile_keys);
-  const double own_time = each > 128 ? 2.0 : 1.5, shared_time = rows > 128 ? 2.0 : 1.5;
-  const double own_work = own_items * double(own_tiles) * kFull, shared_work = shared_items * double(shared_tiles);
-  const double least = (own_tiles > 0 ? own_items : 0.0) + (shared_tiles > 0 ? shared_items : 0.0);
-  const double est256 = 6.5 + (own_work * own_time + shared_work * shared_time +
-                               1.5 * kStart * (least > kSms ? least : double(kSms))) / kSms;
-  TreePlan plan = {256, 256, 0};
-  if (each <= 32) {
-    const double bytes = double(a.batch * suffix_max) * heads * double(a.head_dim) * 4.0 * kFull;
-    const double est16 = (a.prefix_len > 0 ? 10.0 : 8.0) + bytes / (each <= 16 ? 5.5e6 : 2.7e6) +
-                         (a.prefix_len > 0 ? (shared_work * shared_time + 1.5 * kStart * shared_items) / kSms : 0.0);
-    if (est16 < est64 && est16 < est256) {
-      plan.prefix_rows = rows > 16 || a.prefix_len > 1024 ? 256 : 16;
-      plan.suffix_rows = 16;
-      return plan;
-    }
-  }
-  if (est64 < est256) {
-    // as many items as there are places, of one unit or more; longer ones in about four rounds
-    const int64_t units = int64_t(own_units + shared_units), whole = tiles(units, 2 * kSms), four = units / (4 * kSms);
-    plan.prefix_rows = plan.suffix_rows = 64;
-    plan.per = whole <= 6 ? whole : four < 6 ? 6 : four;
-    // one range where that is one unit more at most: it saves the join (12 trees of 47 over up to 128 keys, 16 heads
-    // over 4: 9.7 us in two ranges, 6.0 in one)
-    if (shared_tiles == 0 && whole <= 6 && tiles(suffix_max, kUnit) <= whole + 1) plan.per = whole + 1;
-    return plan;
-  }
-  // The ranges that end soonest: shared items, all alike, in rounds (an item's start and end are 5.5 tiles of an SM's
-  // time there: 16 sequences and heads over 47458 keys take 77 us in 9 ranges, one round, 111 in 10), then own ones on
-  // the SMs that the last round leaves and behind it. Those are counted too, for a few items too many are a round more
-  // (6 sequences x 6 heads of 96 over 28842 keys: 4 ranges, 144 items, 95 us, 5 ranges 147): a third as if sequences
-  // were all as long as the longest, the rest with lengths spread evenly from 60% of it up, where a range behind a
-  // sequence's end costs nothing (37 sequences over 500 keys in ranges of 480: 17.3 us, in one range 20.4).
-  const double kItem = 5.5;
-  double best = 0.0;
+  const double narrow = a.head_dim <= 64 ? 0.8 : 1.0;
+  const double own_tile = (each > 128 ? 1.75 : 1.0) * narrow, shared_tile = (rows > 128 ? 1.75 : 1.0) * narrow;
+  const double own_work = own_items * double(own_tiles) * kFull * own_tile;
   const int64_t longest = own_tiles > shared_tiles ? own_tiles : shared_tiles;
+  double best = 0.0;
+  int64_t best_per = 0;
   for (int64_t parts = 1; parts <= kMaxRanges && parts <= longest; parts += parts / 16 + 1) {
     const int64_t per = tiles(longest, parts);
     const int64_t s = tiles(shared_tiles, per), o = tiles(own_tiles, per);
-    double uneven = 0.0;  // ranges of a sequence that hold keys, on average; one sequence is the longest
-    for (int64_t r = 0; r < o; ++r) {
-      const double part = double(own_tiles - r * per) / (2.0 * (1.0 - kFull) * double(own_tiles));
-      uneven += (1.0 + (part < 1.0 ? part : 1.0) * double(a.batch - 1)) / double(a.batch);
-    }
+    // ranges of a sequence that hold keys, on average: `all` that every sequence reaches, and of the others the part
+    // (1 - start / longest) / 0.4 of sequences; one sequence is the longest
+    const double spread_of = 2.0 * (1.0 - kFull) * double(own_tiles);
+    const int64_t reach = int64_t((double(own_tiles) - spread_of) / double(per)) + 1, all = o < reach ? o : reach;
+    const double others =
+        o > all ? double(o - all) * (double(own_tiles) - 0.5 * double(per) * double(all + o - 1)) / spread_of : 0.0;
+    const double uneven = a.batch > 0 ? (double(o) + (double(all) + others) * double(a.batch - 1)) / double(a.batch) : 0.0;
     const double shared_all = shared_items * double(s);
-    const double item = double(per < shared_tiles ? per : shared_tiles) + kItem;
-    const double own_item = double(per < own_tiles ? per : own_tiles) + kItem;
+    const double item = double(per < shared_tiles ? per : shared_tiles) * shared_tile + kItem;
+    const double own_item = double(per < own_tiles ? per : own_tiles) * own_tile + kItem;
     const double whole = double(int64_t(shared_all) / kSms), rest = shared_all - whole * kSms;
     const double spare = kSms - rest, last = rest > 0.0 ? item : 0.0;
+    const double beside = spare * double(int64_t(last / own_item));
     auto end = [&](double ranges, double work) {  // behind the whole rounds
-      const double all = own_items * ranges;
-      if (all > 0.0 && all <= spare) return last > own_item ? last : own_item;  // all at once
-      if (all <= spare * double(int64_t(last / own_item))) return last;
-      const double beside = spare * double(int64_t(last / own_item)), more = work + kItem * all - spare * last;
-      const double rounds = double((int64_t(all - beside) + kSms - 1) / kSms) * own_item;
+      const double count = own_items * ranges;
+      if (count > 0.0 && count <= spare) return last > own_item ? last : own_item;  // all at once
+      if (count <= beside) return last;
+      const double more = work + kItem * count - spare * last;
+      const double rounds = double((int64_t(count - beside) + kSms - 1) / kSms) * own_item;
       const double spread = (more > 0.0 ? more / kSms : 0.0) + 0.5 * own_item;
       return last + (rounds < spread ? rounds : spread);
     };
-    const double time = whole * item + end(double(o), own_work / kFull) / 3.0 + end(uneven, own_work) * 2.0 / 3.0;
-    const double cost = time + double(s + o) * double(rows) * heads * 1e-4;
+    double time = whole * item + end(double(o), own_work / kFull) / 3.0 + end(uneven, own_work) * 2.0 / 3.0;
+    if (time < bytes / kBytes + kItem) time = bytes / kBytes + kItem;
+    // partial results and their join
+    const double cost = time + double(s + o) * double(rows) * heads * 1.5e-4 + (s + o > 1 ? 2.0 : 0.0);
     if (parts == 1 || cost < best) {
       best = cost;
-      plan.per = 2 * per;
+      best_per = 2 * per;
     }
   }
-  return plan;
+  const double est256 = 0.95 * (2.0 + best);
+
+  // 64 rows
+  const int64_t own_units = tiles(suffix_max, kUnit), shared_units = tiles(a.prefix_len, kUnit);
+  const double own64 = double(a.batch * tiles(each, 64)) * heads, shared64 = double(tiles(rows, 64)) * heads;
+  const double work64 = (own64 * double(own_units) * kFull + shared64 * double(shared_units)) / (2.0 * kSms);
+  const double items64 = (own64 + (shared_units > 0 ? shared64 : 0.0)) / (2.0 * kSms);
+  const double few64 = 7.0 + (shared_units > 0 ? 3.4 : 2.4) * work64, many64 = 3.5 + 2.5 * work64 + 3.9 * items64;
+  const double est64 = (items64 > 1.0 && many64 > few64 ? many64 : few64) *
+                       (own_units > 32 || shared_units > 32 ? 1.2 : 1.0);
+  if (each <= 32) {
+    double est16 = 8.0 + own_bytes / (each <= 16 ? 5.5e6 : 2.7e6);
+    if (a.prefix_len > 0)
+      est16 += 5.0 + 1.5 * shared_items * (double(shared_tiles) * (rows > 128 ? 1.75 : 1.0) + kItem) / kSms;
+    if (est16 < est64 && est16 < est256)
+      return {rows > 16 || a.prefix_len > 1024 ? 256 : 16, 16, 0};
+  }
+  if (est64 >= est256) return {256, 256, best_per};
+  // as many items as there are places, of one unit or more; longer ones in about four rounds
+  const int64_t units = int64_t(own64 * double(own_units) + shared64 * double(shared_units));
+  const int64_t whole = tiles(units, 2 * kSms), four = units / (4 * kSms);
+  // one range where that is one unit more at most: it saves the join (12 trees of 47 over up to 128 keys, 16 heads over
+  // 4: 9.7 us in two ranges, 6.0 in one)
+  const bool one = shared_units == 0 && whole <= 6 && own_units <= whole + 1;
+  return {64, 64, one ? whole + 1 : whole <= 6 ? whole : four < 6 ? 6 : four};
 }
 
 }  // namespace

@@ -32,6 +32,15 @@
 //   * warp 12: issues the products. S of the next keys follows O += P V of a
 //     tile in issue order, so P is read before S overwrites it, and the signal
 //     that S is complete also says that O is at rest.
+// In calls of trees, an item of up to 128 rows over two key tiles or more is a pair of
+// halves: with one tile of rows a key tile's products and its softmax wait for one
+// another (1.4 us per key tile), so tile 0 takes the even key tiles and tile 1 the odd
+// ones, with Q, S and O as above, K and V by a warp each (small boxes are bound by
+// their issue), and the ring one tile longer at 128 elements (the second tile of Q is
+// not there). The halves' maxima, sums and outputs are joined on the way out. 16 trees
+// of up to 32 nodes and 32 heads over 8 take 60 us over 4000 keys without, 44 with it
+// (1.05 us per key tile; two key tiles 13.2 and 12.1), one of 25 over 50000 keys of 32
+// heads 132 and 124.
 // An item leaves its partial result, or the output; an item of own keys of a call
 // with one range of each joins the shared keys' part of its rows on the way out.
 // Tensor memory: S (and P) of the tiles in columns 0 and 128, O in 256 and 384.
@@ -42,6 +51,8 @@
 // Waits are bounded; one that runs out sets bit 0 of the device error flags.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+
+#include <type_traits>
 
 #include "nf4_prefix_attn.cuh"
 
@@ -57,6 +68,7 @@ constexpr int kTcThreads = 512;
 constexpr int kTileRows = 128;
 constexpr int kTileKeys = 128;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kKeys = 4;  // barriers of K tiles where key tiles take turns
 constexpr int kGo = 4;  // key tiles whose loads may be under way (a ring of 8 tiles holds less than 4 pairs)
 // Registers: 512 threads launch with 128 each (65536); the two softmax
 // warpgroups take 184, the others keep 72: 256 x 184 + 256 x 72 = 65536. (With
@@ -221,10 +233,22 @@ struct Layout {
   static constexpr uint32_t kTile = kBlocks * kBlock;           // 128 rows
   static constexpr int kStages = DP == 128 ? 5 : 8;             // ring of K and V tiles
   static constexpr int kLag = 3;                                // tiles that a loader leaves in flight
+  static constexpr int kPairStages = DP == 128 ? 6 : 8;         // with the second tile of Q among them
   static constexpr uint32_t kRing = 2 * kTile;                  // after the two tiles of Q
   static constexpr uint32_t kBars = kRing + kStages * kTile;
   static constexpr uint32_t kBytes = kBars + 256 + 1024;        // + slack to align the base
 };
+
+// Address of ring tile `slot`; the one past a ring of kStages is the second tile of Q, in front of it.
+template <int DP>
+__device__ __forceinline__ uint32_t ring_tile(uint32_t sbase, int slot) {
+  using L = Layout<DP>;
+  return sbase + L::kRing + uint32_t(slot < L::kStages ? slot : -1) * L::kTile;
+}
+// The two softmax warps of the same 32 rows.
+__device__ __forceinline__ void pair_sync(int quarter) {
+  asm volatile("bar.sync %0, 64;" ::"r"(quarter + 2) : "memory");
+}
 
 template <typename H, int DP, bool kTma, bool T>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -240,9 +264,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // a barrier costs the issuing thread some 250 cycles while the tensor cores
   // keep the shared memory busy, and their queue does not bridge that.
   uint64_t* const go = reinterpret_cast<uint64_t*>(smem + L::kBars);    // [kGo], key tile i: i % kGo
-  uint64_t* const kfirst = go + kGo;                                    // K_0 landed
-  uint64_t* const empty = kfirst + 1;                                   // a ring tile's products are done
-  uint64_t* const sfull = empty + L::kStages;                           // S of a tile complete, O at rest
+  uint64_t* const kfirst = go + kGo;                                    // K_0 landed; [kKeys], in a pair K_i: i % kKeys
+  uint64_t* const empty = kfirst + kKeys;                               // a ring tile's products are done
+  uint64_t* const sfull = empty + 8;                                    // S of a tile complete, O at rest
   uint64_t* const psecond = sfull + 2;                                  // P of the second tile written
   uint64_t* const qfull = psecond + 1;                                  // Q of a tile in place (4 softmax warps)
   uint64_t* const tail = qfull + 2;                                     // the last tile of V landed, to be cleaned
@@ -252,16 +276,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int step = kTma ? maps.tile_keys : kTileKeys;
   if (kTma && step < kTileKeys) {
     const int past = (kTileKeys - step) * 8;  // 16 bytes each
-    for (int block = 0; block < L::kStages * L::kBlocks; ++block)
+    for (int block = T && L::kPairStages > L::kStages ? -L::kBlocks : 0; block < L::kStages * L::kBlocks; ++block)
       for (int e = tid; e < past; e += kTcThreads)
-        *reinterpret_cast<uint4*>(smem + L::kRing + block * L::kBlock + step * 128 + e * 16) =
+        *reinterpret_cast<uint4*>(smem + int(L::kRing) + block * int(L::kBlock) + step * 128 + e * 16) =
             make_uint4(0u, 0u, 0u, 0u);
     fence_async_smem();
   }
   if (tid == 0) {
     for (int i = 0; i < kGo; ++i) mbar_init(&go[i], 4 + 2 * kLoaders);
-    for (int i = 0; i < L::kStages; ++i) mbar_init(&empty[i], 1);
-    mbar_init(kfirst, kLoaders);
+    for (int i = 0; i < 8; ++i) mbar_init(&empty[i], 1);
+    for (int i = 0; i < kKeys; ++i) mbar_init(&kfirst[i], kLoaders);
     mbar_init(psecond, 4);
     mbar_init(tail, 1);
     for (int i = 0; i < 2; ++i) {
@@ -291,6 +315,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int n = (it.k1 - it.k0 + step - 1) / step;  // key tiles
   const bool works = it.rows > 0 && n > 0;          // the same in the whole CTA
   const int tiles = it.rows > kTileRows ? 2 : 1;
+  const bool pair = T && kTma && tiles == 1 && n > 1 && !(a.fused && a.splits > 0);
   if (!works) {
     if (a.fused) {
       if (a.beside) pdl_wait_prior_grid();
@@ -345,7 +370,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       cp_async_commit();
     }
     const uint32_t tbase = tmem_address();
-    if (tile < tiles) {
+    if (tile < tiles || pair) {
       cp_async_wait<0>();
       fence_async_smem();
       __syncwarp();
@@ -353,7 +378,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
       const uint32_t s_col = tbase + lanes + uint32_t(tile) * 128u;
       const uint32_t o_col = tbase + lanes + 256u + uint32_t(tile) * 128u;
-      const int r = tile * kTileRows + (warp & 3) * 32 + lane;
+      // (a register, in place of what `pair` follows from: with that kept through the loop two registers spill, and
+      // every key tile waits for them)
+      int stride = pair ? 2 : 1;
+      asm volatile("" : "+r"(stride));
+      const int row0 = pair ? 0 : tile * kTileRows;  // in a pair this tile's keys are every second 128
+      const int r = row0 + (warp & 3) * 32 + lane;
       const int limit = r < it.rows ? min(visible_keys<T>(it, (it.r0 + r) / a.group), it.k1) - it.k0 : 0;
       // key tiles below this one need no mask in this warp
       int free_tiles = T ? max(min(unmasked_keys<T>(it, 0), it.k1) - it.k0, 0) / step : limit / step;
@@ -364,8 +394,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        wait(&sfull[tile], uint32_t(i) & 1u);
+      for (int i = tile & (stride - 1); i < n; i += stride) {
+        wait(&sfull[tile], uint32_t(i >> (stride - 1)) & 1u);
         __syncwarp();
         tc_fence_after();
         float s[128];
@@ -402,7 +432,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int j = 1; j < 32; ++j) mx[c] = fmaxf(mx[c], s[4 * j + c]);
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-        if (i == 0) {
+        if (i < stride) {
           m = top;
         } else if (__any_sync(0xffffffffu, top > m + kGrowth)) {
           const float nm = fmaxf(m, top);
@@ -440,7 +470,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(tile == 0 ? &go[i % kGo] : psecond);
+        if (lane == 0) mbar_arrive(tile == 0 || stride > 1 ? &go[i % kGo] : psecond);
       }
       m -= kLift<H>;  // from here what l and O are relative to
       const bool mine = r < it.rows;
@@ -457,127 +487,204 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int rl = 4 * j + (lane >> 3);
         dst[j] = reinterpret_cast<char*>(__shfl_sync(
             0xffffffffu, reinterpret_cast<uint64_t>(a.direct ? ro.out : reinterpret_cast<char*>(ro.part)), rl));
-        if (tile * kTileRows + (warp & 3) * 32 + rl >= it.rows) dst[j] = nullptr;
+        if (row0 + (warp & 3) * 32 + rl >= it.rows) dst[j] = nullptr;
       }
-      const bool joins = a.fused && a.splits > 0;
-      float2 shared = make_float2(-INFINITY, 0.0f);  // the row's shared keys: maximum and sum,
-      float4 z[8];                                   // and 32 columns of their output, of the rows in dst
-      auto shared_part = [&](int c) {
-        const int row = int(ro.row);  // below 2^30
-        const bool there = part_holds(shared);
-        const float* src = a.part + c * 32 + ch * 4;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int rl = 4 * j + (lane >> 3);
-          const int at = __shfl_sync(0xffffffffu, row, rl);
-          const bool here = __shfl_sync(0xffffffffu, int(there), rl) && dst[j] && c * 32 + ch * 4 < a.dim;
-          z[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (here) z[j] = *reinterpret_cast<const float4*>(src + int64_t(at) * a.dim);
-        }
-      };
-      if (joins) {
-        if (a.beside) pdl_wait_prior_grid();
-        shared = a.ml[ro.row];
-        shared_part(0);
-      }
-      wait(&sfull[tile], uint32_t(n) & 1u);  // the last product is in O
-      __syncwarp();
-      tc_fence_after();
-      float l = l2[0].x + l2[0].y + (l2[1].x + l2[1].y);
-      float own = 1.0f, other = 0.0f;  // weights of this item and of the shared keys
-      const bool holds = part_holds(make_float2(m, l));
-      if (joins) {
-        const float top = fmaxf(m, shared.x);
-        own = part_weight(make_float2(m, l), top);
-        l *= own;
-        if (part_holds(shared)) {
-          other = part_weight(shared, top);
-          l = fmaf(shared.y, other, l);
-        }
-        m = top;
-      }
-      const bool any = l > 0.0f || l != l;
-      const float inv = any ? 1.0f / l : 0.0f;
-      const float bad = ok ? 0.0f : __uint_as_float(0x7fc00000u);
-      if (a.fused) {
-        own *= inv;
-        other *= inv;
-#pragma unroll 1
-        for (int c = 0; c < DP / 32; ++c) {
-          float o[32];
-          tmem_ld32(o_col + 32u * c, o);
-          tmem_ld_wait(o, 32);
-          __syncwarp();  // the stage's last pass has been read
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float4 w = make_float4(bad, bad, bad, bad);
-            if (holds)
-              w = make_float4(o[4 * j] * own + bad, o[4 * j + 1] * own + bad, o[4 * j + 2] * own + bad,
-                              o[4 * j + 3] * own + bad);
-            *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = w;
-          }
+      if constexpr (T && kTma) {
+        if (stride > 1) {
+          // Both halves of the keys of this thread's row are in its lane of tensor memory; maxima and sums change
+          // hands through the stages, and each warp writes every second piece of the columns.
+          // (Both stand in the first tile of Q: the second's place may still hold the other half's last keys.)
+          wait(&sfull[tile], uint32_t(tile == 0 ? (n + 1) >> 1 : n >> 1) & 1u);  // this half's last product is in O
           __syncwarp();
-          uint2 y[8];
+          const float sum = l2[0].x + l2[0].y + (l2[1].x + l2[1].y);
+          const float2 here = make_float2(m, ok ? sum : __uint_as_float(0x7fc00000u));
+          float2* const exchange = reinterpret_cast<float2*>(smem + (warp & 3) * 4096) + lane;
+          exchange[tile * 32] = here;
+          tc_fence_before();
+          pair_sync(warp & 3);  // and so is the other half's
+          tc_fence_after();
+          const float2 there = exchange[(tile ^ 1) * 32];
+          pair_sync(warp & 3);  // it has been read
+          const float top = fmaxf(here.x, there.x);
+          const float f_here = part_holds(here) ? part_weight(here, top) : 0.0f;
+          const float f_there = part_holds(there) ? part_weight(there, top) : 0.0f;
+          const float l = here.y * f_here + there.y * f_there;
+          const bool any = l > 0.0f || l != l;
+          const float bad = here.y == here.y && there.y == there.y ? 0.0f : __uint_as_float(0x7fc00000u);
+          const float by = a.direct ? (any ? 1.0f / l : 0.0f) : 1.0f;
+          const float f0 = (tile == 0 ? f_here : f_there) * by, f1 = (tile == 0 ? f_there : f_here) * by;
+          const uint32_t o_at = o_col - uint32_t(tile) * 128u;
+          auto columns = [&](uint32_t at, float* o) {  // 32 joined columns
+            float x[32];
+            tmem_ld32(o_at + at, o);
+            tmem_ld32(o_at + 128u + at, x);
+            tmem_ld_wait(o, 32);
+            tmem_ld_wait(x, 32);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float v = f0 != 0.0f ? o[j] * f0 : 0.0f;
+              o[j] = (f1 != 0.0f ? fmaf(x[j], f1, v) : v) + bad;
+            }
+          };
+#pragma unroll 1
+          for (int c = tile; c < (a.direct ? DP / 64 : DP / 32); c += 2) {
+            uint32_t w[32];
+            float o[32];
+            if (!a.direct) {
+              columns(32u * c, o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(o[j]);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                columns(64u * c + 32u * h, o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[16 * h + j] = H::down2(o[2 * j], o[2 * j + 1]);
+              }
+            }
+            __syncwarp();  // the stage's last pass has been read
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                  make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            __syncwarp();
+            const int at = c * 128 + ch * 16;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int rl = 4 * j + (lane >> 3);
+              const uint4 y = *reinterpret_cast<const uint4*>(stage + rl * 128 + ((ch ^ (rl & 7)) << 4));
+              if (dst[j] && at < row_bytes) *reinterpret_cast<uint4*>(dst[j] + at) = y;
+            }
+          }
+          if (mine && tile == 0) {
+            if (!a.direct)
+              *ro.ml = make_float2(top, l);
+            else if (ro.lse)
+              *ro.lse = any ? fmaf(top, kLn2, logf(l)) : -INFINITY;
+          }
+        }
+      }
+      if (stride == 1) {
+        const bool joins = a.fused && a.splits > 0;
+        float2 shared = make_float2(-INFINITY, 0.0f);  // the row's shared keys: maximum and sum,
+        float4 z[8];                                   // and 32 columns of their output, of the rows in dst
+        auto shared_part = [&](int c) {
+          const int row = int(ro.row);  // below 2^30
+          const bool there = part_holds(shared);
+          const float* src = a.part + c * 32 + ch * 4;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int rl = 4 * j + (lane >> 3);
-            const float4 w = *reinterpret_cast<const float4*>(stage + rl * 128 + ((ch ^ (rl & 7)) << 4));
-            const float f = __shfl_sync(0xffffffffu, other, rl);
-            y[j] = joins ? make_uint2(H::down2(fmaf(z[j].x, f, w.x), fmaf(z[j].y, f, w.y)),
-                                      H::down2(fmaf(z[j].z, f, w.z), fmaf(z[j].w, f, w.w)))
-                         : make_uint2(H::down2(w.x, w.y), H::down2(w.z, w.w));
+            const int at = __shfl_sync(0xffffffffu, row, rl);
+            const bool here = __shfl_sync(0xffffffffu, int(there), rl) && dst[j] && c * 32 + ch * 4 < a.dim;
+            z[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (here) z[j] = *reinterpret_cast<const float4*>(src + int64_t(at) * a.dim);
           }
-          if (joins && c + 1 < DP / 32) shared_part(c + 1);
-          const int col = c * 32 + ch * 4;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (dst[j] && col < a.dim) *reinterpret_cast<uint2*>(dst[j] + col * 2) = y[j];
+        };
+        if (joins) {
+          if (a.beside) pdl_wait_prior_grid();
+          shared = a.ml[ro.row];
+          shared_part(0);
         }
-      }
-      const int passes = a.fused ? 0 : a.direct ? DP / 64 : DP / 32;
-      float o[32];
-      if (!a.direct) tmem_ld32(o_col, o);
+        wait(&sfull[tile], uint32_t(n) & 1u);  // the last product is in O
+        __syncwarp();
+        tc_fence_after();
+        float l = l2[0].x + l2[0].y + (l2[1].x + l2[1].y);
+        float own = 1.0f, other = 0.0f;  // weights of this item and of the shared keys
+        const bool holds = part_holds(make_float2(m, l));
+        if (joins) {
+          const float top = fmaxf(m, shared.x);
+          own = part_weight(make_float2(m, l), top);
+          l *= own;
+          if (part_holds(shared)) {
+            other = part_weight(shared, top);
+            l = fmaf(shared.y, other, l);
+          }
+          m = top;
+        }
+        const bool any = l > 0.0f || l != l;
+        const float inv = any ? 1.0f / l : 0.0f;
+        const float bad = ok ? 0.0f : __uint_as_float(0x7fc00000u);
+        if (a.fused) {
+          own *= inv;
+          other *= inv;
 #pragma unroll 1
-      for (int c = 0; c < passes; ++c) {
-        uint32_t w[32];
-        if (!a.direct) {
-          tmem_ld_wait(o, 32);
+          for (int c = 0; c < DP / 32; ++c) {
+            float o[32];
+            tmem_ld32(o_col + 32u * c, o);
+            tmem_ld_wait(o, 32);
+            __syncwarp();  // the stage's last pass has been read
 #pragma unroll
-          for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(o[j] + bad);
-          if (c + 1 < passes) tmem_ld32(o_col + 32u * (c + 1), o);
-        } else {
+            for (int j = 0; j < 8; ++j) {
+              float4 w = make_float4(bad, bad, bad, bad);
+              if (holds)
+                w = make_float4(o[4 * j] * own + bad, o[4 * j + 1] * own + bad, o[4 * j + 2] * own + bad,
+                                o[4 * j + 3] * own + bad);
+              *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = w;
+            }
+            __syncwarp();
+            uint2 y[8];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            tmem_ld32(o_col + 64u * c + 32u * h, o);
+            for (int j = 0; j < 8; ++j) {
+              const int rl = 4 * j + (lane >> 3);
+              const float4 w = *reinterpret_cast<const float4*>(stage + rl * 128 + ((ch ^ (rl & 7)) << 4));
+              const float f = __shfl_sync(0xffffffffu, other, rl);
+              y[j] = joins ? make_uint2(H::down2(fmaf(z[j].x, f, w.x), fmaf(z[j].y, f, w.y)),
+                                        H::down2(fmaf(z[j].z, f, w.z), fmaf(z[j].w, f, w.w)))
+                           : make_uint2(H::down2(w.x, w.y), H::down2(w.z, w.w));
+            }
+            if (joins && c + 1 < DP / 32) shared_part(c + 1);
+            const int col = c * 32 + ch * 4;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (dst[j] && col < a.dim) *reinterpret_cast<uint2*>(dst[j] + col * 2) = y[j];
+          }
+        }
+        const int passes = a.fused ? 0 : a.direct ? DP / 64 : DP / 32;
+        float o[32];
+        if (!a.direct) tmem_ld32(o_col, o);
+#pragma unroll 1
+        for (int c = 0; c < passes; ++c) {
+          uint32_t w[32];
+          if (!a.direct) {
             tmem_ld_wait(o, 32);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) w[16 * h + j] = H::down2(o[2 * j] * inv + bad, o[2 * j + 1] * inv + bad);
+            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(o[j] + bad);
+            if (c + 1 < passes) tmem_ld32(o_col + 32u * (c + 1), o);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              tmem_ld32(o_col + 64u * c + 32u * h, o);
+              tmem_ld_wait(o, 32);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[16 * h + j] = H::down2(o[2 * j] * inv + bad, o[2 * j + 1] * inv + bad);
+            }
           }
-        }
-        __syncwarp();  // the stage's last pass has been read
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-              make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        __syncwarp();
-        uint4 y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int rl = 4 * j + (lane >> 3);
-          y[j] = *reinterpret_cast<const uint4*>(stage + rl * 128 + ((ch ^ (rl & 7)) << 4));
-        }
-        const int at = c * 128 + ch * 16;
-        if (at < row_bytes) {
+          __syncwarp();  // the stage's last pass has been read
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (dst[j]) *reinterpret_cast<uint4*>(dst[j] + at) = y[j];
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          __syncwarp();
+          uint4 y[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int rl = 4 * j + (lane >> 3);
+            y[j] = *reinterpret_cast<const uint4*>(stage + rl * 128 + ((ch ^ (rl & 7)) << 4));
+          }
+          const int at = c * 128 + ch * 16;
+          if (at < row_bytes) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (dst[j]) *reinterpret_cast<uint4*>(dst[j] + at) = y[j];
+          }
         }
-      }
-      if (mine) {
-        if (!a.direct)
-          *ro.ml = make_float2(m, l);
-        else if (ro.lse)
-          *ro.lse = any ? fmaf(m, kLn2, logf(l)) : -INFINITY;
+        if (mine) {
+          if (!a.direct)
+            *ro.ml = make_float2(m, l);
+          else if (ro.lse)
+            *ro.lse = any ? fmaf(m, kLn2, logf(l)) : -INFINITY;
+        }
       }
     }
     if (a.fused) {
@@ -589,7 +696,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int rows = maps.box_rows;
     const int valid = it.k1 - it.k0 - (n - 1) * step;  // keys of the last tile
     const bool clean = valid % rows != 0;                   // its last box reaches past them
-    if (warp == 8) {
+    // Copies tiles kFirst (0: K) to kLast (1: V) of every key tile; in a pair K and V have a warp each.
+    auto copy_tiles = [&](auto paired, auto first, auto last) {
+      constexpr bool kPair = decltype(paired)::value;
+      constexpr int kFirst = decltype(first)::value, kLast = decltype(last)::value;
+      constexpr int kStages = kPair ? L::kPairStages : L::kStages;
       const int per_tile = (step / rows) * L::kBlocks;  // boxes of a tile: up to 32
       const int box = lane / L::kBlocks, block = lane % L::kBlocks;
       const bool mine = lane < per_tile;
@@ -618,15 +729,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int next_page, next_slot;
         fetch(i + 1, &next_page, &next_slot);
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int u = 2 * i + kv, slot = u % L::kStages;
-          if (u >= L::kStages) wait(&empty[slot], uint32_t(u / L::kStages - 1) & 1u);
-          uint64_t* const bar = kv == 0 ? (i == 0 ? kfirst : &go[(i - 1) % kGo])
+        for (int kv = kFirst; kv <= kLast; ++kv) {
+          const int u = 2 * i + kv, slot = u % kStages;
+          if (u >= kStages) wait(&empty[slot], uint32_t(u / kStages - 1) & 1u);
+          uint64_t* const bar = kv == 0 ? (kPair ? &kfirst[i % kKeys] : i == 0 ? kfirst : &go[(i - 1) % kGo])
                                 : clean && i + 1 == n ? tail : &go[i % kGo];
           if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(step * L::kBlocks) * 128u);
           __syncwarp();
-          const uint32_t dst = sbase + L::kRing + uint32_t(slot) * L::kTile + uint32_t(block) * L::kBlock +
-                               uint32_t(box * rows) * 128u;
+          if (kPair && kv == 1 && i + 1 < n && lane == 0) mbar_arrive(&go[i % kGo]);  // in the place of the next K's
+          const uint32_t dst = ring_tile<DP>(sbase, slot) + uint32_t(block) * L::kBlock + uint32_t(box * rows) * 128u;
           if (mine) {
             if (kv == 0)
               tma_load_box(dst, &maps.k, block * 64, maps.k_slot, maps.k_head, slot0, it.head, page, bar,
@@ -639,12 +750,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         page = next_page;
         slot0 = next_slot;
       }
-      if (lane == 0) mbar_arrive(&go[(n - 1) % kGo]);  // there is no K after the last V
+      // There is no K after the last V. (In a pair the warp of V says so: that of K is ahead, and the barrier may still
+      // be that of key tile n - 1 - kGo.)
+      if (kLast == 1 && lane == 0) mbar_arrive(&go[(n - 1) % kGo]);
+    };
+    using Is = std::true_type;
+    using No = std::false_type;
+    using K = std::integral_constant<int, 0>;
+    using V = std::integral_constant<int, 1>;
+    if (warp == 8) {
+      if constexpr (T) {
+        if (pair)
+          copy_tiles(Is(), K(), K());
+        else
+          copy_tiles(No(), K(), V());
+      } else {
+        copy_tiles(No(), K(), V());
+      }
+    } else if (T && pair && warp == 10) {
+      copy_tiles(Is(), V(), V());
     } else if (warp == 9 && clean) {
       wait(tail, 0u);
       __syncwarp();
       const int u = 2 * n - 1, to = (valid + rows - 1) / rows * rows;
-      unsigned char* const tile = smem + L::kRing + (u % L::kStages) * L::kTile;
+      unsigned char* const tile = smem + (ring_tile<DP>(sbase, pair ? u % L::kPairStages : u % L::kStages) - sbase);
       for (int e = valid * 8 + lane; e < to * 8; e += 32)
 #pragma unroll
         for (int b = 0; b < L::kBlocks; ++b)
@@ -736,39 +865,82 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         tc_commit(&sfull[t]);
       };
-      wait(kfirst, 0u);
-      for (int t = 0; t < tiles; ++t) {
-        wait(&qfull[t], 0u);
-        product_s(t, 0);
-      }
-      tc_commit(&empty[0]);
-#pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        const int uv = 2 * i + 1, uk = 2 * i + 2;
-        const uint64_t vd = desc_n_major(ring + uint32_t(uv % L::kStages) * L::kTile, L::kBlock);
-        for (int t = 0; t < tiles; ++t) {
-          if (t == 0)
-            wait(&go[i % kGo], uint32_t(i / kGo) & 1u);
-          else
-            wait(psecond, uint32_t(i) & 1u);
-          tc_fence_after();
+      // Key tiles that take turns: S of the next but one follows O += P V of one.
+      if constexpr (T && kTma) {
+        if (pair) {
+          constexpr int kStages = L::kPairStages;
+          auto pair_s = [&](int i) {
+            const int slot = 2 * i % kStages;
+            wait(&kfirst[i % kKeys], uint32_t(i / kKeys) & 1u);
+            tc_fence_after();
+            const uint64_t qd = desc_k_major(sbase), kd = desc_k_major(ring_tile<DP>(sbase, slot));
 #pragma unroll
-          for (int s = 0; s < kTileKeys / 16; ++s)  // 16 keys: two groups of eight rows
-            mma_ts(tbase + 256u + uint32_t(t) * 128u, tbase + uint32_t(t) * 128u + 8u * s,
-                   vd + uint64_t(s * (2048 >> 4)), kIdO, (i > 0 || s > 0) ? 1u : 0u);
-          const bool end = t + 1 == tiles;
-          if (end) tc_commit(&empty[uv % L::kStages]);
-          if (i + 1 < n) {
-            product_s(t, uk);
-            if (end) tc_commit(&empty[uk % L::kStages]);
-          } else {
-            tc_commit(&sfull[t]);
+            for (int s = 0; s < DP / 16; ++s) {
+              const uint64_t step = uint64_t((s >> 2) * (L::kBlock >> 4) + (s & 3) * 2);
+              mma_ss(tbase + uint32_t(i & 1) * 128u, qd + step, kd + step, kIdS, s > 0 ? 1u : 0u);
+            }
+            tc_commit(&sfull[i & 1]);
+            tc_commit(&empty[slot]);
+          };
+          wait(&qfull[0], 0u);
+          pair_s(0);
+          pair_s(1);
+#pragma unroll 1
+          for (int i = 0; i < n; ++i) {
+            const int slot = (2 * i + 1) % kStages;
+            const uint32_t t = uint32_t(i & 1) * 128u;
+            const uint64_t vd = desc_n_major(ring_tile<DP>(sbase, slot), L::kBlock);
+            wait(&go[i % kGo], uint32_t(i / kGo) & 1u);
+            tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < kTileKeys / 16; ++s)
+              mma_ts(tbase + 256u + t, tbase + t + 8u * s, vd + uint64_t(s * (2048 >> 4)), kIdO,
+                     (i > 1 || s > 0) ? 1u : 0u);
+            tc_commit(&empty[slot]);
+            if (i + 2 < n)
+              pair_s(i + 2);
+            else
+              tc_commit(&sfull[i & 1]);
           }
+          const int end = 2 * n - 1;
+          ok = mbar_wait_counted(&empty[end % kStages], uint32_t(end / kStages) & 1u) && ok;
         }
       }
-      // The ring's last tiles: every product is done before the memory is given back.
-      const int last = 2 * n - 1;
-      ok = mbar_wait_counted(&empty[last % L::kStages], uint32_t(last / L::kStages) & 1u) && ok;
+      if (!pair) {
+        wait(kfirst, 0u);
+        for (int t = 0; t < tiles; ++t) {
+          wait(&qfull[t], 0u);
+          product_s(t, 0);
+        }
+        tc_commit(&empty[0]);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+          const int uv = 2 * i + 1, uk = 2 * i + 2;
+          const uint64_t vd = desc_n_major(ring + uint32_t(uv % L::kStages) * L::kTile, L::kBlock);
+          for (int t = 0; t < tiles; ++t) {
+            if (t == 0)
+              wait(&go[i % kGo], uint32_t(i / kGo) & 1u);
+            else
+              wait(psecond, uint32_t(i) & 1u);
+            tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < kTileKeys / 16; ++s)  // 16 keys: two groups of eight rows
+              mma_ts(tbase + 256u + uint32_t(t) * 128u, tbase + uint32_t(t) * 128u + 8u * s,
+                     vd + uint64_t(s * (2048 >> 4)), kIdO, (i > 0 || s > 0) ? 1u : 0u);
+            const bool end = t + 1 == tiles;
+            if (end) tc_commit(&empty[uv % L::kStages]);
+            if (i + 1 < n) {
+              product_s(t, uk);
+              if (end) tc_commit(&empty[uk % L::kStages]);
+            } else {
+              tc_commit(&sfull[t]);
+            }
+          }
+        }
+        // The ring's last tiles: every product is done before the memory is given back.
+        const int last = 2 * n - 1;
+        ok = mbar_wait_counted(&empty[last % L::kStages], uint32_t(last / L::kStages) & 1u) && ok;
+      }
     }
     __syncwarp();
   }
@@ -776,7 +948,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // After a wait that ran out, tensor copies may still be in flight: wait for
   // them, with the same bound, before the shared memory is given back.
   if (__syncthreads_or(!ok) && kTma && tid == 0)
-    for (int i = n > kGo ? n - kGo : 0; i < n; ++i) mbar_wait_counted(&go[i % kGo], uint32_t(i / kGo) & 1u);
+    for (int i = n > kGo ? n - kGo : 0; i < n; ++i) {
+      mbar_wait_counted(&go[i % kGo], uint32_t(i / kGo) & 1u);
+      if (pair) mbar_wait_counted(&kfirst[i % kKeys], uint32_t(i / kKeys) & 1u);
+    }
   tc_fence_before();
   __syncthreads();
   if (warp == 12) {
