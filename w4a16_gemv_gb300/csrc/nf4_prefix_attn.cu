@@ -793,7 +793,7 @@ int sms_for_own(const PrefixArgs& p, int64_t own_items, int64_t tiles, int64_t p
 //     2 trees of 8 over 300 + 60 keys (12 heads over 2): 10.4 us, 16 on two kernels;
 //   * everything on the tcgen05 kernel in one launch: 6.5 of start and end per item and 1 per
 //     tile (1.75 with more than 128 rows; 0.8 of that at 64 elements), in the ranges that end
-//     soonest, or the bytes at 6.3 TB/s. One tree of 25 over 50000 keys of 32 heads: 129 us,
+//     soonest, or the bytes at 6.3 TB/s. One tree of 25 over 50000 keys of 32 heads: 124 us,
 //     213 on 16-row tiles; 37 trees of up to 13 over 777 + 500 keys in pages of 24: 18, 22 on
 //     64-row tiles;
 //   * up to 16 rows of a sequence: own keys on 16-row tiles, at about 5.5 TB/s (up to

@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       if (stride == 1) {
-        const bool joins = a.fused && a.splits > 0;
+        const bool joins = !T && a.fused && a.splits > 0;  // (trees' own items never do)
         float2 shared = make_float2(-INFINITY, 0.0f);  // the row's shared keys: maximum and sum,
         float4 z[8];                                   // and 32 columns of their output, of the rows in dst
         auto shared_part = [&](int c) {
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const bool any = l > 0.0f || l != l;
         const float inv = any ? 1.0f / l : 0.0f;
         const float bad = ok ? 0.0f : __uint_as_float(0x7fc00000u);
-        if (a.fused) {
+        if (!T && a.fused) {
           own *= inv;
           other *= inv;
 #pragma unroll 1
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               if (dst[j] && col < a.dim) *reinterpret_cast<uint2*>(dst[j] + col * 2) = y[j];
           }
         }
-        const int passes = a.fused ? 0 : a.direct ? DP / 64 : DP / 32;
+        const int passes = !T && a.fused ? 0 : a.direct ? DP / 64 : DP / 32;
         float o[32];
         if (!a.direct) tmem_ld32(o_col, o);
 #pragma unroll 1
@@ -657,7 +657,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               tmem_ld32(o_col + 64u * c + 32u * h, o);
               tmem_ld_wait(o, 32);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) w[16 * h + j] = H::down2(o[2 * j] * inv + bad, o[2 * j + 1] * inv + bad);
+              for (int j = 0; j < 16; ++j)
+                w[16 * h + j] = T && !any ? H::down2(bad, bad)
+                                          : H::down2(o[2 * j] * inv + bad, o[2 * j + 1] * inv + bad);
             }
           }
           __syncwarp();  // the stage's last pass has been read
