@@ -145,6 +145,15 @@ def test_everything_at_once(dtype, counts, vocab):
     assert lib().nf4_device_error_flags() == 0
 
 
+@pytest.mark.parametrize("bias", [1, 3, 5, 7, 33, 1023])
+@pytest.mark.parametrize("history", [None, 1, 235, 3000])
+def test_bias_lists_of_any_length(bias, history):
+    """(what lies behind the list in shared memory is read 16 bytes at a time)"""
+    c = Case([1] * 9 + [6], 1307, "bf16" if bias % 4 == 1 else "fp32", seed=bias, history=history, bias=bias)
+    c.check(c.run(), close=bias < 100)
+    assert lib().nf4_device_error_flags() == 0
+
+
 @pytest.mark.parametrize("parts", [dict(history=None), dict(bias=None), dict(mask=False), dict(draft=False),
                                    dict(penalties=False), dict(history=None, draft=False), dict(history=None, bias=None, draft=False),
                                    dict(history=None, bias=None, draft=False, mask=False, penalties=False),

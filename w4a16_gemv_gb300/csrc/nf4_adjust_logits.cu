@@ -156,14 +156,14 @@ __global__ void __launch_bounds__(kThreads, kResident) adjust_logits_kernel(cons
   using S = typename E::Store;
   constexpr int V = kVector ? 16 / int(sizeof(S)) : 1;
   const nf4_adjust_logits_args& a = p.a;
-  extern __shared__ __align__(16) uint32_t words[];  // of the CTA's tokens; then their bits, the bias list, the listed tokens
+  extern __shared__ __align__(16) uint32_t words[];  // of the CTA's tokens; then their bits, the listed tokens, the bias list
   __shared__ uint64_t s_best[kMostRows];             // of the rows, in this CTA,
   __shared__ uint64_t s_all[8][kMostRows];           // and (in the cluster's first) in all
   __shared__ int s_listed;
   uint32_t* const bits = words + p.slice / W::kPerWord;
-  int* const s_bias = reinterpret_cast<int*>(bits + p.slice / 32);
+  uint32_t* const s_list = bits + p.slice / 32;  // (16-byte aligned: slices are whole blocks; a bias list is any length)
+  int* const s_bias = reinterpret_cast<int*>(s_list + kList);
   float* const s_value = reinterpret_cast<float*>(s_bias + a.bias_width);
-  uint32_t* const s_list = reinterpret_cast<uint32_t*>(s_value + a.bias_width);
   int* const s_stage = reinterpret_cast<int*>(s_list) + (threadIdx.x >> 5) * (kSteps * 128 + kQueue);
   uint32_t* const s_queue = reinterpret_cast<uint32_t*>(s_stage + kSteps * 128);
   const int tid = threadIdx.x;
