@@ -112,7 +112,7 @@ NF4_API nf4_status nf4_tree_attention(const nf4_tree_attention_args* args, void*
 typedef struct nf4_adjust_logits_args {
   const void* logits;          /* [rows][vocab] of dtype */
   int64_t logits_stride;       /* elements between rows */
-  void* out;                   /* [rows][vocab] of dtype; may be logits (same stride) */
+  void* out;                   /* [rows][vocab] of dtype; may be logits (same stride), else shares no element with it */
   int64_t out_stride;
   int32_t* best;               /* NULL, or [rows]: index of each row's largest output */
   int64_t rows;                /* 0 .. 2^20 */

@@ -164,6 +164,14 @@ def test_refusals(lib, name, status, cases):
         assert call(lib, name, **kw) == status, kw
 
 
+def test_adjusted_logits_over_other_rows_are_refused(lib):
+    """out is logits itself, or shares no element with it."""
+    for kw in (dict(out=A + 4), dict(out=A - 4), dict(out=A + 4 * 5000 - 4), dict(out_stride=2000), dict(logits_stride=0),
+               dict(out=A + 4 * 1000), dict(rows=1, out=A + 4), dict(vocab=600, out=A + 4 * 500),
+               dict(vocab=500, out=A + 4 * 501), dict(vocab=500, out=A + 4 * 499), dict(vocab=400, out=A + 4 * 500, out_stride=1001)):
+        assert call(lib, "nf4_adjust_logits", **kw) == ERR_SIZE, kw
+
+
 def test_calls_without_work(lib):
     assert call(lib, "nf4_kv_pages", batch=0, tokens=0) == OK
     assert call(lib, "nf4_tree_attention", tokens=0, tree_mask=0) == OK

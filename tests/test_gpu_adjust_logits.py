@@ -154,6 +154,17 @@ def test_bias_lists_of_any_length(bias, history):
     assert lib().nf4_device_error_flags() == 0
 
 
+def test_logits_and_outputs_are_columns_of_one_buffer():
+    c = Case([1, 3], 500, "bf16", seed=12)
+    want = c.run()
+    both = torch.cat((c.logits, torch.zeros_like(c.logits)), 1)
+    c.logits = both[:, :500]
+    got = c.run(out=both[:, 500:])
+    assert torch.equal(got[0].view(torch.int16), want[0].view(torch.int16)) and torch.equal(got[1], want[1])
+    with pytest.raises(lib().NF4Error, match="INVALID_SIZE"):
+        c.run(out=both[:, 499:999])
+
+
 @pytest.mark.parametrize("parts", [dict(history=None), dict(bias=None), dict(mask=False), dict(draft=False),
                                    dict(penalties=False), dict(history=None, draft=False), dict(history=None, bias=None, draft=False),
                                    dict(history=None, bias=None, draft=False, mask=False, penalties=False),

@@ -21,6 +21,19 @@ bool in(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
 // Rows of `width` elements that are written lie apart.
 bool apart(int64_t rows, int64_t stride, int64_t width) { return rows <= 1 || stride >= width; }
 
+// Rows of `width` elements read at `in` and written at `out` share no byte, or are the same rows.
+bool apart_or_same(const void* in, int64_t in_stride, const void* out, int64_t out_stride, int64_t rows, int64_t width,
+                   int64_t size) {
+  const uintptr_t i = reinterpret_cast<uintptr_t>(in), o = reinterpret_cast<uintptr_t>(out);
+  if (i == o && (rows <= 1 || in_stride == out_stride)) return true;
+  const uintptr_t i_end = i + uintptr_t(((rows - 1) * in_stride + width) * size);
+  const uintptr_t o_end = o + uintptr_t(((rows - 1) * out_stride + width) * size);
+  if (i_end <= o || o_end <= i) return true;
+  if (rows <= 1 || in_stride != out_stride) return false;
+  const uintptr_t step = uintptr_t(in_stride * size), off = (o > i ? o - i : i - o) % step;  // columns of one buffer
+  return off >= uintptr_t(width * size) && step - off >= uintptr_t(width * size);
+}
+
 cudaStream_t on(nf4_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 nf4_status check_tree(const nf4_tree_attention_args& a) {
@@ -97,6 +110,7 @@ nf4_status nf4_adjust_logits(const nf4_adjust_logits_args* args, nf4_stream_t st
                 a.bias_tokens, a.bias_values, a.mask, a.mask_rows, a.draft_tokens) ||
       !aligned(a.tree_mask, 8))
     return NF4_ERR_MISALIGNED;
+  if (!apart_or_same(a.logits, a.logits_stride, a.out, a.out_stride, a.rows, a.vocab, int64_t(size))) return NF4_ERR_INVALID_SIZE;
   return nf4::status_of(nf4::launch_adjust_logits(a, on(stream)));
 }
 
