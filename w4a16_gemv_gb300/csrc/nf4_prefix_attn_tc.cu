@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < kGo; ++i) mbar_init(&go[i], 4 + 2 * kLoaders);
-    for (int i = 0; i < 8; ++i) mbar_init(&empty[i], 1);
-    for (int i = 0; i < kKeys; ++i) mbar_init(&kfirst[i], kLoaders);
+    for (int i = 0; i < (T ? L::kPairStages : L::kStages); ++i) mbar_init(&empty[i], 1);
+    for (int i = 0; i < (T ? kKeys : 1); ++i) mbar_init(&kfirst[i], kLoaders);
     mbar_init(psecond, 4);
     mbar_init(tail, 1);
     for (int i = 0; i < 2; ++i) {
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // (a register, in place of what `pair` follows from: with that kept through the loop two registers spill, and
       // every key tile waits for them)
       int stride = pair ? 2 : 1;
-      asm volatile("" : "+r"(stride));
+      if constexpr (T && kTma) asm volatile("" : "+r"(stride));
       const int row0 = pair ? 0 : tile * kTileRows;  // in a pair this tile's keys are every second 128
       const int r = row0 + (warp & 3) * 32 + lane;
       const int limit = r < it.rows ? min(visible_keys<T>(it, (it.r0 + r) / a.group), it.k1) - it.k0 : 0;
