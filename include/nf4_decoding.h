@@ -198,16 +198,18 @@ typedef struct nf4_tree_commit_args {
  * draft_tokens[y] == targets[x], until there is none or the path has max_path
  * nodes. accepted counts the path's nodes, chosen lists targets along it (the
  * sequence's new tokens, the last of which is the next tree's node 0), new_lens
- * is lens - n + accepted. With caches, the keys and values of the path's node j
- * (own key lens - n + path[j]) move to own key lens - n + j, in every layer; the
- * rejected nodes' slots then hold anything.
+ * is lens - n + accepted, or 0 where that is negative. With caches, the keys and
+ * values of the path's node j (own key lens - n + path[j]) move to own key
+ * lens - n + j, in every layer; the rejected nodes' slots then hold anything.
  * The two caches, and their layers, must not overlap (nor may two sequences share a
  * page that is moved).
  * A sequence without nodes: accepted 0, path and chosen -1, new_lens = lens.
  * A node whose parent is not a node before it is on no path, nor is one past
  * the first 4096 of its sequence; a row whose slot
- * lies on a page out of range, or past the table's width, is not moved; cu_q and
- * lens are clamped; all set bit 1 of the device error flags.
+ * lies on a page out of range, or past the table's width, is not moved; nor is one of
+ * a sequence's first nodes where lens is less than its nodes, so that these have no
+ * own key; cu_q is clamped; all set bit 1 of the device error flags, and so does such
+ * a lens where nothing would move.
  * Fastest when head_dim and the strides are multiples of 8 and the caches
  * 16-byte aligned. One launch.
  * Errors: NF4_ERR_NULL, NF4_ERR_INVALID_SIZE, NF4_ERR_MISALIGNED, NF4_ERR_CUDA.

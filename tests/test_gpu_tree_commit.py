@@ -252,3 +252,25 @@ def test_refusals():
         run(*a, page_table=table, k_cache=c.k, v_cache=c.v, new_lens=a[4])
     with pytest.raises(lib().NF4Error, match="INVALID_SIZE"):
         run(a[0], a[1], a[2], None, a[4], 4)
+
+
+@pytest.mark.parametrize("cache", [False, True], ids=["tokens", "cache"])
+def test_fewer_keys_than_nodes_are_reported(cache):
+    """The first nodes then have no key: new_lens is lens - n + accepted, at least 0, and the sequence is reported, also
+    where nothing moves."""
+    for lens, accepted in (([2, 20], 6), ([5, 6], 6), ([0, 9], 6), ([2, 20], 1)):
+        c = Case([6, 6], seed=3, chain=True, chance=1.0, base=20)
+        for t in c.targets:
+            t[0] = t[0] if accepted == 6 else 777
+        a = list(c.args(8))
+        a[4] = ints(lens)
+        kw = dict(page_table=ints(c.table), k_cache=c.k, v_cache=c.v) if cache else {}
+        before = c.k.clone(), c.v.clone()
+        got = lib().nf4_tree_commit(*a, **kw)
+        assert got[0].tolist() == [accepted] * 2
+        assert got[3].tolist() == [max(0, n - 6 + accepted) for n in lens]
+        assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip((c.k, c.v), before))
+        assert lib().nf4_device_error_flags() == 2, lens
+        a[4] = ints([6, 20])
+        lib().nf4_tree_commit(*a, **kw)
+        assert lib().nf4_device_error_flags() == 0

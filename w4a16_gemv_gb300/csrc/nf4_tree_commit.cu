@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_cons
     if (tid == 0) {
       a.accepted[b] = n;
       a.new_lens[b] = max(base + n, 0);
-      bad = bad || given_len < 0;
+      bad = bad || given_len < hi - lo;  // (also where it is negative)
     }
   }
   if (a.layers > 0 && n > 0) {
