@@ -274,3 +274,17 @@ def test_fewer_keys_than_nodes_are_reported(cache):
         a[4] = ints([6, 20])
         lib().nf4_tree_commit(*a, **kw)
         assert lib().nf4_device_error_flags() == 0
+
+
+def test_tables_without_a_page():
+    """A table of no columns holds no row: what would move stays, and is reported; where nothing moves, nothing is."""
+    for moves in (True, False):
+        c = Case([6, 6], seed=3, chain=True, chance=1.0, base=20)
+        if moves:
+            c.parents = [[-1, 0, 0, 2, 2, 4]] * 2
+            c.draft, c.targets = [[0, 1, 2, 3, 4, 5]] * 2, [[2, 0, 4, 0, 5, 9]] * 2
+        before = c.k.clone(), c.v.clone()
+        got = lib().nf4_tree_commit(*c.args(8), page_table=ints([]).view(2, 0), k_cache=c.k, v_cache=c.v)
+        assert got[0].tolist() == ([4, 4] if moves else [6, 6])
+        assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip((c.k, c.v), before))
+        assert lib().nf4_device_error_flags() == (2 if moves else 0)

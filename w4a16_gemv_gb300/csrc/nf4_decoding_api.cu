@@ -140,7 +140,7 @@ nf4_status nf4_tree_commit(const nf4_tree_commit_args* args, nf4_stream_t stream
     return NF4_ERR_MISALIGNED;
   if (moves && a.new_lens == a.lens) return NF4_ERR_INVALID_SIZE;  // other blocks read lens while it is written
   nf4_tree_commit_args c = a;
-  if (!moves || a.width == 0 || a.num_pages == 0) c.layers = 0;
+  if (!moves) c.layers = 0;  // (with no page, or a table of no columns, every row that would move is reported)
   return nf4::status_of(nf4::launch_tree_commit(c, on(stream)));
 }
 
