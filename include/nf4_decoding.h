@@ -201,8 +201,11 @@ typedef struct nf4_tree_commit_args {
  * is lens - n + accepted, or 0 where that is negative. With caches, the keys and
  * values of the path's node j (own key lens - n + path[j]) move to own key
  * lens - n + j, in every layer; the rejected nodes' slots then hold anything.
- * The two caches, and their layers, must not overlap (nor may two sequences share a
- * page that is moved).
+ * The two caches, and their layers, pages, slots and heads, must not overlap (nor may
+ * two sequences share a page that is moved). Of such caches this call refuses equal
+ * base pointers and strides of 0 of a dimension of more than one; the rest is the
+ * caller's to see to. (The Python entry point sees how large its tensors are, and
+ * refuses any that share an element.)
  * A sequence without nodes: accepted 0, path and chosen -1, new_lens = lens.
  * A node whose parent is not a node before it is on no path, nor is one past
  * the first 4096 of its sequence; a row whose slot

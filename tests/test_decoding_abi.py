@@ -172,6 +172,15 @@ def test_adjusted_logits_over_other_rows_are_refused(lib):
         assert call(lib, "nf4_adjust_logits", **kw) == ERR_SIZE, kw
 
 
+def test_caches_whose_rows_are_at_two_indices_are_refused(lib):
+    """A stride of 0 of a dimension of more than one; of one element it is not used."""
+    for cache in "kv":
+        for dim, one in (("layer", "layers"), ("page", "num_pages"), ("slot", "page_size"), ("head", "k_heads")):
+            kw = {f"{cache}_{dim}_stride": 0}
+            assert call(lib, "nf4_tree_commit", **kw) == ERR_SIZE, kw
+            assert call(lib, "nf4_tree_commit", batch=0, **kw, **{one: 1}) == OK, kw
+
+
 def test_calls_without_work(lib):
     assert call(lib, "nf4_kv_pages", batch=0, tokens=0) == OK
     assert call(lib, "nf4_tree_attention", tokens=0, tree_mask=0) == OK

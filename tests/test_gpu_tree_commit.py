@@ -288,3 +288,53 @@ def test_tables_without_a_page():
         assert got[0].tolist() == ([4, 4] if moves else [6, 6])
         assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip((c.k, c.v), before))
         assert lib().nf4_device_error_flags() == (2 if moves else 0)
+
+
+def one_buffer(shape, dt=torch.bfloat16):
+    return torch.randint(-2 ** 15, 2 ** 15, shape, device="cuda", dtype=torch.int16).view(dt)
+
+
+def test_caches_of_one_buffer():
+    """Keys and values side by side, whichever dimension divides them, in one buffer."""
+    base = Case([12, 30, 1], seed=7, layers=3)
+    layers, pool, page, heads, dim = base.k.shape
+    sides = [one_buffer((2, *base.k.shape)).unbind(0), one_buffer((layers, 2, *base.k.shape[1:])).unbind(1),
+             one_buffer((layers, pool, 2, page, heads, dim)).unbind(2),
+             one_buffer((layers, pool, page, 2, heads, dim)).unbind(3), one_buffer((layers, pool, page, heads, 2, dim)).unbind(4),
+             one_buffer((layers, pool, page, heads, 2 * dim)).split(dim, -1),
+             one_buffer((pool, 2, layers, page, heads, dim)).transpose(0, 2).unbind(1)]
+    other = one_buffer((layers, 2, pool * page * heads * dim))  # the layers alike, the heads of one in front of its slots
+    sides.append((other[:, 0].view(base.k.shape), other[:, 1].view(layers, pool, heads, page, dim).transpose(2, 3)))
+    for k, v in sides:
+        for first, second in ((k, v), (v, k)):
+            c = Case([12, 30, 1], seed=7, layers=3)
+            c.k, c.v = first, second
+            c.check(8)
+
+
+def test_caches_that_overlap_are_refused():
+    c = Case([12, 30, 1], seed=7, layers=3)
+    layers, pool, page, heads, dim = c.k.shape
+    args, table = c.args(8), ints(c.table)
+    wide = one_buffer((layers + 1, pool + 1, page, heads, 2 * dim))
+    flat = one_buffer((layers * pool * page * heads * dim + 64,))
+
+    def shifted(by):
+        return flat[by:by + 64 * (flat.numel() // 64 - 1)].view(c.k.shape)
+    pairs = [(c.k, c.k), (c.k, c.v[:, :, :, :1].expand_as(c.k)), (c.k[:1].expand_as(c.k), c.v),
+             (c.k[:, :1].expand_as(c.k), c.v), (c.k[:, :, :1].expand_as(c.k), c.v),
+             (wide[:layers, :pool, ..., :dim], wide[:layers, :pool, ..., dim - 1:2 * dim - 1]),
+             (wide[:layers, :pool, ..., :dim], wide[:layers, 1:, ..., :dim]), (wide[:layers, :pool, ..., :dim], wide[1:, :pool, ..., :dim]),
+             (shifted(0), shifted(1)), (shifted(64), shifted(0)),
+             (flat.as_strided(c.k.shape, (pool * page * heads * dim // 2, page * heads * dim, heads * dim, dim, 1)), c.v),
+             (wide[:layers, :pool, ..., :dim], wide[1:, 1:, ..., :dim])]
+    for i, (k, v) in enumerate(pairs):
+        before = k.clone(), v.clone()
+        with pytest.raises((ValueError, lib().NF4Error), match="overlap|INVALID_SIZE"):
+            lib().nf4_tree_commit(*args, page_table=table, k_cache=k, v_cache=v)
+        assert torch.equal(k.view(torch.int16), before[0].view(torch.int16)), i
+        assert torch.equal(v.view(torch.int16), before[1].view(torch.int16)), i
+    # of a dimension of one element the stride says nothing
+    one = Case([12, 30], seed=7, heads=1, layers=1)
+    one.k = one.k.as_strided(one.k.shape, (0, *one.k.stride()[1:3], 0, 1))
+    one.check(8)

@@ -85,6 +85,50 @@ const uint64_t* bits(PyObject* o, const char* name, int64_t rows, c10::DeviceInd
   return static_cast<const uint64_t*>(t.data_ptr());
 }
 
+// The dimensions of more than one element, the largest stride first.
+struct Dims {
+  int64_t stride[5], size[5], extent[5];  // extent: elements from the first to the last of this dimension and those behind it
+  int n = 0;
+  int64_t from(int i) const { return i < n ? extent[i] : 1; }
+};
+// False where two indices of the tensor may be one address: strides that do not nest.
+bool nested(const at::Tensor& t, Dims* d) {
+  for (int64_t i = 0; i < t.dim(); ++i) {
+    if (t.size(i) <= 1) continue;
+    int at = d->n++;
+    for (; at > 0 && d->stride[at - 1] < t.stride(i); --at) {
+      d->stride[at] = d->stride[at - 1];
+      d->size[at] = d->size[at - 1];
+    }
+    d->stride[at] = t.stride(i);
+    d->size[at] = t.size(i);
+  }
+  for (int i = d->n - 1; i >= 0; --i) {
+    if (d->stride[i] < d->from(i + 1)) return false;
+    d->extent[i] = d->stride[i] * (d->size[i] - 1) + d->from(i + 1);
+  }
+  return true;
+}
+// Whether elements of a, and of b `off` elements on, may meet. A dimension that both have (a stacked cache's layers) is taken
+// apart; what is left meets where its ranges do.
+bool may_meet(const Dims& a, const Dims& b, int i, int64_t off) {
+  if (off >= a.from(i) || -off >= b.from(i)) return false;
+  if (i >= a.n || i >= b.n || a.stride[i] != b.stride[i] || a.size[i] != b.size[i]) return true;
+  const int64_t s = a.stride[i], low = off >= 0 ? off / s : -((s - 1 - off) / s);
+  for (int64_t d = low; d <= low + 1; ++d)  // (what is inside is no longer than the stride)
+    if (d < a.size[i] && -d < a.size[i] && may_meet(a, b, i + 1, off - d * s)) return true;
+  return false;
+}
+void check_apart(const at::Tensor& k, const at::Tensor& v) {
+  if (k.numel() == 0) return;
+  Dims a, b;
+  if (!nested(k, &a) || !nested(v, &b)) throw ValueError("k_cache and v_cache must not overlap themselves");
+  const int64_t bytes = static_cast<char*>(v.data_ptr()) - static_cast<char*>(k.data_ptr()), size = int64_t(k.element_size());
+  const int64_t off = bytes >= 0 ? bytes / size : -((size - 1 - bytes) / size);
+  if (may_meet(a, b, 0, off) || (bytes % size != 0 && may_meet(a, b, 0, off + 1)))
+    throw ValueError("k_cache and v_cache must not overlap");
+}
+
 PyObject* py_kv_pages(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
   return guarded([&]() -> PyObject* {
     static const char* const kNames[] = {"lens",      "page_table", "held",      "free_pages", "free_count",     "page_size",
@@ -301,6 +345,7 @@ PyObject* py_tree_commit(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyO
       if (type != at::kBFloat16 && type != at::kHalf) throw TypeError("k_cache must be bf16 or fp16");
       check(kc, "k_cache", type, kc.sizes(), dev, false);
       check(vc, "v_cache", type, kc.sizes(), dev, false);
+      check_apart(kc, vc);
       const int64_t o = d - 4;
       a.layers = d == 5 ? kc.size(0) : 1;
       a.num_pages = kc.size(o);
@@ -374,9 +419,9 @@ PyMethodDef kDecodingMethods[] = {
      "accepted=None, path=None, chosen=None, new_lens=None, stream=None)\n--\n\n"
      "Walks each sequence's drafted tree (parents, draft_tokens, the model's targets: int32 [tokens]) from node 0 along the\n"
      "nodes that hold the model's choice, and moves the accepted nodes' keys and values to their places behind the cached\n"
-     "ones (caches [pages, page_size, kv_heads, dim], or [layers, ...] of them). lens int32 [batch] counts the own keys\n"
-     "with all nodes. Returns (accepted, path, chosen, new_lens): int32 [batch], [batch, max_path] twice (-1 behind the\n"
-     "last), [batch]."},
+     "ones (caches [pages, page_size, kv_heads, dim], or [layers, ...] of them, that share no element; of one buffer where\n"
+     "their views interleave alike). lens int32 [batch] counts the own keys with all nodes. Returns (accepted, path, chosen,\n"
+     "new_lens): int32 [batch], [batch, max_path] twice (-1 behind the last), [batch]."},
     {nullptr, nullptr, 0, nullptr}};
 
 }  // namespace nf4_binding

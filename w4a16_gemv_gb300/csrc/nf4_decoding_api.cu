@@ -127,7 +127,13 @@ nf4_status nf4_tree_commit(const nf4_tree_commit_args* args, nf4_stream_t stream
     for (const int64_t s : {a.k_layer_stride, a.k_page_stride, a.k_slot_stride, a.k_head_stride, a.v_layer_stride,
                             a.v_page_stride, a.v_slot_stride, a.v_head_stride})
       if (!in(s, 0, kMaxStride)) return NF4_ERR_INVALID_SIZE;
-    if (a.layers > 1 && (a.k_layer_stride == 0 || a.v_layer_stride == 0)) return NF4_ERR_INVALID_SIZE;  // moved twice
+    // a row at two indices would be moved twice, beside itself
+    const int64_t sizes[] = {a.layers, a.num_pages, a.page_size, a.k_heads};
+    const int64_t strides[][4] = {{a.k_layer_stride, a.k_page_stride, a.k_slot_stride, a.k_head_stride},
+                                  {a.v_layer_stride, a.v_page_stride, a.v_slot_stride, a.v_head_stride}};
+    for (const auto& of : strides)
+      for (int i = 0; i < 4; ++i)
+        if (sizes[i] > 1 && of[i] == 0) return NF4_ERR_INVALID_SIZE;
     if (a.k_cache && a.k_cache == a.v_cache) return NF4_ERR_INVALID_SIZE;  // both would be moved, beside one another
   }
   if (a.batch == 0) return NF4_OK;
