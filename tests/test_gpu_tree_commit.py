@@ -338,3 +338,38 @@ def test_caches_that_overlap_are_refused():
     one = Case([12, 30], seed=7, heads=1, layers=1)
     one.k = one.k.as_strided(one.k.shape, (0, *one.k.stride()[1:3], 0, 1))
     one.check(8)
+
+
+def moving(c, moves):
+    """Gives sequence b a tree whose accepted branch lies moves[b] rows (of moves[b] + 2 nodes) behind a rejected first
+    child: all of its nodes but node 0 move by one."""
+    for b, m in enumerate(moves):
+        n = c.counts[b]
+        assert n == m + 2
+        c.parents[b] = [-1, 0] + [0 if x == 2 else x - 1 for x in range(2, n)]
+        c.draft[b] = [900 + x for x in range(n)]
+        c.targets[b] = [c.draft[b][x + 1] for x in range(n - 1)] + [7]
+        if n > 2:
+            c.targets[b][0] = c.draft[b][2]
+        else:
+            c.targets[b][0] = 7
+    return c
+
+
+@pytest.mark.parametrize("batch,heads,dim,layers", [(130, 8, 128, 7), (300, 2, 64, 7), (460, 1, 64, 9), (1000, 1, 20, 3)])
+@pytest.mark.parametrize("moves", [[1], [3], [8], [9], [0, 1, 3, 8, 9, 17, 5]], ids=str)
+def test_blocks_of_several_layers(batch, heads, dim, layers, moves):
+    """More sequences than there are places for a block of each layer (152 SMs of six): a block takes several layers, whose
+    rows follow one another in rounds of eight, and the last block of a sequence fewer."""
+    moves = [moves[b % len(moves)] for b in range(batch)]
+    c = moving(Case([m + 2 for m in moves], seed=batch, heads=heads, dim=dim, layers=layers, base=40), moves)
+    got = c.check(32)
+    assert got[0].tolist() == [m + 1 for m in moves]
+
+
+@pytest.mark.parametrize("offset", [0, 3])
+@pytest.mark.parametrize("layers", [None, 2])
+def test_more_columns_than_blocks(offset, layers):
+    """32768 elements of a row one by one, and 4096 chunks of it: a sequence has 64 blocks of 128 threads at most."""
+    c = moving(Case([11, 2, 3], seed=5, heads=32, dim=512, layers=layers, offset=offset), [9, 0, 1])
+    c.check(16)
