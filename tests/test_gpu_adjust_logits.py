@@ -354,3 +354,104 @@ def test_refusals():
             run(x, **kw)
     with pytest.raises(TypeError, match="bf16, fp16 or fp32"):
         run(x.double())
+
+
+def layout(c, rows, offset):
+    """Random logits for the case, their rows on 16-byte boundaries ("aligned"), at the same distance from one ("alike": an
+    odd row length is not a whole number of chunks) or one after another ("dense"); and an output laid out alike."""
+    dtype, vocab = DTYPES[c.dtype], c.vocab
+    stride = vocab if offset is None else -(-vocab // 8) * 8 + 8
+    at = offset or 0
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    wide = (torch.randn(2, rows, stride, device="cuda", generator=g) * 3).to(dtype)
+    c.logits = wide[0, :, at:at + vocab]
+    return wide[1, :, at:at + vocab]
+
+
+def forest(counts, vocab, dtype, history, offset, gap=(0, 0), pool=24, seed=0, bias=5):
+    """A case of many rows whose drafted tokens are few different ones, side by side in pairs, so that the branches of
+    neighbouring rows share tokens and words; the histories hold some of them. gap: rows before and behind the requests'."""
+    c = Case(counts, vocab, dtype, seed=seed, history=history, bias=bias)
+    rng = np.random.default_rng(seed + 1)
+    rows = sum(counts) + sum(gap)
+    first = rng.integers(0, vocab // 2, pool // 2) * 2
+    tokens = np.concatenate((first, first + 1)).astype(np.int32)
+    c.cu = c.cu + np.int32(gap[0])
+    c.h["draft_tokens"] = rng.choice(tokens, rows).astype(np.int32)
+    c.h["tree_mask"] = rng.integers(-2 ** 63, 2 ** 63, (rows, c.h["tree_mask"].shape[1])).astype(np.int64)
+    c.h["mask_rows"] = rng.integers(-1, c.h["mask"].shape[0], rows).astype(np.int32)
+    c.h["history"][:, ::5] = rng.choice(tokens, c.h["history"][:, ::5].shape)
+    for n in ("draft_tokens", "tree_mask", "mask_rows", "history"):
+        c.kw[n] = on_gpu(c.h[n])
+    c.kw["cu_rows"] = on_gpu(c.cu)
+    return c, layout(c, rows, offset)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("vocab,offset", [(1000, 0), (1003, 0), (1003, 3), (1003, None)], ids=["aligned", "odd", "skewed", "dense"])
+def test_many_rows_in_trees(dtype, vocab, offset):
+    """More rows than there are CTAs (two on each of 152 SMs), so that a cluster takes several: from branch to branch of a
+    request, from request to request, and rows that no request holds before and behind them."""
+    counts = [1, 7, 40, 70, 0] * 6
+    c, out = forest(counts, vocab, dtype, 50, offset, gap=(5, 9), seed=vocab)
+    got = c.run()
+    c.check(got)
+    into, best = c.run(out=out)  # rows alike in input and output, 16 bytes at a time
+    assert into is out and torch.equal(into, got[0]) and torch.equal(best, got[1])
+    into, best = c.run(out=c.logits)
+    assert into is c.logits and torch.equal(into, got[0]) and torch.equal(best, got[1])
+    assert lib().nf4_device_error_flags() == 0
+
+
+@pytest.mark.parametrize("dtype,history", [("bf16", 50), ("fp16", 20000), ("fp32", 300), ("fp32", 20000)])
+@pytest.mark.parametrize("vocab,offset", [(20000, 0), (20003, 2)], ids=["aligned", "skewed"])
+def test_many_rows_of_several_ctas(dtype, history, vocab, offset):
+    """Clusters of four CTAs (74 at once, or fewer) with several rows each; words of 16 bits and, for histories past their
+    counts, of 32."""
+    counts = [3, 70, 1, 40, 100, 7]
+    c, out = forest(counts, vocab, dtype, history, offset, seed=history)
+    got = c.run(out=out)
+    c.check(got, rows=[0, 1, 2, 3, 4, 40, 72, 73, 74, 75, 90, 113, 114, 115, 116, 117, 170, 213, 214, 215, 220], close=False)
+    dense = c.run()  # (other offsets of rows modulo 16 bytes)
+    assert torch.equal(dense[0], got[0]) and torch.equal(dense[1], got[1])
+    assert lib().nf4_device_error_flags() == 0
+
+
+def test_many_rows_one_each():
+    """More requests than 64 rows of every cluster, each with a history of its own."""
+    c = Case([1] * 21000, 100, "fp32", seed=2, history=9, bias=3, draft=False)
+    rows = list(range(0, 21000, 97)) + [20999]
+    c.check(c.run(), rows=rows, close=False)
+    assert lib().nf4_device_error_flags() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_more_tokens_than_the_list_holds(dtype):
+    """Every token of a vocabulary in the history: 15000 of each of eight CTAs, whose lists hold 8192."""
+    c = Case([1], 120000, dtype, seed=4, history=200000, draft=False)
+    rng = np.random.default_rng(5)
+    c.h["history"][0] = np.concatenate((rng.permutation(120000), rng.integers(0, 120000, 80000)))
+    c.h["history_lens"][:], c.h["prompt_lens"][:] = 200000, 100000
+    for n in ("history", "history_lens", "prompt_lens"):
+        c.kw[n] = on_gpu(c.h[n])
+    c.check(c.run(), close=False)
+    assert lib().nf4_device_error_flags() == 0
+
+
+@pytest.mark.parametrize("words", [8191, 8180, 16000])
+def test_lists_that_fill_up(words):
+    """So many words of one CTA's blocks (those are dealt out in turn, 256 tokens each, to four) that its list is full, or
+    becomes full as the branches of a tree bring tokens to it."""
+    vocab, counts = 70000, [20] * 8
+    c, out = forest(counts, vocab, "bf16", words, 0, seed=words, pool=2)
+    mine = np.flatnonzero(np.arange(vocab) // 256 % 4 == 1)
+    rng = np.random.default_rng(words)
+    for b in range(len(counts)):
+        c.h["history"][b] = rng.permutation(mine)[:words]
+    c.h["history_lens"][:], c.h["prompt_lens"][:] = words, words // 2
+    c.h["draft_tokens"][:] = rng.choice(mine, len(c.h["draft_tokens"]))
+    for n in ("history", "history_lens", "prompt_lens", "draft_tokens"):
+        c.kw[n] = on_gpu(c.h[n])
+    c.check(c.run(out=out), rows=range(0, 160, 3), close=False)
+    assert lib().nf4_device_error_flags() == 0
