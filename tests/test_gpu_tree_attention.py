@@ -277,6 +277,25 @@ def test_tokens_that_no_sequence_holds(counts):
     d.check(alone)
 
 
+@pytest.mark.parametrize("counts,length", [([6, 9], 21), ([2, 3], 3000), ([100, 70], 21), ([64, 30], 5000), ([200, 130], 700)],
+                         ids=str)
+def test_tokens_that_no_sequence_holds_without_shared_keys(counts, length):
+    """They see no key: zeros and -infinity."""
+    c = Call(12, 2, 128, 0, [n + length for n in counts], counts, seed=8)
+    want = c.run()
+    c.check(want)
+    n = sum(counts)
+    d = Call(12, 2, 128, 0, [m + length for m in counts], counts, seed=8, behind=9)
+    d.q[4:4 + n] = c.q
+    d.mask = torch.cat((d.mask[n:n + 4], c.mask, d.mask[n + 4:]))
+    d.cu_q = c.cu_q + 4
+    out, lse = torch.full_like(d.q, 7.0), torch.full((n + 9, 12), 7.0, device="cuda")
+    d.run(out=out, lse=lse)
+    c.check((out[4:4 + n].contiguous(), lse[4:4 + n].contiguous()))
+    assert not torch.cat((out[:4], out[4 + n:])).any()
+    assert (torch.cat((lse[:4], lse[4 + n:])) == float("-inf")).all()
+
+
 def test_infinities_in_keys_that_are_not_seen():
     """A key of infinities and NaN reaches the rows that see it alone."""
     for n in (6, 40, 150):
@@ -353,6 +372,17 @@ def test_key_tiles_in_turns(dt, hq, hk, dim, page, prefix):
     """Up to 128 rows of a sequence over two key tiles and more: each half of the tiles has a softmax of its own."""
     lens = [129, 130, 200, 240, 241, 256, 257, 384, 385, 500, 640, 641, 900, 1024, 1025, 1150]
     c = Call(hq, hk, dim, prefix, lens, [1 + (7 * b) % 32 for b in range(16)], page=page, dt=dt, seed=page + prefix)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("hq,hk,dim", [(32, 8, 128), (16, 8, 64), (24, 8, 80)])
+@pytest.mark.parametrize("page", [16, 24, 128])
+@pytest.mark.parametrize("prefix", [8000, 8192, 12345])
+@pytest.mark.parametrize("counts", [[8] * 4, [1, 31], [5, 0, 12, 7]], ids=str)
+def test_shared_key_tiles_in_turns(dt, hq, hk, dim, page, prefix, counts):
+    """Up to 128 rows of the whole call over a long shared prefix."""
+    c = Call(hq, hk, dim, prefix, [n + 40 * b for b, n in enumerate(counts)], counts, page=page, dt=dt, seed=page + prefix)
     c.check(c.run())
 
 
