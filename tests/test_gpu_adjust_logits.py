@@ -455,3 +455,24 @@ def test_lists_that_fill_up(words):
         c.kw[n] = on_gpu(c.h[n])
     c.check(c.run(out=out), rows=range(0, 160, 3), close=False)
     assert lib().nf4_device_error_flags() == 0
+
+
+def test_offsets_past_32_bits():
+    """5 G bytes of logits: the last rows are as the same rows by themselves."""
+    rows, vocab, last = 40000, 64001, 25
+    x = torch.empty(rows, vocab, dtype=torch.bfloat16, device="cuda")
+    x.normal_()
+    c = Case([last], vocab, "bf16", seed=1)
+    x[-last:] = c.logits
+    cu = torch.tensor([rows - last, rows], dtype=torch.int32, device="cuda")
+    kw = {k: v for k, v in c.kw.items() if k not in ("cu_rows", "draft_tokens", "tree_mask", "mask_rows")}
+    draft = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    tree = torch.zeros(rows, 1, dtype=torch.int64, device="cuda")
+    mask_rows = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    draft[-last:], tree[-last:], mask_rows[-last:] = c.kw["draft_tokens"], c.kw["tree_mask"], c.kw["mask_rows"]
+    out, best = lib().nf4_adjust_logits(x, cu_rows=cu, draft_tokens=draft, tree_mask=tree, mask_rows=mask_rows, return_best=True, **kw)
+    assert torch.equal(out[:-last], x[:-last])
+    for r in range(0, rows - last, 4999):
+        assert int(best[r]) == int((x[r] == x[r].max()).nonzero()[0])
+    c.check((out[-last:], best[-last:]), close=False)
+    assert lib().nf4_device_error_flags() == 0

@@ -409,6 +409,23 @@ def test_infinities_and_nan_in_one_half_of_the_keys():
     assert lib().nf4_device_error_flags() == 0
 
 
+@pytest.mark.parametrize("prefix,counts,lens", [(300, [8, 5], [60, 41]), (0, [25] * 3, [700, 25, 3000]), (5000, [70, 9], [90, 200])])
+def test_pages_past_32_bits(prefix, counts, lens):
+    """Caches of 4.3 GB, whose last pages are the call's."""
+    c = Call(12, 2, 128, prefix, lens, counts, seed=prefix)
+    want = c.run()
+    pages = 1 << 19
+    pool = c.k.shape[0]
+    big = torch.empty(2, pages, *c.k.shape[1:], dtype=c.k.dtype, device="cuda")
+    big[0, -pool:], big[1, -pool:] = c.k, c.v
+    c.k, c.v = big
+    c.prefix_pages = c.prefix_pages + (pages - pool)
+    c.suffix_pages = torch.where(c.suffix_pages < pool, c.suffix_pages + (pages - pool), c.suffix_pages)
+    got = c.run()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    c.check(got)
+
+
 def test_two_streams_and_workspaces():
     c = Call(12, 2, 128, 2000, [300, 200], [9, 12], seed=5)
     want = c.run()

@@ -373,3 +373,27 @@ def test_more_columns_than_blocks(offset, layers):
     """32768 elements of a row one by one, and 4096 chunks of it: a sequence has 64 blocks of 128 threads at most."""
     c = moving(Case([11, 2, 3], seed=5, heads=32, dim=512, layers=layers, offset=offset), [9, 0, 1])
     c.check(16)
+
+
+def test_offsets_past_32_bits():
+    """Rows that lie 8 GB and more behind the caches' first."""
+    c = moving(Case([11, 4], seed=9, page=16, heads=8, dim=128, layers=3, base=40), [9, 2])
+    pages = 1 << 17  # 4 GB a layer
+    at = {p: pages - 1 - p for row in c.table for p in row if p < c.k.shape[1]}
+    big = torch.empty(2, 3, pages, 16, 8, 128, dtype=torch.bfloat16, device="cuda")
+    small = c.k, c.v
+    c.table = [[at.get(p, p) for p in row] for row in c.table]
+    for new, old in zip(big, small):
+        for p, q in at.items():
+            new[:, q] = old[:, p]
+    args = c.args(16)
+    got = lib().nf4_tree_commit(*args, page_table=ints(c.table), k_cache=big[0], v_cache=big[1])
+    c.table = [[pages - 1 - p if p < pages else p for p in row] for row in c.table]
+    n, path, chosen, lens, k, v = c.want(16)
+    assert [g.tolist() for g in got] == [n, path, chosen, lens]
+    for new, want in zip(big, (k, v)):
+        have = want.clone()
+        for p, q in at.items():
+            have[:, p] = new[:, q]
+        assert torch.equal(c.kept(have, n).contiguous().view(torch.int16), c.kept(want, n).contiguous().view(torch.int16))
+    assert lib().nf4_device_error_flags() == 0
