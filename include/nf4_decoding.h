@@ -103,6 +103,10 @@ NF4_API size_t nf4_tree_attention_workspace_size(const nf4_tree_attention_args* 
  * Everything else is as stated there: rounding, joins in a fixed order,
  * workspaces, error flags; non-finite values in k stay with the rows that see
  * the key, those in v of an own key may also reach other rows of the sequence.
+ * The work is cut up for own keys as many as a row of suffix_pages can hold: wider
+ * tables give the same results, later. One tree of 25 nodes over 4000 keys (32 heads
+ * over 8) takes 13.8 us with a table for 4000 keys, 14.9 for 8192, 25 for 32768 and 40
+ * for 131072.
  * Errors: as nf4_prefix_attention; also NF4_ERR_NULL and NF4_ERR_MISALIGNED (8
  *   bytes) for tree_mask, NF4_ERR_INVALID_SIZE for its words and stride.
  */
@@ -125,7 +129,7 @@ typedef struct nf4_adjust_logits_args {
   int64_t history_stride;
   int64_t history_width;       /* 0 .. 2^28 */
   const int32_t* history_lens; /* [requests]: tokens that count, 0 .. history_width */
-  const int32_t* prompt_lens;  /* NULL (0), or [requests]: how many of these are the prompt */
+  const int32_t* prompt_lens;  /* NULL (0), or [requests]: how many of these are the prompt, from 0; past the last, all */
   const float* repetition;     /* NULL (1), or [requests] */
   const float* frequency;      /* NULL (0), or [requests] */
   const float* presence;       /* NULL (0), or [requests] */
@@ -162,7 +166,13 @@ typedef struct nf4_adjust_logits_args {
  * drafted one's also below 0) are not counted; a mask row at or past mask_count
  * is no mask; lengths and cu_rows are clamped; all set bit 1 of the device error
  * flags.
- * One launch; one pass over the logits. Fastest when rows are 16-byte aligned.
+ * One launch; one pass over the logits. Fastest when the rows of logits and out
+ * are whole numbers of 16 bytes apart. Where rows of a tree differ in their distance from
+ * a 16-byte boundary (rows of odd length one after another), each row goes through the
+ * history again: 16 trees of up to 32 rows of 50257 in bf16 over 3000 words take 75 us,
+ * 51 with rows of 50264. Where rows of out lie otherwise than those of logits (padded
+ * logits, a dense out), elements are moved one by one: 105 us, 51 into an out that is
+ * padded alike, 50 in place.
  * Errors: NF4_ERR_NULL, NF4_ERR_INVALID_SIZE, NF4_ERR_UNSUPPORTED_DTYPE,
  *   NF4_ERR_MISALIGNED (a pointer not aligned to its element), NF4_ERR_CUDA.
  */

@@ -17,9 +17,9 @@
 // division and the bias list for each of its chunks.
 // The logits are read and written once: memory bounds many rows, a chain of loads
 // (offsets, lengths, history) a few. Without a context 64 rows of 128000 in bf16 take
-// 5.7 us and 384 in binary32 65 (5.9 and 6.0 TB/s); with masks, best tokens and 8000 (3000)
-// words of history each 24 and 108, bound by instructions (a quarter of them picks
-// words) and by the latencies between a row's stream and its listed tokens.
+// 5.6 us and 384 in binary32 66 (5.9 and 6.0 TB/s); with masks, best tokens and 8000 (3000)
+// words of history each 24 and 108, bound by instructions (1200 of 3250 per warp are the
+// history's) and by the latencies between a row's stream and its listed tokens.
 #include "nf4_decoding.cuh"
 #include "nf4_prefix_attn.cuh"  // 16-byte asynchronous copies
 

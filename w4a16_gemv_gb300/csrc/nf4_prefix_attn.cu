@@ -790,15 +790,17 @@ int sms_for_own(const PrefixArgs& p, int64_t own_items, int64_t tiles, int64_t p
 // taken; "units" are 64 keys of a tile of 64 rows, "tiles" whole key tiles of 256.
 //   * everything on 64-row tiles in one launch: 7 + 2.4 per unit and SM's two CTAs (3.4 where some are shared), or, with
 //     more items than those, 2.5 and 3.9 for each of them; a fifth more for many ranges.
-//     2 trees of 8 over 300 + 60 keys (12 heads over 2): 10.4 us, 16 on two kernels;
+//     2 trees of 8 over 300 + 60 keys (12 heads over 2): 6.7 us, 9.4 on two kernels;
 //   * everything on the tcgen05 kernel in one launch: 6.5 of start and end per item and 1 per
 //     tile (1.75 with more than 128 rows; 0.8 of that at 64 elements), in the ranges that end
 //     soonest, or the bytes at 6.3 TB/s. One tree of 25 over 50000 keys of 32 heads: 124 us,
-//     213 on 16-row tiles; 37 trees of up to 13 over 777 + 500 keys in pages of 24: 18, 22 on
+//     214 on 16-row tiles; 37 trees of up to 13 over 777 + 500 keys in pages of 24: 18, 21 on
 //     64-row tiles;
 //   * up to 16 rows of a sequence: own keys on 16-row tiles, at about 5.5 TB/s (up to
-//     32, at 2.7), and shared ones on the tcgen05 kernel beside them: 8 sequences x 32
-//     heads x 16 nodes over 500 + 300 keys 18.4 us, 22.7 on 64-row tiles.
+//     32, at 2.7 to 3.8, where two tiles read the same keys), and shared ones on the tcgen05
+//     kernel beside them: 8 sequences x 32 heads x 16 nodes over 500 + 300 keys 22.3 us, 24.4
+//     on 64-row tiles. (64 sequences x 8 heads x 24 rows over 2000 keys: 107 us on 16-row
+//     tiles, 89 on the tcgen05 kernel, which is taken.)
 // Over 192 shapes drawn at random the choice of the kernel costs 1% against the best
 // of them; with its ranges the plan's time is 2% below the best of the kernels with 1, 2, 4,
 // 8, 16, 48 and 128 ranges tried for each, and at worst 1.45 times it: 8 trees of nearly
@@ -822,7 +824,7 @@ TreePlan plan_tree(const nf4_prefix_attention_args& a, int64_t suffix_max, int64
   // Those are counted too, for a few items too many are a round more (6 sequences x 6 heads of 96 over 28842 keys: 4
   // ranges, 144 items, 95 us, 5 ranges 147): a third as if sequences were all as long as the longest, the rest with
   // lengths spread evenly from 60% of it up, where a range behind a sequence's end costs nothing (37 sequences over 500
-  // keys in ranges of 480: 17.3 us, in one range 20.4).
+  // keys in ranges of 480: 17.8 us, in one range 20.8).
   const double own_items = double(a.batch * tiles(each, 256)) * heads, shared_items = double(tiles(rows, 256)) * heads;
   const int64_t own_tiles = tiles(suffix_max, tile_keys), shared_tiles = tiles(a.prefix_len, tile_keys);
   const double narrow = a.head_dim <= 64 ? 0.8 : 1.0;

@@ -38,9 +38,10 @@
 // ones, with Q, S and O as above, K and V by a warp each (small boxes are bound by
 // their issue), and the ring one tile longer at 128 elements (the second tile of Q is
 // not there). The halves' maxima, sums and outputs are joined on the way out. 16 trees
-// of up to 32 nodes and 32 heads over 8 take 60 us over 4000 keys without, 44 with it
-// (1.05 us per key tile; two key tiles 13.2 and 12.1), one of 25 over 50000 keys of 32
-// heads 132 and 124.
+// of up to 32 nodes and 32 heads over 8 take 58 us over 4000 keys without, 44 with it
+// (1.05 us per key tile; two key tiles 12.5 and 11.9), one of 25 over 50000 keys of 32
+// heads 141 and 124. (tests/test_attention_barriers.py runs the barriers of this form as
+// a model under random interleavings; whoever changes an arrival here changes it there.)
 // An item leaves its partial result, or the output; an item of own keys of a call
 // with one range of each joins the shared keys' part of its rows on the way out.
 // Tensor memory: S (and P) of the tiles in columns 0 and 128, O in 256 and 384.
