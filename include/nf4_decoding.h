@@ -43,8 +43,8 @@ typedef struct nf4_kv_pages_args {
   const int32_t* free_count;  /* [1] */
   int64_t* slots;             /* [tokens]: flat slot of each token's key and value */
   int64_t* positions;         /* [tokens], or NULL */
-  int32_t* new_lens;          /* [batch]: lens with the new tokens; not lens itself */
-  int32_t* new_held;          /* [batch]; may be held */
+  int32_t* new_lens;          /* [batch]: lens with the new tokens; shares no entry with lens */
+  int32_t* new_held;          /* [batch]; may be held, else shares no entry with it */
   int32_t* new_free_count;    /* [1]; may be free_count */
   int64_t batch;              /* 0 .. 2^20 */
   int64_t tokens;             /* 0 .. 2^24 */
@@ -190,7 +190,8 @@ typedef struct nf4_tree_commit_args {
   int32_t* accepted;           /* [batch]: nodes of the accepted path */
   int32_t* path;               /* [batch][max_path]: the nodes, in order; -1 behind the last */
   int32_t* chosen;             /* [batch][max_path]: the model's choice after each of them; -1 behind the last */
-  int32_t* new_lens;           /* [batch]: own keys with the accepted nodes only; may be lens where there is no cache */
+  int32_t* new_lens;           /* [batch]: own keys with the accepted nodes only; may be lens where there is no cache,
+                                  else shares no entry with it */
   void* k_cache;               /* NULL: nothing is moved; else `layers` caches of 16-bit elements */
   int64_t k_layer_stride, k_page_stride, k_slot_stride, k_head_stride;
   void* v_cache;

@@ -181,6 +181,16 @@ def test_caches_whose_rows_are_at_two_indices_are_refused(lib):
             assert call(lib, "nf4_tree_commit", batch=0, **kw, **{one: 1}) == OK, kw
 
 
+def test_lengths_written_over_others_are_refused(lib):
+    """Lists that are read while they are written: the same one only where the call says so, others apart."""
+    for off in (0, 4, -4, 8, -8):  # three entries of four bytes
+        assert call(lib, "nf4_kv_pages", new_lens=A + off) == ERR_SIZE
+        assert call(lib, "nf4_tree_commit", new_lens=A + off) == ERR_SIZE
+        if off:
+            assert call(lib, "nf4_kv_pages", new_held=A + off) == ERR_SIZE
+            assert call(lib, "nf4_tree_commit", new_lens=A + off, k_cache=0, v_cache=0) == ERR_SIZE
+
+
 def test_calls_without_work(lib):
     assert call(lib, "nf4_kv_pages", batch=0, tokens=0) == OK
     assert call(lib, "nf4_tree_attention", tokens=0, tree_mask=0) == OK
@@ -223,3 +233,10 @@ def test_binding_refuses_before_it_looks_at_a_gpu(lib):
         nf4.nf4_tree_commit(i, i, i, None, i, 4)
     with pytest.raises(TypeError, match="tensor"):
         nf4.nf4_tree_attention(1, 2, 3, 4, 5, 6, 7, 8)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="these calls would launch")
+def test_lengths_in_place_and_side_by_side(lib):
+    for off in (0, 12, -12):
+        assert call(lib, "nf4_kv_pages", new_held=A + off) == ERR_CUDA
+        assert call(lib, "nf4_tree_commit", new_lens=A + off, k_cache=0, v_cache=0) == ERR_CUDA

@@ -34,6 +34,12 @@ bool apart_or_same(const void* in, int64_t in_stride, const void* out, int64_t o
   return off >= uintptr_t(width * size) && step - off >= uintptr_t(width * size);
 }
 
+// Two lists of `count` int32 share an entry.
+bool meet(const int32_t* a, const int32_t* b, int64_t count) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return (x > y ? x - y : y - x) < uintptr_t(count * 4);
+}
+
 cudaStream_t on(nf4_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 nf4_status check_tree(const nf4_tree_attention_args& a) {
@@ -61,7 +67,8 @@ nf4_status nf4_kv_pages(const nf4_kv_pages_args* args, nf4_stream_t stream) {
                 a.new_free_count) ||
       !aligned(a.slots, 8) || !aligned(a.positions, 8))
     return NF4_ERR_MISALIGNED;
-  if (a.batch > 0 && a.new_lens == a.lens) return NF4_ERR_INVALID_SIZE;  // tokens read lens while it is written
+  // Tokens read lens while new_lens is written; a request's held is read before its own new_held is.
+  if (meet(a.new_lens, a.lens, a.batch) || (a.new_held != a.held && meet(a.new_held, a.held, a.batch))) return NF4_ERR_INVALID_SIZE;
   return nf4::status_of(nf4::launch_kv_pages(a, on(stream)));
 }
 
@@ -144,7 +151,8 @@ nf4_status nf4_tree_commit(const nf4_tree_commit_args* args, nf4_stream_t stream
   if (!aligned4(a.parents, a.draft_tokens, a.targets, a.cu_q, a.lens, a.accepted, a.path, a.chosen, a.new_lens, a.page_table) ||
       !aligned(a.k_cache, 2) || !aligned(a.v_cache, 2))
     return NF4_ERR_MISALIGNED;
-  if (moves && a.new_lens == a.lens) return NF4_ERR_INVALID_SIZE;  // other blocks read lens while it is written
+  // Other blocks of a sequence, and of other ones, read lens while new_lens is written.
+  if ((moves || a.new_lens != a.lens) && meet(a.new_lens, a.lens, a.batch)) return NF4_ERR_INVALID_SIZE;
   nf4_tree_commit_args c = a;
   if (!moves) c.layers = 0;  // (with no page, or a table of no columns, every row that would move is reported)
   return nf4::status_of(nf4::launch_tree_commit(c, on(stream)));
