@@ -476,3 +476,14 @@ def test_offsets_past_32_bits():
         assert int(best[r]) == int((x[r] == x[r].max()).nonzero()[0])
     c.check((out[-last:], best[-last:]), close=False)
     assert lib().nf4_device_error_flags() == 0
+
+
+def test_calls_on_several_streams():
+    """Calls that run beside one another on the same inputs."""
+    c = Case([20, 70, 1], 50003, "bf16", seed=2, history=3000)
+    want = c.run()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got = [c.run(stream=streams[i % 4]) for i in range(24)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[0]) and torch.equal(b, want[1]) for o, b in got)

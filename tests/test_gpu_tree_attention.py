@@ -426,6 +426,31 @@ def test_pages_past_32_bits(prefix, counts, lens):
     c.check(got)
 
 
+@pytest.mark.parametrize("prefix", [0, 300, 8000])
+def test_no_sequences_and_tables_of_no_columns(prefix):
+    c = Call(12, 2, 128, prefix, [0, 0], [5, 3], seed=8, width=0)
+    c.check(c.run())
+    d = Call(12, 2, 128, prefix, [], [], seed=8, behind=9)
+    out, lse = d.run()
+    if prefix == 0:
+        assert not out.any() and (lse == float("-inf")).all()
+    d.counts, d.lens, d.seen = [9], [0], [set()] * 9
+    d.suffix_pages = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    d.check((out, lse))
+
+
+def test_the_last_word_of_the_widest_mask():
+    """65536 nodes have a bit, the 70 behind them none: every row sees the last node that has one, row 5 the first too."""
+    n = 65536 + 70
+    c = Call(1, 1, 8, 0, [n], [n], seed=1, seen=[set()] * n, mask_words=1, page=64)
+    mask = torch.zeros(n, 1024, dtype=torch.int64, device="cuda")
+    mask[:, 1023], mask[5, 0] = -(1 << 63), 1
+    out, lse = c.run(mask=mask)
+    last = c.v[c.suffix_pages[0, 65535 // 64].long(), 65535 % 64, 0]
+    same = (out[:, 0] == last).all(1)
+    assert same[:5].all() and same[6:].all() and not same[5] and lib().nf4_device_error_flags() == 0
+
+
 def test_two_streams_and_workspaces():
     c = Call(12, 2, 128, 2000, [300, 200], [9, 12], seed=5)
     want = c.run()
